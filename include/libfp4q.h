@@ -28,7 +28,8 @@
  * Dtype codes: FP4Q_F32 = IEEE binary32, FP4Q_BF16 = bfloat16.
  * All pointers must be 16-byte aligned and every row stride (in bytes) a
  * multiple of 16, or the call returns FP4Q_ERR_ALIGNMENT; the one exception
- * is fp4q_gemm's C, which only needs its element alignment (any ld_c >= N).
+ * is fp4q_gemm's C, which only needs its element alignment (any ld_c >= N),
+ * besides what the gated, norm and AdamW calls state for themselves.
  */
 #ifndef LIBFP4Q_H
 #define LIBFP4Q_H
@@ -498,6 +499,141 @@ size_t fp4q_hot_channels_workspace_bytes(int64_t rows, int64_t cols);
 fp4q_status_t fp4q_hot_channels(const void* x, int64_t rows, int64_t cols, int64_t ld_x,
                                 int32_t n_hot, int32_t* hot_idx, float* err, void* workspace,
                                 size_t workspace_bytes, void* stream);
+
+/*
+ * fp4q_gemm_gated -- the two projections of a gated feed-forward block, the
+ * activation and the product in one FP4 GEMM:
+ *   G = deq(X) deq(Wg)^T,  U = deq(X) deq(Wu)^T,  H = act(G) * U
+ *   act(g) = g / (1 + exp(-z)), z = g                                 FP4Q_SILU
+ *                               z = 2 sqrt(2/pi) (g + 0.044715 g^3)   FP4Q_GELU (tanh form)
+ *   X: x_codes [M, K/2], x_scales [M, K/32]; Wg, Wu: codes [F, K/2], scales
+ *   [F, K/32] each (K-major, block 32, as fp4q_quantize writes them); the two
+ *   may be the row halves of one packed [2F, K/2] array.
+ *   h: bf16 [M, F], row stride ld_h >= F.  gate, up: bf16 [M, F], row stride
+ *   ld_gu >= F, written with G and U for fp4q_gemm_gated_grad; both NULL
+ *   where no gradient follows.  H is formed from the fp32 products, each
+ *   output rounded once, to nearest even.  With gate and up the halves of one
+ *   [M, 2F] buffer, ld_gu = 2F.
+ *   K % 64 == 0, K < 2^24; M, F >= 1 arbitrary.  Code pointers and x_scales
+ *   16-byte aligned; the weights' scales 4-byte aligned (2-byte where
+ *   K % 128 == 64), so that halves of a packed array qualify for every F;
+ *   h, gate, up element-aligned (16-byte rows are written faster).
+ *   Deterministic: no atomics; an output's sum over K does not depend on F or
+ *   on the other rows.  A 0xFF scale byte gives NaN in the outputs it feeds.
+ */
+typedef enum { FP4Q_SILU = 0, FP4Q_GELU = 1 } fp4q_act_t;
+fp4q_status_t fp4q_gemm_gated(int64_t M, int64_t F, int64_t K, const uint8_t* x_codes,
+                              const uint8_t* x_scales, const uint8_t* gate_codes,
+                              const uint8_t* gate_scales, const uint8_t* up_codes,
+                              const uint8_t* up_scales, fp4q_act_t act, void* h, int64_t ld_h,
+                              void* gate, void* up, int64_t ld_gu, void* stream);
+
+/*
+ * fp4q_gemm_gated_grad -- the gradients of G and U behind the down projection,
+ * in the epilogue of the GEMM that brings the gradient back through it:
+ *   D = deq(dY) deq(W)^T,  dU = D * act(G),  dG = D * U * act'(G)
+ *   dY: dy_codes [M, K/2], dy_scales [M, K/32]; W (the down projection):
+ *   w_codes [F, K/2], w_scales [F, K/32]; K is the block's outer width.
+ *   gate, up: bf16 [M, F], row stride ld_gu, as fp4q_gemm_gated wrote them;
+ *   d_gate, d_up: bf16 [M, F], row stride ld_d, written (not overlapping gate
+ *   or up).  With d_gate and d_up the halves of one [M, 2F] buffer (ld_d = 2F)
+ *   a quantisation of that buffer is the operand of the input gradient,
+ *   fp4q_gemm over K = 2F, and of the weight gradients.
+ *   D is not rounded before the products.  Sizes and alignment as
+ *   fp4q_gemm_gated (w_scales 16-byte aligned).
+ */
+fp4q_status_t fp4q_gemm_gated_grad(int64_t M, int64_t F, int64_t K, const uint8_t* dy_codes,
+                                   const uint8_t* dy_scales, const uint8_t* w_codes,
+                                   const uint8_t* w_scales, fp4q_act_t act, const void* gate,
+                                   const void* up, int64_t ld_gu, void* d_gate, void* d_up,
+                                   int64_t ld_d, void* stream);
+
+/*
+ * fp4q_layer_norm -- normalisation of the rows of x:
+ *   y = (x - mean) * rstd * weight + bias,
+ *   mean = sum(x) / cols, or 0 with FP4Q_RMS_NORM,
+ *   rstd = 1 / sqrt(sum((x - mean)^2) / cols + eps)
+ *   x: bf16 or fp32 [rows, cols], row stride ld_x >= cols; y: bf16 or fp32
+ *   (either with either x), row stride ld_y >= cols; weight, bias: [cols] of
+ *   w_dtype, NULL for ones and zeros; mean, rstd: fp32 [rows], written for
+ *   the gradient, NULL to skip (mean is not written with FP4Q_RMS_NORM).
+ *   The squares are summed around the mean, in fp32.  eps >= 0.  Any cols;
+ *   every pointer needs only its element's alignment (16-byte rows run
+ *   faster).  A row holding Inf or NaN gives NaN in that row alone.
+ */
+typedef enum { FP4Q_LAYER_NORM = 0, FP4Q_RMS_NORM = 1 } fp4q_norm_t;
+fp4q_status_t fp4q_layer_norm(fp4q_norm_t kind, const void* x, fp4q_dtype_t x_dtype, int64_t rows,
+                              int64_t cols, int64_t ld_x, const void* weight, const void* bias,
+                              fp4q_dtype_t w_dtype, double eps, void* y, fp4q_dtype_t y_dtype,
+                              int64_t ld_y, float* mean, float* rstd, void* stream);
+
+/*
+ * fp4q_layer_norm_grad -- its backward pass, with xh = (x - mean) rstd and
+ * t = dy * weight:
+ *   dx = rstd (t - mean_c(t) - xh mean_c(t xh))   (FP4Q_RMS_NORM: no mean_c(t))
+ *   dweight = sum over rows of dy xh,  dbias = sum over rows of dy
+ *   dy: bf16 or fp32 [rows, cols], row stride ld_dy; x as in the forward call;
+ *   dx: of x_dtype, row stride ld_dx (may be dy's or x's memory, element for
+ *   element, where the types agree); mean (NULL with FP4Q_RMS_NORM) and rstd
+ *   as the forward call wrote them.  dweight, dbias: fp32 [cols], written (not
+ *   added to); NULL to skip either.
+ *   workspace >= fp4q_layer_norm_grad_workspace_bytes(rows, cols) device
+ *   bytes, 16-byte aligned, not needed where dweight and dbias are NULL.
+ *   Sums in fp32 in an order that depends on the sizes alone.
+ */
+size_t fp4q_layer_norm_grad_workspace_bytes(int64_t rows, int64_t cols);
+fp4q_status_t fp4q_layer_norm_grad(fp4q_norm_t kind, const void* dy, fp4q_dtype_t dy_dtype,
+                                   int64_t ld_dy, const void* x, fp4q_dtype_t x_dtype,
+                                   int64_t rows, int64_t cols, int64_t ld_x, const void* weight,
+                                   fp4q_dtype_t w_dtype, const float* mean, const float* rstd,
+                                   void* dx, int64_t ld_dx, float* dweight, float* dbias,
+                                   void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * fp4q_adamw_step -- one AdamW step over many tensors:
+ *   g = grad * (*grad_scale)           (grad_scale: device fp32, NULL for 1)
+ *   m = beta1 m + (1 - beta1) g,       v = beta2 v + (1 - beta2) g^2
+ *   param = param (1 - lr weight_decay)
+ *           - lr (m / (1 - beta1^step)) / (sqrt(v / (1 - beta2^step)) + eps)
+ *   tensors: HOST array of n descriptors, read during the call only; each
+ *   tensor is `numel` consecutive elements, its pointers 16-byte aligned
+ *   (scales: element-aligned); numel = 0 is skipped.  The tensors of one call
+ *   must not overlap.
+ *     param   fp32, updated;  copy: bf16 rounding of the new param (what the
+ *             quantiser reads next), NULL to skip
+ *     grad    fp32 or bf16 (grad_dtype, one for the call)
+ *     state_bits 32: exp_avg (m) and exp_avg_sq (v) fp32, updated; the scale
+ *             pointers are ignored
+ *     state_bits 8: exp_avg holds m and exp_avg_sq holds sqrt(v) as E4M3
+ *             codes, one byte per element, each with ceil(numel / 32) E8M0
+ *             scale bytes (exp_avg_scales, exp_avg_sq_scales): 2^(byte-127) =
+ *             2^(floor(log2 amax) - 7) of its 32 elements.  All-zero codes
+ *             and scales are the initial state.  Rounding is stochastic:
+ *             Philox4x32-10, key `seed`, counter (position / 4, step), 32-bit
+ *             word position % 4, low half for m and high half for sqrt(v); an
+ *             element's position is its index plus the sizes of the call's
+ *             earlier tensors, each rounded up to 32.  A block with an Inf or
+ *             NaN gets scale 0xFF (NaN) and zero codes.
+ *   step >= 1 counts from 1.  lr, weight_decay, eps >= 0, 0 <= beta < 1.
+ *   All arithmetic on elements in fp32.  No workspace; the descriptors travel
+ *   as kernel arguments (44 tensors to a launch), so a call can be captured
+ *   into a graph, which then replays its step and lr.
+ */
+typedef struct fp4q_adamw_tensor {
+    float* param;
+    const void* grad;
+    void* exp_avg;
+    void* exp_avg_sq;
+    uint8_t* exp_avg_scales;
+    uint8_t* exp_avg_sq_scales;
+    uint16_t* copy;
+    int64_t numel;
+    double weight_decay;
+} fp4q_adamw_tensor_t;
+fp4q_status_t fp4q_adamw_step(const fp4q_adamw_tensor_t* tensors, int32_t n, int32_t state_bits,
+                              fp4q_dtype_t grad_dtype, double lr, double beta1, double beta2,
+                              double eps, int64_t step, uint64_t seed, const float* grad_scale,
+                              void* stream);
 
 /*
  * fp4q_set_next_launch -- options for the next kernel that this thread

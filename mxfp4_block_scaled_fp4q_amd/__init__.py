@@ -16,6 +16,8 @@ F32, BF16 = 0, 1
 ROW, COL = 0, 1
 RNE, SR = 0, 1
 STE, DGE = 0, 1
+SILU, GELU = 0, 1
+LAYER_NORM, RMS_NORM = 0, 1
 
 STATUS = {0: "FP4Q_OK", 1: "FP4Q_ERR_INVALID", 2: "FP4Q_ERR_UNSUPPORTED",
           3: "FP4Q_ERR_ALIGNMENT", 4: "FP4Q_ERR_WORKSPACE", 5: "FP4Q_ERR_HIP"}
@@ -28,6 +30,8 @@ EXPORTS = ["fp4q_channel_mask", "fp4q_quantize_masked", "fp4q_gemm_hcp_split",
            "fp4q_gemm_hcp", "fp4q_hot_channels_workspace_bytes", "fp4q_hot_channels",
            "fp4q_quantize_2d", "fp4q_quantize_2d_tile", "fp4q_quantize_rht", "fp4q_occ_max_nnz",
            "fp4q_occ_workspace_bytes", "fp4q_occ_quantize", "fp4q_occ_spmm",
+           "fp4q_gemm_gated", "fp4q_gemm_gated_grad", "fp4q_layer_norm",
+           "fp4q_layer_norm_grad_workspace_bytes", "fp4q_layer_norm_grad", "fp4q_adamw_step",
            "fp4q_set_next_launch", "fp4q_status_string",
            "fp4q_last_error", "fp4q_abi_version"]
 
@@ -36,6 +40,14 @@ class Fp4qError(RuntimeError):
     def __init__(self, status, detail):
         super().__init__(f"{STATUS.get(status, status)}: {detail}")
         self.status = status
+
+
+class AdamwTensor(_ct.Structure):
+    """One tensor of an AdamW step (fp4q_adamw_tensor_t)."""
+    _fields_ = [("param", _ct.c_void_p), ("grad", _ct.c_void_p), ("exp_avg", _ct.c_void_p),
+                ("exp_avg_sq", _ct.c_void_p), ("exp_avg_scales", _ct.c_void_p),
+                ("exp_avg_sq_scales", _ct.c_void_p), ("copy", _ct.c_void_p),
+                ("numel", _ct.c_int64), ("weight_decay", _ct.c_double)]
 
 
 _lib = None
@@ -49,8 +61,8 @@ def lib():
             raise ImportError(f"{LIB_PATH} is not built; run "
                               "mxfp4_block_scaled_fp4q_amd/build.py (or __graft_entry__.build())")
         L = _ct.CDLL(LIB_PATH)
-        P, I64, I32, U64, F, SZ = (_ct.c_void_p, _ct.c_int64, _ct.c_int32, _ct.c_uint64,
-                                   _ct.c_float, _ct.c_size_t)
+        P, I64, I32, U64, F, SZ, D = (_ct.c_void_p, _ct.c_int64, _ct.c_int32, _ct.c_uint64,
+                                      _ct.c_float, _ct.c_size_t, _ct.c_double)
         sig = {
             "fp4q_quantize": (I32, [P, I32, I64, I64, I64, I32, I32, I32, U64, U64, P, P, P]),
             "fp4q_quantize_dual": (I32, [P, I32, I64, I64, I64, I32, I32, U64, I32, U64, U64, P, P,
@@ -82,6 +94,16 @@ def lib():
                                         P, I64, P, P, SZ, P]),
             "fp4q_occ_spmm": (I32, [I64, I64, I64, P, P, P, P, I64, P, I64, P]),
             "fp4q_hot_channels": (I32, [P, I64, I64, I64, I32, P, P, P, SZ, P]),
+            "fp4q_gemm_gated": (I32, [I64, I64, I64, P, P, P, P, P, P, I32, P, I64, P, P, I64,
+                                      P]),
+            "fp4q_gemm_gated_grad": (I32, [I64, I64, I64, P, P, P, P, I32, P, P, I64, P, P, I64,
+                                           P]),
+            "fp4q_layer_norm": (I32, [I32, P, I32, I64, I64, I64, P, P, I32, D, P, I32, I64, P, P,
+                                      P]),
+            "fp4q_layer_norm_grad_workspace_bytes": (SZ, [I64, I64]),
+            "fp4q_layer_norm_grad": (I32, [I32, P, I32, I64, P, I32, I64, I64, I64, P, I32, P, P,
+                                           P, I64, P, P, P, SZ, P]),
+            "fp4q_adamw_step": (I32, [P, I32, I32, I32, D, D, D, D, I64, U64, P, P]),
             "fp4q_set_next_launch": (I32, [P, P, _ct.c_uint32]),
             "fp4q_status_string": (_ct.c_char_p, [I32]),
             "fp4q_last_error": (_ct.c_char_p, []),
@@ -549,3 +571,244 @@ def occ_spmm(row_ptr, col_idx, vals, w, y, stream=None):
     _check(lib().fp4q_occ_spmm(M, N, K, _ptr(row_ptr), _ptr(col_idx), _ptr(vals), _ptr(w),
                                w.stride(0), _ptr(y), y.stride(0), _stream(stream)))
     return y
+
+
+def _rows(t, name, dtype=None, shape=None):
+    """Row stride of a 2-D device tensor with unit column stride (the stride
+    of a single row, or of columns one element wide, is free)."""
+    _need_cuda(t)
+    if dtype is not None:
+        _need(t, name, dtype, shape, dense=False)
+    elif shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] != 1):
+        raise ValueError(f"{name} must be 2-D with unit column stride")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _codes(codes, scales, name, rows=None, K=None):
+    """Checks one K-major block-32 operand; returns its rows and K."""
+    torch = _torch()
+    _need_cuda(codes, scales)
+    if codes.dim() != 2:
+        raise ValueError(f"{name}_codes must be 2-D")
+    rows = codes.shape[0] if rows is None else rows
+    K = 2 * codes.shape[1] if K is None else K
+    _need(codes, f"{name}_codes", torch.uint8, (rows, K // 2))
+    _need(scales, f"{name}_scales", torch.uint8, (rows, K // 32))
+    return rows, K
+
+
+def gemm_gated(x_codes, x_scales, gate_codes, gate_scales, up_codes, up_scales, act=SILU,
+               save=False, h=None, gate=None, up=None, stream=None):
+    """act(X Wg^T) * (X Wu^T) of quantised operands in one kernel
+    (fp4q_gemm_gated): x_codes [M, K/2], the weights' codes [F, K/2] (rows of
+    one packed array will do).  Returns h (bf16 [M, F]), or (h, gate, up)
+    where save is set or gate and up are given; with save alone they are the
+    halves of one [M, 2F] tensor."""
+    torch = _torch()
+    M, K = _codes(x_codes, x_scales, "x")
+    F, _ = _codes(gate_codes, gate_scales, "gate", K=K)
+    _codes(up_codes, up_scales, "up", F, K)
+    if h is None:
+        h = torch.empty((M, F), dtype=torch.bfloat16, device=x_codes.device)
+    ldh = _rows(h, "h", torch.bfloat16, (M, F))
+    if (gate is None) != (up is None):
+        raise ValueError("gate and up are given both or neither")
+    if gate is None and save:
+        both = torch.empty((M, 2 * F), dtype=torch.bfloat16, device=x_codes.device)
+        gate, up = both[:, :F], both[:, F:]
+    ldgu = 0
+    if gate is not None:
+        ldgu = _rows(gate, "gate", torch.bfloat16, (M, F))
+        if _rows(up, "up", torch.bfloat16, (M, F)) != ldgu:
+            raise ValueError("gate and up must have the same row stride")
+    _check(lib().fp4q_gemm_gated(M, F, K, _ptr(x_codes), _ptr(x_scales), _ptr(gate_codes),
+                                 _ptr(gate_scales), _ptr(up_codes), _ptr(up_scales), act, _ptr(h),
+                                 ldh, _ptr(gate), _ptr(up), ldgu, _stream(stream)))
+    return h if gate is None else (h, gate, up)
+
+
+def gemm_gated_grad(dy_codes, dy_scales, w_codes, w_scales, gate, up, act=SILU, d_gate=None,
+                    d_up=None, stream=None):
+    """Gradients of the gated block's two products behind its down projection
+    (fp4q_gemm_gated_grad): dy_codes [M, K/2], w_codes [F, K/2], gate and up
+    bf16 [M, F] as gemm_gated returned them.  Returns (d_gate, d_up), bf16,
+    the halves of one [M, 2F] tensor unless given."""
+    torch = _torch()
+    M, K = _codes(dy_codes, dy_scales, "dy")
+    F, _ = _codes(w_codes, w_scales, "w", K=K)
+    ldgu = _rows(gate, "gate", torch.bfloat16, (M, F))
+    if _rows(up, "up", torch.bfloat16, (M, F)) != ldgu:
+        raise ValueError("gate and up must have the same row stride")
+    if (d_gate is None) != (d_up is None):
+        raise ValueError("d_gate and d_up are given both or neither")
+    if d_gate is None:
+        both = torch.empty((M, 2 * F), dtype=torch.bfloat16, device=dy_codes.device)
+        d_gate, d_up = both[:, :F], both[:, F:]
+    ldd = _rows(d_gate, "d_gate", torch.bfloat16, (M, F))
+    if _rows(d_up, "d_up", torch.bfloat16, (M, F)) != ldd:
+        raise ValueError("d_gate and d_up must have the same row stride")
+    _check(lib().fp4q_gemm_gated_grad(M, F, K, _ptr(dy_codes), _ptr(dy_scales), _ptr(w_codes),
+                                      _ptr(w_scales), act, _ptr(gate), _ptr(up), ldgu,
+                                      _ptr(d_gate), _ptr(d_up), ldd, _stream(stream)))
+    return d_gate, d_up
+
+
+def _affine(weight, bias, cols):
+    """Dtype code of the norm's weight and bias vectors."""
+    for t, name in ((weight, "weight"), (bias, "bias")):
+        if t is not None:
+            _need_cuda(t)
+            _need(t, name, t.dtype, (cols,))
+    if weight is not None and bias is not None and weight.dtype != bias.dtype:
+        raise TypeError("weight and bias must have the same dtype")
+    t = weight if weight is not None else bias
+    return F32 if t is None else _dt(t)
+
+
+def layer_norm(x, weight=None, bias=None, eps=1e-5, kind=LAYER_NORM, y=None, out_dtype=None,
+               stats=True, mean=None, rstd=None, stream=None):
+    """Layer norm (or RMS norm) of the rows of x (fp4q_layer_norm).  Returns
+    (y, mean, rstd): y of out_dtype (x's by default), mean and rstd fp32 per
+    row for layer_norm_grad (mean None for RMS_NORM, both None without
+    stats)."""
+    torch = _torch()
+    ldx = _rows(x, "x")
+    R, C = x.shape
+    wdt = _affine(weight, bias, C)
+    if y is None:
+        y = torch.empty((R, C), dtype=x.dtype if out_dtype is None else out_dtype, device=x.device)
+    ldy = _rows(y, "y", shape=(R, C))
+    if stats:
+        if mean is None and kind == LAYER_NORM:
+            mean = torch.empty((R,), dtype=torch.float32, device=x.device)
+        if rstd is None:
+            rstd = torch.empty((R,), dtype=torch.float32, device=x.device)
+    for t, name in ((mean, "mean"), (rstd, "rstd")):
+        if t is not None:
+            _need_cuda(t)
+            _need(t, name, torch.float32, (R,))
+    _check(lib().fp4q_layer_norm(kind, _ptr(x), _dt(x), R, C, ldx, _ptr(weight), _ptr(bias), wdt,
+                                 eps, _ptr(y), _dt(y), ldy, _ptr(mean), _ptr(rstd),
+                                 _stream(stream)))
+    return y, mean, rstd
+
+
+def layer_norm_grad_workspace_bytes(rows, cols):
+    return int(lib().fp4q_layer_norm_grad_workspace_bytes(rows, cols))
+
+
+def layer_norm_grad(dy, x, weight, mean, rstd, kind=LAYER_NORM, dx=None, want_weight=True,
+                    want_bias=True, dweight=None, dbias=None, workspace=None, stream=None):
+    """Backward pass of layer_norm (fp4q_layer_norm_grad).  Returns (dx,
+    dweight, dbias): dx of x's dtype, the others fp32 (None where not
+    wanted)."""
+    torch = _torch()
+    ldx = _rows(x, "x")
+    R, C = x.shape
+    lddy = _rows(dy, "dy", shape=(R, C))
+    wdt = _affine(weight, None, C)
+    if dx is None:
+        dx = torch.empty((R, C), dtype=x.dtype, device=x.device)
+    lddx = _rows(dx, "dx", x.dtype, (R, C))
+    if dweight is None and want_weight:
+        dweight = torch.empty((C,), dtype=torch.float32, device=x.device)
+    if dbias is None and want_bias:
+        dbias = torch.empty((C,), dtype=torch.float32, device=x.device)
+    for t, name, n in ((mean, "mean", R), (rstd, "rstd", R), (dweight, "dweight", C),
+                       (dbias, "dbias", C)):
+        if t is not None:
+            _need_cuda(t)
+            _need(t, name, torch.float32, (n,))
+    nbytes = 0
+    if dweight is not None or dbias is not None:
+        if workspace is None:
+            workspace = _scratch(layer_norm_grad_workspace_bytes(R, C), x.device, stream)
+        nbytes = workspace.numel() * workspace.element_size()
+    _check(lib().fp4q_layer_norm_grad(kind, _ptr(dy), _dt(dy), lddy, _ptr(x), _dt(x), R, C, ldx,
+                                      _ptr(weight), wdt, _ptr(mean), _ptr(rstd), _ptr(dx), lddx,
+                                      _ptr(dweight), _ptr(dbias), _ptr(workspace), nbytes,
+                                      _stream(stream)))
+    return dx, dweight, dbias
+
+
+class AdamwPlan:
+    """The tensors of an AdamW step, checked once (see adamw_plan).  Holds
+    references to them."""
+
+    def __init__(self, array, bits, grad_dtype, tensors):
+        self.array, self.bits, self.grad_dtype, self.tensors = array, bits, grad_dtype, tensors
+
+
+def adamw_state(param, bits=32):
+    """Zero moments for one parameter: (exp_avg, exp_avg_sq, exp_avg_scales,
+    exp_avg_sq_scales); the scales are None for bits=32."""
+    torch = _torch()
+    n = param.numel()
+    if bits == 32:
+        return (torch.zeros(n, dtype=torch.float32, device=param.device),
+                torch.zeros(n, dtype=torch.float32, device=param.device), None, None)
+    if bits != 8:
+        raise ValueError("bits must be 8 or 32")
+    return tuple(torch.zeros(k, dtype=torch.uint8, device=param.device)
+                 for k in (n, n, (n + 31) // 32, (n + 31) // 32))
+
+
+def adamw_plan(params, grads, exp_avg, exp_avg_sq, exp_avg_scales=None, exp_avg_sq_scales=None,
+               copies=None, weight_decay=0.0):
+    """Checks the tensors of an AdamW step and keeps their addresses for
+    adamw_step.  params: contiguous fp32 tensors; grads: fp32 or bf16, one
+    dtype; exp_avg, exp_avg_sq: fp32, or uint8 (E4M3 codes of m and of
+    sqrt(v)) with the uint8 scales, ceil(numel/32) per tensor; copies: bf16
+    tensors to receive the new params, or None; weight_decay: a number, or
+    one per tensor."""
+    torch = _torch()
+    n = len(params)
+    bits = 8 if exp_avg_scales is not None else 32
+    if (exp_avg_scales is None) != (exp_avg_sq_scales is None):
+        raise ValueError("exp_avg_scales and exp_avg_sq_scales are given both or neither")
+    state = torch.uint8 if bits == 8 else torch.float32
+    none = [None] * n
+    if not isinstance(weight_decay, (list, tuple)):
+        weight_decay = [weight_decay] * n
+    cols = dict(params=params, grads=grads, exp_avg=exp_avg, exp_avg_sq=exp_avg_sq,
+                exp_avg_scales=exp_avg_scales or none, exp_avg_sq_scales=exp_avg_sq_scales or none,
+                copies=copies or none, weight_decay=weight_decay)
+    for name, c in cols.items():
+        if len(c) != n:
+            raise ValueError(f"{name} must have one entry per tensor ({n}), got {len(c)}")
+    gdtype = grads[0].dtype if n else torch.float32
+    if gdtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"grads must be bf16 or fp32, got {gdtype}")
+    array = (AdamwTensor * max(n, 1))()
+    for i, (p, g, m, v, ms, vs, c, wd) in enumerate(zip(*cols.values())):
+        k = p.numel()
+        for t, name, dtype, size in ((p, "param", torch.float32, k), (g, "grad", gdtype, k),
+                                     (m, "exp_avg", state, k), (v, "exp_avg_sq", state, k),
+                                     (ms, "exp_avg_scales", torch.uint8, (k + 31) // 32),
+                                     (vs, "exp_avg_sq_scales", torch.uint8, (k + 31) // 32),
+                                     (c, "copy", torch.bfloat16, k)):
+            if t is None:
+                continue
+            _need_cuda(t)
+            _need(t, f"{name} {i}", dtype)
+            if t.numel() != size:
+                raise ValueError(f"{name} {i} must have {size} elements, got {t.numel()}")
+        array[i] = AdamwTensor(*(0 if t is None else t.data_ptr() for t in (p, g, m, v, ms, vs, c)),
+                               k, wd)
+    return AdamwPlan(array, bits, BF16 if gdtype == torch.bfloat16 else F32,
+                     (list(zip(*list(cols.values())[:-1])), n))
+
+
+def adamw_step(plan, lr, step, beta1=0.9, beta2=0.999, eps=1e-8, seed=0, grad_scale=None,
+               stream=None):
+    """One AdamW step over the plan's tensors, in place (fp4q_adamw_step).
+    step counts from 1; seed: the stochastic rounding of 8-bit moments;
+    grad_scale: a device fp32 scalar that multiplies the gradients."""
+    if grad_scale is not None:
+        _need_cuda(grad_scale)
+        _need(grad_scale, "grad_scale", _torch().float32)
+    _check(lib().fp4q_adamw_step(plan.array, plan.tensors[1], plan.bits, plan.grad_dtype, lr,
+                                 beta1, beta2, eps, step, seed, _ptr(grad_scale),
+                                 _stream(stream)))

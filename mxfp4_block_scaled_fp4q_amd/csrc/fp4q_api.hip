@@ -43,6 +43,29 @@ static_assert(fp4q::kHcpStaticScratchBytes == FP4Q_HCP_NOALLOC_MAX_BYTES,
 // chunks; element counts up to 2^33 are accepted.
 constexpr int64_t kMaxElems = (int64_t)1 << 33;
 
+// Sizes that the gated calls share (as fp4q_gemm's; the tiles of one launch
+// are counted in 31 bits).
+fp4q_status_t gated_sizes(const char* who, int64_t M, int64_t F, int64_t K) {
+    if (M <= 0 || F <= 0 || K <= 0) return fail(FP4Q_ERR_INVALID, "%s: bad sizes", who);
+    if (K % 64) return fail(FP4Q_ERR_INVALID, "%s: K %% 64 != 0", who);
+    if (M >= ((int64_t)1 << 30) || F >= ((int64_t)1 << 30))
+        return fail(FP4Q_ERR_INVALID, "%s: dimension too large", who);
+    if (K >= ((int64_t)1 << 24))
+        return fail(FP4Q_ERR_UNSUPPORTED, "%s: K must be below 2^24", who);
+    if (((M + 255) / 256) * ((F + 127) / 128) >= ((int64_t)1 << 31))
+        return fail(FP4Q_ERR_UNSUPPORTED, "%s: too many tiles", who);
+    return FP4Q_OK;
+}
+
+// Sizes that the norm calls share; `ld` is the smallest row stride.
+fp4q_status_t norm_sizes(const char* who, int64_t rows, int64_t cols, int64_t ld) {
+    if (rows <= 0 || cols <= 0) return fail(FP4Q_ERR_INVALID, "%s: bad sizes", who);
+    if (rows >= ((int64_t)1 << 31) || cols >= ((int64_t)1 << 31))
+        return fail(FP4Q_ERR_INVALID, "%s: dimension too large", who);
+    if (ld < cols) return fail(FP4Q_ERR_INVALID, "%s: row stride below cols", who);
+    return FP4Q_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -641,6 +664,160 @@ fp4q_status_t fp4q_occ_spmm(int64_t M, int64_t N, int64_t K, const int64_t* row_
     return hip_status(fp4q::launch_occ_spmm(M, N, row_ptr, col_idx, vals, w, ld_w, y, ld_y,
                                             (hipStream_t)stream),
                       "occ_spmm launch");
+}
+
+fp4q_status_t fp4q_gemm_gated(int64_t M, int64_t F, int64_t K, const uint8_t* x_codes,
+                              const uint8_t* x_scales, const uint8_t* gate_codes,
+                              const uint8_t* gate_scales, const uint8_t* up_codes,
+                              const uint8_t* up_scales, fp4q_act_t act, void* h, int64_t ld_h,
+                              void* gate, void* up, int64_t ld_gu, void* stream) {
+    if (!x_codes || !x_scales || !gate_codes || !gate_scales || !up_codes || !up_scales || !h)
+        return fail(FP4Q_ERR_INVALID, "gemm_gated: null pointer");
+    if (!gate != !up)
+        return fail(FP4Q_ERR_INVALID, "gemm_gated: gate and up are given both or neither");
+    if (act != FP4Q_SILU && act != FP4Q_GELU)
+        return fail(FP4Q_ERR_INVALID, "gemm_gated: bad act %d", (int)act);
+    const fp4q_status_t e = gated_sizes("gemm_gated", M, F, K);
+    if (e != FP4Q_OK) return e;
+    if (ld_h < F || (gate && ld_gu < F))
+        return fail(FP4Q_ERR_INVALID, "gemm_gated: row stride below F");
+    const uintptr_t scale_align = K % 128 ? 2 : 4;
+    if (!aligned16(x_codes) || !aligned16(x_scales) || !aligned16(gate_codes) ||
+        !aligned16(up_codes) || ((uintptr_t)gate_scales % scale_align) ||
+        ((uintptr_t)up_scales % scale_align) || ((uintptr_t)h % 2) || ((uintptr_t)gate % 2) ||
+        ((uintptr_t)up % 2))
+        return fail(FP4Q_ERR_ALIGNMENT,
+                    "gemm_gated: codes and x_scales must be 16-byte aligned, the weights' scales "
+                    "%d-byte aligned, outputs element-aligned", (int)scale_align);
+    return hip_status(fp4q::launch_gemm_gated(M, F, K, x_codes, x_scales, gate_codes, gate_scales,
+                                              up_codes, up_scales, (int)act, (uint16_t*)h, ld_h,
+                                              (uint16_t*)gate, (uint16_t*)up, ld_gu,
+                                              (hipStream_t)stream),
+                      "gemm_gated launch");
+}
+
+fp4q_status_t fp4q_gemm_gated_grad(int64_t M, int64_t F, int64_t K, const uint8_t* dy_codes,
+                                   const uint8_t* dy_scales, const uint8_t* w_codes,
+                                   const uint8_t* w_scales, fp4q_act_t act, const void* gate,
+                                   const void* up, int64_t ld_gu, void* d_gate, void* d_up,
+                                   int64_t ld_d, void* stream) {
+    if (!dy_codes || !dy_scales || !w_codes || !w_scales || !gate || !up || !d_gate || !d_up)
+        return fail(FP4Q_ERR_INVALID, "gemm_gated_grad: null pointer");
+    if (act != FP4Q_SILU && act != FP4Q_GELU)
+        return fail(FP4Q_ERR_INVALID, "gemm_gated_grad: bad act %d", (int)act);
+    const fp4q_status_t e = gated_sizes("gemm_gated_grad", M, F, K);
+    if (e != FP4Q_OK) return e;
+    if (ld_gu < F || ld_d < F)
+        return fail(FP4Q_ERR_INVALID, "gemm_gated_grad: row stride below F");
+    if (!aligned16(dy_codes) || !aligned16(dy_scales) || !aligned16(w_codes) ||
+        !aligned16(w_scales) || ((uintptr_t)gate % 2) || ((uintptr_t)up % 2) ||
+        ((uintptr_t)d_gate % 2) || ((uintptr_t)d_up % 2))
+        return fail(FP4Q_ERR_ALIGNMENT,
+                    "gemm_gated_grad: operand pointers must be 16-byte aligned, the others "
+                    "element-aligned");
+    return hip_status(fp4q::launch_gemm_gated_grad(
+                          M, F, K, dy_codes, dy_scales, w_codes, w_scales, (int)act,
+                          (const uint16_t*)gate, (const uint16_t*)up, ld_gu, (uint16_t*)d_gate,
+                          (uint16_t*)d_up, ld_d, (hipStream_t)stream),
+                      "gemm_gated_grad launch");
+}
+
+fp4q_status_t fp4q_layer_norm(fp4q_norm_t kind, const void* x, fp4q_dtype_t x_dtype, int64_t rows,
+                              int64_t cols, int64_t ld_x, const void* weight, const void* bias,
+                              fp4q_dtype_t w_dtype, double eps, void* y, fp4q_dtype_t y_dtype,
+                              int64_t ld_y, float* mean, float* rstd, void* stream) {
+    if (kind != FP4Q_LAYER_NORM && kind != FP4Q_RMS_NORM)
+        return fail(FP4Q_ERR_INVALID, "layer_norm: bad kind %d", (int)kind);
+    if (!x || !y) return fail(FP4Q_ERR_INVALID, "layer_norm: null pointer");
+    if (!valid_dtype(x_dtype) || !valid_dtype(y_dtype) || !valid_dtype(w_dtype))
+        return fail(FP4Q_ERR_INVALID, "layer_norm: bad dtype");
+    const fp4q_status_t e = norm_sizes("layer_norm", rows, cols, ld_x < ld_y ? ld_x : ld_y);
+    if (e != FP4Q_OK) return e;
+    if (!(eps >= 0.0) || !(eps < 1e30)) return fail(FP4Q_ERR_INVALID, "layer_norm: bad eps");
+    if (((uintptr_t)x % esize(x_dtype)) || ((uintptr_t)y % esize(y_dtype)) ||
+        ((uintptr_t)weight % esize(w_dtype)) || ((uintptr_t)bias % esize(w_dtype)) ||
+        ((uintptr_t)mean % 4) || ((uintptr_t)rstd % 4))
+        return fail(FP4Q_ERR_ALIGNMENT, "layer_norm: pointers must be element-aligned");
+    return hip_status(fp4q::launch_norm(x, x_dtype, rows, cols, ld_x, weight, bias, w_dtype,
+                                        (float)eps, kind == FP4Q_RMS_NORM, y, y_dtype, ld_y, mean,
+                                        rstd, (hipStream_t)stream),
+                      "layer_norm launch");
+}
+
+size_t fp4q_layer_norm_grad_workspace_bytes(int64_t rows, int64_t cols) {
+    if (rows <= 0 || cols <= 0) return 0;
+    return fp4q::norm_grad_workspace_bytes(rows, cols);
+}
+
+fp4q_status_t fp4q_layer_norm_grad(fp4q_norm_t kind, const void* dy, fp4q_dtype_t dy_dtype,
+                                   int64_t ld_dy, const void* x, fp4q_dtype_t x_dtype,
+                                   int64_t rows, int64_t cols, int64_t ld_x, const void* weight,
+                                   fp4q_dtype_t w_dtype, const float* mean, const float* rstd,
+                                   void* dx, int64_t ld_dx, float* dweight, float* dbias,
+                                   void* workspace, size_t workspace_bytes, void* stream) {
+    if (kind != FP4Q_LAYER_NORM && kind != FP4Q_RMS_NORM)
+        return fail(FP4Q_ERR_INVALID, "layer_norm_grad: bad kind %d", (int)kind);
+    if (!dy || !x || !rstd || !dx || (kind == FP4Q_LAYER_NORM && !mean))
+        return fail(FP4Q_ERR_INVALID, "layer_norm_grad: null pointer");
+    if (!valid_dtype(x_dtype) || !valid_dtype(dy_dtype) || !valid_dtype(w_dtype))
+        return fail(FP4Q_ERR_INVALID, "layer_norm_grad: bad dtype");
+    const int64_t ld = ld_x < ld_dy ? ld_x : ld_dy;
+    const fp4q_status_t e = norm_sizes("layer_norm_grad", rows, cols, ld < ld_dx ? ld : ld_dx);
+    if (e != FP4Q_OK) return e;
+    if (((uintptr_t)x % esize(x_dtype)) || ((uintptr_t)dy % esize(dy_dtype)) ||
+        ((uintptr_t)dx % esize(x_dtype)) || ((uintptr_t)weight % esize(w_dtype)) ||
+        ((uintptr_t)mean % 4) || ((uintptr_t)rstd % 4) || ((uintptr_t)dweight % 4) ||
+        ((uintptr_t)dbias % 4))
+        return fail(FP4Q_ERR_ALIGNMENT, "layer_norm_grad: pointers must be element-aligned");
+    if (dweight || dbias) {
+        const size_t need = fp4q::norm_grad_workspace_bytes(rows, cols);
+        if (!workspace) return fail(FP4Q_ERR_INVALID, "layer_norm_grad: null workspace");
+        if (!aligned16(workspace))
+            return fail(FP4Q_ERR_ALIGNMENT, "layer_norm_grad: workspace must be 16-byte aligned");
+        if (workspace_bytes < need)
+            return fail(FP4Q_ERR_WORKSPACE, "layer_norm_grad: workspace %zu < %zu bytes",
+                        workspace_bytes, need);
+    }
+    return hip_status(fp4q::launch_norm_grad(dy, dy_dtype, ld_dy, x, x_dtype, rows, cols, ld_x,
+                                             weight, w_dtype, mean, rstd, kind == FP4Q_RMS_NORM, dx,
+                                             ld_dx, dweight, dbias, workspace,
+                                             (hipStream_t)stream),
+                      "layer_norm_grad launch");
+}
+
+fp4q_status_t fp4q_adamw_step(const fp4q_adamw_tensor_t* tensors, int32_t n, int32_t state_bits,
+                              fp4q_dtype_t grad_dtype, double lr, double beta1, double beta2,
+                              double eps, int64_t step, uint64_t seed, const float* grad_scale,
+                              void* stream) {
+    if (n < 0 || (n > 0 && !tensors)) return fail(FP4Q_ERR_INVALID, "adamw_step: no tensors");
+    if (state_bits != 8 && state_bits != 32)
+        return fail(FP4Q_ERR_INVALID, "adamw_step: state_bits %d", state_bits);
+    if (!valid_dtype(grad_dtype)) return fail(FP4Q_ERR_INVALID, "adamw_step: bad grad dtype");
+    if (!(lr >= 0.0) || !(lr < 1e30) || !(eps >= 0.0) || !(eps < 1e30) || !(beta1 >= 0.0) ||
+        !(beta1 < 1.0) || !(beta2 >= 0.0) || !(beta2 < 1.0))
+        return fail(FP4Q_ERR_INVALID, "adamw_step: bad lr, eps or beta");
+    if (step < 1 || step >= ((int64_t)1 << 32))
+        return fail(FP4Q_ERR_INVALID, "adamw_step: step counts from 1, below 2^32");
+    if ((uintptr_t)grad_scale % 4)
+        return fail(FP4Q_ERR_ALIGNMENT, "adamw_step: grad_scale must be 4-byte aligned");
+    for (int32_t i = 0; i < n; ++i) {
+        const fp4q_adamw_tensor_t& t = tensors[i];
+        if (t.numel < 0 || t.numel >= ((int64_t)1 << 40))
+            return fail(FP4Q_ERR_INVALID, "adamw_step: tensor %d: numel", i);
+        if (!(t.weight_decay >= 0.0) || !(t.weight_decay < 1e30))
+            return fail(FP4Q_ERR_INVALID, "adamw_step: tensor %d: weight_decay", i);
+        if (t.numel == 0) continue;
+        if (!t.param || !t.grad || !t.exp_avg || !t.exp_avg_sq ||
+            (state_bits == 8 && (!t.exp_avg_scales || !t.exp_avg_sq_scales)))
+            return fail(FP4Q_ERR_INVALID, "adamw_step: tensor %d: null pointer", i);
+        if (!aligned16(t.param) || !aligned16(t.grad) || !aligned16(t.exp_avg) ||
+            !aligned16(t.exp_avg_sq) || !aligned16(t.copy))
+            return fail(FP4Q_ERR_ALIGNMENT, "adamw_step: tensor %d: pointers must be 16-byte aligned",
+                        i);
+    }
+    return hip_status(fp4q::launch_adamw(tensors, n, state_bits, grad_dtype, lr, beta1, beta2, eps,
+                                         step, seed, grad_scale, (hipStream_t)stream),
+                      "adamw_step launch");
 }
 
 }  // extern "C"

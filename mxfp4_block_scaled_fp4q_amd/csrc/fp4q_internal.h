@@ -5,6 +5,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+struct fp4q_adamw_tensor;  // include/libfp4q.h
+
 namespace fp4q {
 
 // Options for the next kernel this thread launches through the library
@@ -150,5 +152,30 @@ hipError_t launch_occ_quantize(const void* x, int64_t rows, int64_t cols, int64_
 hipError_t launch_occ_spmm(int64_t M, int64_t N, const int64_t* row_ptr, const int32_t* col_idx,
                            const float* vals, const void* w, int64_t ldw, float* y, int64_t ldy,
                            hipStream_t s);
+// Gated feed-forward: h = act(x wg^T) * (x wu^T), with the two products kept
+// in gate, up where they are not null; and the gradient of the two behind a
+// down projection (K % 64 == 0 both).
+hipError_t launch_gemm_gated(int64_t M, int64_t F, int64_t K, const uint8_t* xc,
+                             const uint8_t* xs, const uint8_t* gc, const uint8_t* gs,
+                             const uint8_t* uc, const uint8_t* us, int act, uint16_t* h,
+                             int64_t ldh, uint16_t* gate, uint16_t* up, int64_t ldgu,
+                             hipStream_t s);
+hipError_t launch_gemm_gated_grad(int64_t M, int64_t F, int64_t K, const uint8_t* yc,
+                                  const uint8_t* ys, const uint8_t* wc, const uint8_t* ws,
+                                  int act, const uint16_t* gate, const uint16_t* up,
+                                  int64_t ldgu, uint16_t* dgate, uint16_t* dup, int64_t ldd,
+                                  hipStream_t s);
+// Layer norm / RMS norm of rows; w, b, mean, rstd may be null.
+hipError_t launch_norm(const void* x, int xdtype, int64_t rows, int64_t cols, int64_t ldx,
+                       const void* w, const void* b, int wdtype, float eps, bool rms, void* y,
+                       int ydtype, int64_t ldy, float* mean, float* rstd, hipStream_t s);
+size_t norm_grad_workspace_bytes(int64_t rows, int64_t cols);
+hipError_t launch_norm_grad(const void* dy, int dydtype, int64_t lddy, const void* x, int xdtype,
+                            int64_t rows, int64_t cols, int64_t ldx, const void* w, int wdtype,
+                            const float* mean, const float* rstd, bool rms, void* dx, int64_t lddx,
+                            float* dw, float* db, void* ws, hipStream_t s);
+hipError_t launch_adamw(const fp4q_adamw_tensor* t, int n, int bits, int gdtype, double lr,
+                        double beta1, double beta2, double eps, int64_t step, uint64_t seed,
+                        const float* grad_scale, hipStream_t s);
 
 }  // namespace fp4q
