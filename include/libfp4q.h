@@ -636,6 +636,23 @@ fp4q_status_t fp4q_adamw_step(const fp4q_adamw_tensor_t* tensors, int32_t n, int
                               void* stream);
 
 /*
+ * fp4q_adamw_table, fp4q_adamw_step_table -- the same step in one launch for
+ * any number of tensors.  fp4q_adamw_table (host only, nothing launched) lays
+ * the descriptors out in HOST memory `table` (16-byte aligned, *table_bytes
+ * long; NULL to ask for the size); it sets *table_bytes to what is needed and
+ * *chunks to the number of chunks.  The caller copies those bytes to device
+ * memory once and passes the copy, n, chunks and state_bits to every step,
+ * which gives the bits that fp4q_adamw_step gives.  The table holds the
+ * tensors' addresses and weight decays: it is made anew when one changes.
+ */
+fp4q_status_t fp4q_adamw_table(const fp4q_adamw_tensor_t* tensors, int32_t n, int32_t state_bits,
+                               void* table, size_t* table_bytes, int64_t* chunks);
+fp4q_status_t fp4q_adamw_step_table(const void* table, int32_t n, int64_t chunks,
+                                    int32_t state_bits, fp4q_dtype_t grad_dtype, double lr,
+                                    double beta1, double beta2, double eps, int64_t step,
+                                    uint64_t seed, const float* grad_scale, void* stream);
+
+/*
  * fp4q_set_next_launch -- options for the next kernel that this thread
  * launches through the library (the first kernel of the next entry point
  * called, for entry points that launch several).  With any option given,

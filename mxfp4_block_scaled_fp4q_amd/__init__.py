@@ -32,6 +32,7 @@ EXPORTS = ["fp4q_channel_mask", "fp4q_quantize_masked", "fp4q_gemm_hcp_split",
            "fp4q_occ_workspace_bytes", "fp4q_occ_quantize", "fp4q_occ_spmm",
            "fp4q_gemm_gated", "fp4q_gemm_gated_grad", "fp4q_layer_norm",
            "fp4q_layer_norm_grad_workspace_bytes", "fp4q_layer_norm_grad", "fp4q_adamw_step",
+           "fp4q_adamw_table", "fp4q_adamw_step_table",
            "fp4q_set_next_launch", "fp4q_status_string",
            "fp4q_last_error", "fp4q_abi_version"]
 
@@ -104,6 +105,8 @@ def lib():
             "fp4q_layer_norm_grad": (I32, [I32, P, I32, I64, P, I32, I64, I64, I64, P, I32, P, P,
                                            P, I64, P, P, P, SZ, P]),
             "fp4q_adamw_step": (I32, [P, I32, I32, I32, D, D, D, D, I64, U64, P, P]),
+            "fp4q_adamw_table": (I32, [P, I32, I32, P, P, P]),
+            "fp4q_adamw_step_table": (I32, [P, I32, I64, I32, I32, D, D, D, D, I64, U64, P, P]),
             "fp4q_set_next_launch": (I32, [P, P, _ct.c_uint32]),
             "fp4q_status_string": (_ct.c_char_p, [I32]),
             "fp4q_last_error": (_ct.c_char_p, []),
@@ -122,13 +125,19 @@ def _check(status):
         raise Fp4qError(status, lib().fp4q_last_error().decode())
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _ptr(t):
-    return _ct.c_void_p(t.data_ptr()) if t is not None else None
+    return t.data_ptr() if t is not None else None
 
 
 def _dt(t):
@@ -141,9 +150,11 @@ def _dt(t):
 
 
 def _stream(stream):
+    if stream is not None:
+        return stream.cuda_stream
     torch = _torch()
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return _ct.c_void_p(s.cuda_stream)
+    # the current stream's handle, without building a Stream object per call
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _need_cuda(*ts):
@@ -735,10 +746,23 @@ def layer_norm_grad(dy, x, weight, mean, rstd, kind=LAYER_NORM, dx=None, want_we
 
 class AdamwPlan:
     """The tensors of an AdamW step, checked once (see adamw_plan).  Holds
-    references to them."""
+    references to them and, for more tensors than one launch takes as kernel
+    arguments, their table in device memory."""
+    ARGUMENTS = 44
 
-    def __init__(self, array, bits, grad_dtype, tensors):
-        self.array, self.bits, self.grad_dtype, self.tensors = array, bits, grad_dtype, tensors
+    def __init__(self, array, n, bits, grad_dtype, tensors):
+        self.array, self.n, self.bits, self.grad_dtype = array, n, bits, grad_dtype
+        self.tensors = tensors
+        self.table, self.chunks = None, 0
+        if n > self.ARGUMENTS:
+            torch = _torch()
+            size, chunks = _ct.c_size_t(0), _ct.c_int64(0)
+            fill = lib().fp4q_adamw_table
+            _check(fill(array, n, bits, None, _ct.byref(size), _ct.byref(chunks)))
+            host = torch.empty(size.value + 16, dtype=torch.uint8)
+            host = host[-host.data_ptr() % 16:][:size.value]
+            _check(fill(array, n, bits, host.data_ptr(), _ct.byref(size), _ct.byref(chunks)))
+            self.table, self.chunks = host.to(tensors[0][0].device), chunks.value
 
 
 def adamw_state(param, bits=32):
@@ -784,21 +808,22 @@ def adamw_plan(params, grads, exp_avg, exp_avg_sq, exp_avg_scales=None, exp_avg_
     array = (AdamwTensor * max(n, 1))()
     for i, (p, g, m, v, ms, vs, c, wd) in enumerate(zip(*cols.values())):
         k = p.numel()
+        nb = (k + 31) // 32
         for t, name, dtype, size in ((p, "param", torch.float32, k), (g, "grad", gdtype, k),
                                      (m, "exp_avg", state, k), (v, "exp_avg_sq", state, k),
-                                     (ms, "exp_avg_scales", torch.uint8, (k + 31) // 32),
-                                     (vs, "exp_avg_sq_scales", torch.uint8, (k + 31) // 32),
+                                     (ms, "exp_avg_scales", torch.uint8, nb),
+                                     (vs, "exp_avg_sq_scales", torch.uint8, nb),
                                      (c, "copy", torch.bfloat16, k)):
             if t is None:
                 continue
             _need_cuda(t)
-            _need(t, f"{name} {i}", dtype)
-            if t.numel() != size:
+            if t.dtype != dtype or t.numel() != size or not t.is_contiguous():
+                _need(t, f"{name} {i}", dtype)
                 raise ValueError(f"{name} {i} must have {size} elements, got {t.numel()}")
         array[i] = AdamwTensor(*(0 if t is None else t.data_ptr() for t in (p, g, m, v, ms, vs, c)),
                                k, wd)
-    return AdamwPlan(array, bits, BF16 if gdtype == torch.bfloat16 else F32,
-                     (list(zip(*list(cols.values())[:-1])), n))
+    return AdamwPlan(array, n, bits, BF16 if gdtype == torch.bfloat16 else F32,
+                     list(zip(*list(cols.values())[:-1])))
 
 
 def adamw_step(plan, lr, step, beta1=0.9, beta2=0.999, eps=1e-8, seed=0, grad_scale=None,
@@ -809,6 +834,10 @@ def adamw_step(plan, lr, step, beta1=0.9, beta2=0.999, eps=1e-8, seed=0, grad_sc
     if grad_scale is not None:
         _need_cuda(grad_scale)
         _need(grad_scale, "grad_scale", _torch().float32)
-    _check(lib().fp4q_adamw_step(plan.array, plan.tensors[1], plan.bits, plan.grad_dtype, lr,
-                                 beta1, beta2, eps, step, seed, _ptr(grad_scale),
-                                 _stream(stream)))
+    if plan.table is None:
+        _check(lib().fp4q_adamw_step(plan.array, plan.n, plan.bits, plan.grad_dtype, lr, beta1, beta2,
+                                     eps, step, seed, _ptr(grad_scale), _stream(stream)))
+    else:
+        _check(lib().fp4q_adamw_step_table(plan.table.data_ptr(), plan.n, plan.chunks, plan.bits,
+                                           plan.grad_dtype, lr, beta1, beta2, eps, step, seed,
+                                           _ptr(grad_scale), _stream(stream)))

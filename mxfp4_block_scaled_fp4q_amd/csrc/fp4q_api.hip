@@ -43,8 +43,8 @@ static_assert(fp4q::kHcpStaticScratchBytes == FP4Q_HCP_NOALLOC_MAX_BYTES,
 // chunks; element counts up to 2^33 are accepted.
 constexpr int64_t kMaxElems = (int64_t)1 << 33;
 
-// Sizes that the gated calls share (as fp4q_gemm's; the tiles of one launch
-// are counted in 31 bits).
+// Sizes that the gated calls share (as fp4q_gemm's; a launch holds below 2^32
+// threads, 512 to a tile).
 fp4q_status_t gated_sizes(const char* who, int64_t M, int64_t F, int64_t K) {
     if (M <= 0 || F <= 0 || K <= 0) return fail(FP4Q_ERR_INVALID, "%s: bad sizes", who);
     if (K % 64) return fail(FP4Q_ERR_INVALID, "%s: K %% 64 != 0", who);
@@ -52,7 +52,7 @@ fp4q_status_t gated_sizes(const char* who, int64_t M, int64_t F, int64_t K) {
         return fail(FP4Q_ERR_INVALID, "%s: dimension too large", who);
     if (K >= ((int64_t)1 << 24))
         return fail(FP4Q_ERR_UNSUPPORTED, "%s: K must be below 2^24", who);
-    if (((M + 255) / 256) * ((F + 127) / 128) >= ((int64_t)1 << 31))
+    if (((M + 255) / 256) * ((F + 127) / 128) >= ((int64_t)1 << 22))
         return fail(FP4Q_ERR_UNSUPPORTED, "%s: too many tiles", who);
     return FP4Q_OK;
 }
@@ -63,6 +63,44 @@ fp4q_status_t norm_sizes(const char* who, int64_t rows, int64_t cols, int64_t ld
     if (rows >= ((int64_t)1 << 31) || cols >= ((int64_t)1 << 31))
         return fail(FP4Q_ERR_INVALID, "%s: dimension too large", who);
     if (ld < cols) return fail(FP4Q_ERR_INVALID, "%s: row stride below cols", who);
+    return FP4Q_OK;
+}
+
+// Arguments that the AdamW calls share.
+fp4q_status_t adamw_scalars(const char* who, int32_t state_bits, fp4q_dtype_t grad_dtype, double lr,
+                            double beta1, double beta2, double eps, int64_t step,
+                            const float* grad_scale) {
+    if (state_bits != 8 && state_bits != 32)
+        return fail(FP4Q_ERR_INVALID, "%s: state_bits %d", who, state_bits);
+    if (!valid_dtype(grad_dtype)) return fail(FP4Q_ERR_INVALID, "%s: bad grad dtype", who);
+    if (!(lr >= 0.0) || !(lr < 1e30) || !(eps >= 0.0) || !(eps < 1e30) || !(beta1 >= 0.0) ||
+        !(beta1 < 1.0) || !(beta2 >= 0.0) || !(beta2 < 1.0))
+        return fail(FP4Q_ERR_INVALID, "%s: bad lr, eps or beta", who);
+    if (step < 1 || step >= ((int64_t)1 << 32))
+        return fail(FP4Q_ERR_INVALID, "%s: step counts from 1, below 2^32", who);
+    if ((uintptr_t)grad_scale % 4)
+        return fail(FP4Q_ERR_ALIGNMENT, "%s: grad_scale must be 4-byte aligned", who);
+    return FP4Q_OK;
+}
+fp4q_status_t adamw_tensors(const char* who, const fp4q_adamw_tensor_t* tensors, int32_t n,
+                            int32_t state_bits) {
+    if (n < 0 || (n > 0 && !tensors)) return fail(FP4Q_ERR_INVALID, "%s: no tensors", who);
+    if (state_bits != 8 && state_bits != 32)
+        return fail(FP4Q_ERR_INVALID, "%s: state_bits %d", who, state_bits);
+    for (int32_t i = 0; i < n; ++i) {
+        const fp4q_adamw_tensor_t& t = tensors[i];
+        if (t.numel < 0 || t.numel >= ((int64_t)1 << 40))
+            return fail(FP4Q_ERR_INVALID, "%s: tensor %d: numel", who, i);
+        if (!(t.weight_decay >= 0.0) || !(t.weight_decay < 1e30))
+            return fail(FP4Q_ERR_INVALID, "%s: tensor %d: weight_decay", who, i);
+        if (t.numel == 0) continue;
+        if (!t.param || !t.grad || !t.exp_avg || !t.exp_avg_sq ||
+            (state_bits == 8 && (!t.exp_avg_scales || !t.exp_avg_sq_scales)))
+            return fail(FP4Q_ERR_INVALID, "%s: tensor %d: null pointer", who, i);
+        if (!aligned16(t.param) || !aligned16(t.grad) || !aligned16(t.exp_avg) ||
+            !aligned16(t.exp_avg_sq) || !aligned16(t.copy))
+            return fail(FP4Q_ERR_ALIGNMENT, "%s: tensor %d: pointers must be 16-byte aligned", who, i);
+    }
     return FP4Q_OK;
 }
 
@@ -789,35 +827,48 @@ fp4q_status_t fp4q_adamw_step(const fp4q_adamw_tensor_t* tensors, int32_t n, int
                               fp4q_dtype_t grad_dtype, double lr, double beta1, double beta2,
                               double eps, int64_t step, uint64_t seed, const float* grad_scale,
                               void* stream) {
-    if (n < 0 || (n > 0 && !tensors)) return fail(FP4Q_ERR_INVALID, "adamw_step: no tensors");
-    if (state_bits != 8 && state_bits != 32)
-        return fail(FP4Q_ERR_INVALID, "adamw_step: state_bits %d", state_bits);
-    if (!valid_dtype(grad_dtype)) return fail(FP4Q_ERR_INVALID, "adamw_step: bad grad dtype");
-    if (!(lr >= 0.0) || !(lr < 1e30) || !(eps >= 0.0) || !(eps < 1e30) || !(beta1 >= 0.0) ||
-        !(beta1 < 1.0) || !(beta2 >= 0.0) || !(beta2 < 1.0))
-        return fail(FP4Q_ERR_INVALID, "adamw_step: bad lr, eps or beta");
-    if (step < 1 || step >= ((int64_t)1 << 32))
-        return fail(FP4Q_ERR_INVALID, "adamw_step: step counts from 1, below 2^32");
-    if ((uintptr_t)grad_scale % 4)
-        return fail(FP4Q_ERR_ALIGNMENT, "adamw_step: grad_scale must be 4-byte aligned");
-    for (int32_t i = 0; i < n; ++i) {
-        const fp4q_adamw_tensor_t& t = tensors[i];
-        if (t.numel < 0 || t.numel >= ((int64_t)1 << 40))
-            return fail(FP4Q_ERR_INVALID, "adamw_step: tensor %d: numel", i);
-        if (!(t.weight_decay >= 0.0) || !(t.weight_decay < 1e30))
-            return fail(FP4Q_ERR_INVALID, "adamw_step: tensor %d: weight_decay", i);
-        if (t.numel == 0) continue;
-        if (!t.param || !t.grad || !t.exp_avg || !t.exp_avg_sq ||
-            (state_bits == 8 && (!t.exp_avg_scales || !t.exp_avg_sq_scales)))
-            return fail(FP4Q_ERR_INVALID, "adamw_step: tensor %d: null pointer", i);
-        if (!aligned16(t.param) || !aligned16(t.grad) || !aligned16(t.exp_avg) ||
-            !aligned16(t.exp_avg_sq) || !aligned16(t.copy))
-            return fail(FP4Q_ERR_ALIGNMENT, "adamw_step: tensor %d: pointers must be 16-byte aligned",
-                        i);
-    }
+    fp4q_status_t e = adamw_scalars("adamw_step", state_bits, grad_dtype, lr, beta1, beta2, eps, step,
+                                    grad_scale);
+    if (e == FP4Q_OK) e = adamw_tensors("adamw_step", tensors, n, state_bits);
+    if (e != FP4Q_OK) return e;
     return hip_status(fp4q::launch_adamw(tensors, n, state_bits, grad_dtype, lr, beta1, beta2, eps,
                                          step, seed, grad_scale, (hipStream_t)stream),
                       "adamw_step launch");
+}
+
+fp4q_status_t fp4q_adamw_table(const fp4q_adamw_tensor_t* tensors, int32_t n, int32_t state_bits,
+                               void* table, size_t* table_bytes, int64_t* chunks) {
+    if (!table_bytes || !chunks) return fail(FP4Q_ERR_INVALID, "adamw_table: null pointer");
+    const fp4q_status_t e = adamw_tensors("adamw_table", tensors, n, state_bits);
+    if (e != FP4Q_OK) return e;
+    const size_t need = fp4q::adamw_table_bytes(tensors, n, chunks);
+    if (*chunks >= ((int64_t)1 << 31))
+        return fail(FP4Q_ERR_UNSUPPORTED, "adamw_table: too many elements");
+    const size_t have = *table_bytes;
+    *table_bytes = need;
+    if (!table) return FP4Q_OK;
+    if (!aligned16(table))
+        return fail(FP4Q_ERR_ALIGNMENT, "adamw_table: table must be 16-byte aligned");
+    if (have < need) return fail(FP4Q_ERR_WORKSPACE, "adamw_table: table %zu < %zu bytes", have, need);
+    fp4q::adamw_table(tensors, n, table);
+    return FP4Q_OK;
+}
+
+fp4q_status_t fp4q_adamw_step_table(const void* table, int32_t n, int64_t chunks, int32_t state_bits,
+                                    fp4q_dtype_t grad_dtype, double lr, double beta1, double beta2,
+                                    double eps, int64_t step, uint64_t seed,
+                                    const float* grad_scale, void* stream) {
+    const fp4q_status_t e = adamw_scalars("adamw_step_table", state_bits, grad_dtype, lr, beta1, beta2,
+                                          eps, step, grad_scale);
+    if (e != FP4Q_OK) return e;
+    if (n < 0 || chunks < 0 || chunks >= ((int64_t)1 << 31) || (chunks > 0 && (!table || n == 0)))
+        return fail(FP4Q_ERR_INVALID, "adamw_step_table: no table");
+    if (!aligned16(table))
+        return fail(FP4Q_ERR_ALIGNMENT, "adamw_step_table: table must be 16-byte aligned");
+    return hip_status(fp4q::launch_adamw_table(table, n, chunks, state_bits, grad_dtype, lr, beta1,
+                                               beta2, eps, step, seed, grad_scale,
+                                               (hipStream_t)stream),
+                      "adamw_step_table launch");
 }
 
 }  // extern "C"

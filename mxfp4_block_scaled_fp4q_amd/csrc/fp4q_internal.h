@@ -177,5 +177,13 @@ hipError_t launch_norm_grad(const void* dy, int dydtype, int64_t lddy, const voi
 hipError_t launch_adamw(const fp4q_adamw_tensor* t, int n, int bits, int gdtype, double lr,
                         double beta1, double beta2, double eps, int64_t step, uint64_t seed,
                         const float* grad_scale, hipStream_t s);
+// The descriptors and the tensor of every chunk of 4096 elements, as the
+// device reads them: bytes (and chunks), the table itself (host memory), and a
+// step that reads it from device memory.
+size_t adamw_table_bytes(const fp4q_adamw_tensor* t, int n, int64_t* groups);
+void adamw_table(const fp4q_adamw_tensor* t, int n, void* table);
+hipError_t launch_adamw_table(const void* table, int n, int64_t groups, int bits, int gdtype,
+                              double lr, double beta1, double beta2, double eps, int64_t step,
+                              uint64_t seed, const float* grad_scale, hipStream_t s);
 
 }  // namespace fp4q

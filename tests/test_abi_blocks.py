@@ -143,3 +143,44 @@ def test_binding_refuses_host_tensors_and_mismatches():
         fq.adamw_plan([x], [x], [x], [x], exp_avg_scales=[x])
     with pytest.raises(ValueError, match="8 or 32"):
         fq.adamw_state(x, 4)
+
+
+def table(L, t, n=None, bits=32, buf=None, nbytes=0):
+    arr = (fq.AdamwTensor * max(len(t), 1))(*t)
+    size, chunks = ct.c_size_t(nbytes), ct.c_int64(-1)
+    status = L.fp4q_adamw_table(arr, len(t) if n is None else n, bits, buf, ct.byref(size), ct.byref(chunks))
+    return status, size.value, chunks.value
+
+
+def test_adamw_table_refusals(L):
+    assert table(L, [tensor(), tensor(grad=NUL)])[0] == 1
+    assert table(L, [tensor()], n=-1)[0] == 1 and table(L, [tensor()], bits=4)[0] == 1
+    assert table(L, [tensor(param=FAKE + 4)])[0] == 3
+    arr = (fq.AdamwTensor * 1)(tensor())
+    assert L.fp4q_adamw_table(arr, 1, 32, NUL, NUL, NUL) == 1
+    status, size, chunks = table(L, [tensor(numel=4096), tensor(numel=4097), tensor(numel=0)])
+    assert status == 0 and chunks == 3
+    buf = (ct.c_uint8 * (size + 32))()
+    at = (ct.addressof(buf) + 15) // 16 * 16
+    same = [tensor(numel=4096), tensor(numel=4097), tensor(numel=0)]
+    assert table(L, same, buf=at, nbytes=size - 1)[0] == 4
+    assert table(L, same, buf=at + 8, nbytes=size)[0] == 3
+    assert table(L, same, buf=at, nbytes=size) == (0, size, 3)
+    # the owners of the three chunks stand behind the descriptors
+    owners = ct.cast(at + size - 12, ct.POINTER(ct.c_uint32))
+    assert [owners[i] for i in range(3)] == [0, 1, 1]
+    assert table(L, [tensor(numel=(1 << 40) - 1)] * 8)[0] == 2
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(table=NUL), 1), (dict(n=-1), 1), (dict(n=0), 1), (dict(chunks=-1), 1), (dict(chunks=1 << 31), 1),
+    (dict(table=FAKE + 8), 3), (dict(bits=16), 1), (dict(gdt=3), 1), (dict(lr=-1.0), 1), (dict(step=0), 1),
+    (dict(scale=FAKE + 1), 3),
+])
+def test_adamw_step_table_refusals(L, kw, status):
+    a = dict(table=FAKE, n=2, chunks=3, bits=32, gdt=0, lr=1e-3, b1=0.9, b2=0.95, eps=1e-8, step=1, seed=0,
+             scale=NUL)
+    a.update(kw)
+    assert L.fp4q_adamw_step_table(*a.values(), NUL) == status
+    assert "adamw_step_table" in L.fp4q_last_error().decode()
+    assert L.fp4q_adamw_step_table(NUL, 0, 0, 32, 0, 1e-3, 0.9, 0.95, 1e-8, 1, 0, NUL, NUL) == 0

@@ -275,3 +275,24 @@ def test_other_stream_and_graph_replays():
         want = run(bits, "plain")
         for how in ("stream", "graph"):
             assert all(torch.equal(a, b) for a, b in zip(run(bits, how), want)), (bits, how)
+
+
+@pytest.mark.parametrize("gdt", GRADS)
+@pytest.mark.parametrize("bits", [32, 8])
+def test_table_gives_the_same_bits_as_arguments(bits, gdt):
+    """One launch that reads a table, and launches of 44 tensors each."""
+    sizes = [1 + (i * 977) % 9000 for i in range(97)] + [0, 3 * 4096 + 5]
+
+    def run(table):
+        prob = Problem(sizes, bits, gdt, copy=True)
+        plan = prob.plan([0.1 * (i % 2) for i in range(len(sizes))])
+        assert plan.table is not None and plan.chunks == sum((k + 4095) // 4096 for k in sizes)
+        if not table:
+            plan.table = None
+        for step in (1, 2):
+            fq.adamw_step(plan, step=step, seed=9, **HYPER)
+        torch.cuda.synchronize()
+        assert prob.guards_intact()
+        return [t for t in (prob.p, prob.m, prob.v, prob.c, prob.ms, prob.vs) if t is not None]
+    for a, b in zip(run(True), run(False)):
+        assert torch.equal(a, b)
