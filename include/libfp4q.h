@@ -517,9 +517,9 @@ fp4q_status_t fp4q_hot_channels(const void* x, int64_t rows, int64_t cols, int64
  *   K % 64 == 0, K < 2^24; M, F >= 1 arbitrary.  Code pointers and x_scales
  *   16-byte aligned; the weights' scales 4-byte aligned (2-byte where
  *   K % 128 == 64), so that halves of a packed array qualify for every F;
- *   h, gate, up element-aligned (16-byte rows are written faster).
- *   Deterministic: no atomics; an output's sum over K does not depend on F or
- *   on the other rows.  A 0xFF scale byte gives NaN in the outputs it feeds.
+ *   h, gate, up element-aligned.
+ *   Deterministic: no atomics, and the order of an output's sum over K depends
+ *   on M, F and K alone.  A 0xFF scale byte gives NaN in the outputs it feeds.
  */
 typedef enum { FP4Q_SILU = 0, FP4Q_GELU = 1 } fp4q_act_t;
 fp4q_status_t fp4q_gemm_gated(int64_t M, int64_t F, int64_t K, const uint8_t* x_codes,
@@ -558,8 +558,7 @@ fp4q_status_t fp4q_gemm_gated_grad(int64_t M, int64_t F, int64_t K, const uint8_
  *   w_dtype, NULL for ones and zeros; mean, rstd: fp32 [rows], written for
  *   the gradient, NULL to skip (mean is not written with FP4Q_RMS_NORM).
  *   The squares are summed around the mean, in fp32.  eps >= 0.  Any cols;
- *   every pointer needs only its element's alignment (16-byte rows run
- *   faster).  A row holding Inf or NaN gives NaN in that row alone.
+ *   every pointer needs only its element's alignment.  A row holding Inf or NaN gives NaN in that row alone.
  */
 typedef enum { FP4Q_LAYER_NORM = 0, FP4Q_RMS_NORM = 1 } fp4q_norm_t;
 fp4q_status_t fp4q_layer_norm(fp4q_norm_t kind, const void* x, fp4q_dtype_t x_dtype, int64_t rows,

@@ -42,9 +42,6 @@
 
 namespace fp4q {
 
-typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
-typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
-
 constexpr int kTensors = 44;     // descriptors per launch: 4 KB of kernel arguments
 constexpr int kChunk = 4096;     // elements per workgroup
 constexpr int kMaxGroups = 1 << 23;  // workgroups per launch: 2^31 threads

@@ -13,9 +13,6 @@ namespace fp4q {
 typedef int v8i __attribute__((ext_vector_type(8)));
 typedef float v16f __attribute__((ext_vector_type(16)));
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
-// Native 4 x 32-bit vectors (HIP's uint4 is a class with unions, which the
-// compiler does not always split into registers).
-typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
 
 static constexpr int BKB = 64;                  // operand bytes per row per K step

@@ -26,10 +26,6 @@
 
 namespace fp4q {
 
-typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
-typedef u32x4 u32x4_a2 __attribute__((aligned(2)));  // at any element's alignment
-typedef u32x4 u32x4_a4 __attribute__((aligned(4)));
-
 template <int BF16T>
 __device__ __forceinline__ float load1(const void* p, int64_t i) {
     if (BF16T) return as_f32((uint32_t)((const uint16_t*)p)[i] << 16);

@@ -92,6 +92,23 @@ def test_forward_row_counts_agree_and_match(orc, M):
     forward_check(orc, x, g, u, fq.SILU, save=True, rows=rows)
 
 
+# 128-row tiles, 256-row tiles and 256 x 256 tiles, with and without a half K step
+TILED = [(250, 1500, 448), (1100, 800, 1152), (1100, 2990, 192), (900, 3900, 1664), (2100, 4100, 320),
+         (2050, 4000, 2176)]
+
+
+def some_rows(M):
+    return np.unique(np.r_[0, 1, M // 2, M - 1, np.linspace(0, M - 1, 6).astype(int)])
+
+
+@pytest.mark.parametrize("act", [fq.SILU, fq.GELU])
+@pytest.mark.parametrize("M,F,K", TILED)
+def test_forward_tiled_forms(orc, M, F, K, act):
+    x, g, u = quant(orc, M, K, M, 1.0), quant(orc, F, K, F + 7, 0.05), quant(orc, F, K, F + 9, 0.05)
+    forward_check(orc, x, g, u, act, save=True, pad=5, rows=some_rows(M))
+    forward_check(orc, x, g, u, act, save=False, rows=some_rows(M))
+
+
 def test_forward_deep_and_wide(orc):
     x, g, u = quant(orc, 40, 5120, 1, 1.0), quant(orc, 384, 5120, 2, 0.02), quant(orc, 384, 5120, 3, 0.02)
     forward_check(orc, x, g, u, fq.SILU, save=True)
@@ -163,6 +180,13 @@ def grad_check(orc, M, F, K, act, pad=0, packed=True, rows=None, sd=1.0):
 def test_grad(orc, M, F, K, act):
     grad_check(orc, M, F, K, act, pad=8, packed=False)
     grad_check(orc, M, F, K, act, pad=1)
+
+
+@pytest.mark.parametrize("act", [fq.SILU, fq.GELU])
+@pytest.mark.parametrize("M,F,K", [(1100, 2000, 448), (1100, 3900, 320), (1500, 5000, 128), (3000, 5900, 1152),
+                                   (4100, 4400, 192)])
+def test_grad_tiled_forms(orc, M, F, K, act):
+    grad_check(orc, M, F, K, act, pad=3, rows=some_rows(M))
 
 
 @pytest.mark.parametrize("act", [fq.SILU, fq.GELU])
