@@ -344,7 +344,11 @@ __global__ __launch_bounds__(64 * Layout<CFG>::WAVES, 1) void gemm_gated_kernel(
                 const int row = row0 + i * 32 + rl;
                 if (row >= o.M) continue;
                 uint16_t* base = out == 0 ? o.h : out == 1 ? o.gate : o.up;
-                store8(base + (int64_t)row * (out == 0 ? o.ldh : o.ldgu) + col, v, o.F - col);
+                base += (int64_t)row * (out == 0 ? o.ldh : o.ldgu) + col;
+                if (o.lines)
+                    store8<1>(base, v, o.F - col);
+                else
+                    store8<0>(base, v, o.F - col);
             }
         __builtin_amdgcn_wave_barrier();
     }
@@ -377,9 +381,14 @@ __global__ __launch_bounds__(64 * Layout<CFG>::WAVES, 1) void gemm_gated_grad_ke
         for (int p = 0; p < PASSES; ++p) {
             const int row = row0 + i * 32 + p * 8;
             q.g[p] = q.u[p] = (u32x4){0u, 0u, 0u, 0u};
-            if (row < o.M) {
-                q.g[p] = load8(o.gate + (int64_t)row * o.ldgu + col, o.F - col);
-                q.u[p] = load8(o.up + (int64_t)row * o.ldgu + col, o.F - col);
+            if (row >= o.M || col >= o.F) continue;
+            const int64_t at = (int64_t)row * o.ldgu;
+            if (o.lines) {
+                q.g[p] = load8<1>(o.gate + at, col, o.F);
+                q.u[p] = load8<1>(o.up + at, col, o.F);
+            } else {
+                q.g[p] = load8<0>(o.gate + at, col, o.F);
+                q.u[p] = load8<0>(o.up + at, col, o.F);
             }
         }
     };
@@ -417,12 +426,17 @@ __global__ __launch_bounds__(64 * Layout<CFG>::WAVES, 1) void gemm_gated_grad_ke
             const float d[8] = {as_f32(d0.x), as_f32(d0.y), as_f32(d0.z), as_f32(d0.w),
                                 as_f32(d1.x), as_f32(d1.y), as_f32(d1.z), as_f32(d1.w)};
             u32x4 og, ou;
-            gated_grad8<GELU>(d, q.g[p], q.u[p], og, ou);
+            gated_grad8<GELU>(d, settle8(q.g[p], col, o.F), settle8(q.u[p], col, o.F), og, ou);
             const int row = row0 + i * 32 + p * 8;
             if (row >= o.M) continue;
             const int64_t off = (int64_t)row * o.ldd + col;
-            store8(o.dgate + off, og, o.F - col);
-            store8(o.dup + off, ou, o.F - col);
+            if (o.lines) {
+                store8<1>(o.dgate + off, og, o.F - col);
+                store8<1>(o.dup + off, ou, o.F - col);
+            } else {
+                store8<0>(o.dgate + off, og, o.F - col);
+                store8<0>(o.dup + off, ou, o.F - col);
+            }
         }
         __builtin_amdgcn_wave_barrier();
         if (!kEarly && i + 2 < G::TM) fetch(i + 2, q);
@@ -445,6 +459,8 @@ static hipError_t go_forward(const GatedCall& g, hipStream_t s) {
 #undef FP4Q_GO
     return hipGetLastError();
 }
+static bool lines(const void* p, int64_t ld) { return (uintptr_t)p % 128 == 0 && ld % 64 == 0; }
+
 // Tiles of bm x bn outputs.
 static int64_t tiles_of(const GatedCall& g, int bm, int bn) {
     return ((int64_t)g.M + bm - 1) / bm * ((g.F + bn - 1) / bn);
@@ -480,7 +496,8 @@ hipError_t launch_gemm_gated(int64_t M, int64_t F, int64_t K, const uint8_t* xc,
                              int64_t ldh, uint16_t* gate, uint16_t* up, int64_t ldgu,
                              hipStream_t s) {
     const GatedCall g{(int)M, (int)F, (int)K, xc, xs, gc, gs, uc, us, h, ldh, gate, up, ldgu,
-                      nullptr, nullptr, 0};
+                      nullptr, nullptr, 0,
+                      lines(h, ldh) && (!gate || (lines(gate, ldgu) && lines(up, ldgu)))};
     return act ? pick_forward<1>(g, s) : pick_forward<0>(g, s);
 }
 
@@ -509,7 +526,8 @@ hipError_t launch_gemm_gated_grad(int64_t M, int64_t F, int64_t K, const uint8_t
                                   int64_t ldgu, uint16_t* dgate, uint16_t* dup, int64_t ldd,
                                   hipStream_t s) {
     const GatedCall g{(int)M, (int)F, (int)K, yc, ys, wc, ws, nullptr, nullptr, nullptr, 0,
-                      (uint16_t*)gate, (uint16_t*)up, ldgu, dgate, dup, ldd};
+                      (uint16_t*)gate, (uint16_t*)up, ldgu, dgate, dup, ldd,
+                      lines(gate, ldgu) && lines(up, ldgu) && lines(dgate, ldd) && lines(dup, ldd)};
     return act ? pick_grad<1>(g, s) : pick_grad<0>(g, s);
 }
 

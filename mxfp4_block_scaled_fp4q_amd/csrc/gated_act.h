@@ -45,31 +45,71 @@ struct GatedCall {
     int64_t ldgu;
     uint16_t *dgate, *dup;       // gradient
     int64_t ldd;
+    int lines;                   // rows of all of these are whole cache lines
 };
 
 // Launches the small-tile form (gated_small.hip) and says so, where it is the
 // one to take.
 bool launch_gated_small(const GatedCall& g, bool grad, int gelu, hipStream_t s);
 
-// 8 bf16 of a row at p, of which the row still holds n: one 16-byte access (a
-// row may begin at any element), or its last elements one by one.
-__device__ __forceinline__ void store8(uint16_t* p, u32x4 v, int n) {
-    if (n >= 8) {
+// Non-temporal accesses of the outputs and of gate and up: faster where rows
+// are whole cache lines, much slower where lines are shared by two rows or
+// tiles, which then pass through memory in parts.
+template <int NT>
+__device__ __forceinline__ void put16(uint16_t* p, u32x4 v) {
+    if (NT)
         __builtin_nontemporal_store(v, (u32x4_a2*)p);
-        return;
-    }
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-        if (e < n) p[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+    else
+        *(u32x4_a2*)p = v;
 }
-__device__ __forceinline__ u32x4 load8(const uint16_t* p, int n) {
-    if (n >= 8) return __builtin_nontemporal_load((const u32x4_a2*)p);
+
+// 8 bf16 at p, of which the row still holds n.
+template <int NT>
+__device__ __forceinline__ void store8(uint16_t* p, u32x4 v, int n) {
+    typedef u32x2 u32x2_a2 __attribute__((aligned(2)));
+    typedef uint32_t u32_a2 __attribute__((aligned(2)));
+    if (n >= 8) {
+        put16<NT>(p, v);
+    } else if (n > 0) {
+        uint32_t w = v.x;
+        if (n & 4) {
+            *(u32x2_a2*)p = (u32x2){v.x, v.y};
+            w = v.z;
+        }
+        uint16_t* q = p + (n & 4);
+        if (n & 2) *(u32_a2*)q = w;
+        if (n & 1) q[n & 2] = (uint16_t)((n & 2) ? ((n & 4) ? v.w : v.y) : w);
+    }
+}
+// Elements col .. col + 7 of a row of F, in two steps, so that no lane waits
+// for its data where it loads them: the row's last ones come from F - 8 and are
+// shifted into place at their use.  (Rows shorter than 8 go one by one.)
+template <int NT>
+__device__ __forceinline__ u32x4 load8(const uint16_t* row, int col, int F) {
+    if (F >= 8) {
+        const uint16_t* p = row + min(col, F - 8);
+        if (NT) return __builtin_nontemporal_load((const u32x4_a2*)p);
+        return *(const u32x4_a2*)p;
+    }
     uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-        if (e < n) w[e >> 1] |= (uint32_t)p[e] << (16 * (e & 1));
+        if (col + e < F) w[e >> 1] |= (uint32_t)row[col + e] << (16 * (e & 1));
     return (u32x4){w[0], w[1], w[2], w[3]};
+}
+__device__ __forceinline__ u32x4 settle8(u32x4 v, int col, int F) {
+    const int n = F - col;
+    if (n >= 8 || n <= 0 || F < 8) return v;
+    uint64_t lo = v.x | (uint64_t)v.y << 32, hi = v.z | (uint64_t)v.w << 32;
+    const int s = 16 * (8 - n);
+    if (s >= 64) {
+        lo = hi >> (s - 64);
+        hi = 0;
+    } else {
+        lo = lo >> s | hi << (64 - s);
+        hi >>= s;
+    }
+    return (u32x4){(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
 }
 
 // Of 8 elements with gradients d, gate g and up u (bf16 pairs), the gradients

@@ -61,8 +61,8 @@ __global__ __launch_bounds__(64 * KS) void gated_small_kernel(const GatedCall g,
             const int i = p * 64 * KS + threadIdx.x;
             const int row = m0 + i / (2 * NT), col = n0 + i % (2 * NT) * 8;
             if (i < GROUPS && row < g.M && col < g.F) {
-                gin[p] = load8(g.gate + row * g.ldgu + col, g.F - col);
-                uin[p] = load8(g.up + row * g.ldgu + col, g.F - col);
+                gin[p] = load8<0>(g.gate + row * g.ldgu, col, g.F);
+                uin[p] = load8<0>(g.up + row * g.ldgu, col, g.F);
             }
         }
     }
@@ -161,9 +161,10 @@ __global__ __launch_bounds__(64 * KS) void gated_small_kernel(const GatedCall g,
                 }
         if (GRAD) {
             u32x4 dg, du;
-            gated_grad8<GELU>(v[0], gin[p], uin[p], dg, du);
-            store8(g.dgate + row * g.ldd + col, dg, n);
-            store8(g.dup + row * g.ldd + col, du, n);
+            gated_grad8<GELU>(v[0], settle8(gin[p], col, g.F), settle8(uin[p], col, g.F), dg,
+                              du);
+            store8<0>(g.dgate + row * g.ldd + col, dg, n);
+            store8<0>(g.dup + row * g.ldd + col, du, n);
         } else {
             u32x4 hv, gv, uv;
 #pragma unroll
@@ -173,10 +174,10 @@ __global__ __launch_bounds__(64 * KS) void gated_small_kernel(const GatedCall g,
                 gv[e] = pack_rne(v[0][2 * e], v[0][2 * e + 1]);
                 uv[e] = pack_rne(v[1][2 * e], v[1][2 * e + 1]);
             }
-            store8(g.h + row * g.ldh + col, hv, n);
+            store8<0>(g.h + row * g.ldh + col, hv, n);
             if (SAVE) {
-                store8(g.gate + row * g.ldgu + col, gv, n);
-                store8(g.up + row * g.ldgu + col, uv, n);
+                store8<0>(g.gate + row * g.ldgu + col, gv, n);
+                store8<0>(g.up + row * g.ldgu + col, uv, n);
             }
         }
     }
