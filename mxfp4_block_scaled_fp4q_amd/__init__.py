@@ -152,9 +152,9 @@ def _dt(t):
 def _stream(stream):
     if stream is not None:
         return stream.cuda_stream
-    torch = _torch()
+    c = _torch()._C
     # the current stream's handle, without building a Stream object per call
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return c._cuda_getCurrentRawStream(c._cuda_getDevice())
 
 
 def _need_cuda(*ts):
@@ -587,26 +587,32 @@ def occ_spmm(row_ptr, col_idx, vals, w, y, stream=None):
 def _rows(t, name, dtype=None, shape=None):
     """Row stride of a 2-D device tensor with unit column stride (the stride
     of a single row, or of columns one element wide, is free)."""
-    _need_cuda(t)
-    if dtype is not None:
-        _need(t, name, dtype, shape, dense=False)
-    elif shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] != 1):
+    if not t.is_cuda:
+        _need_cuda(t)
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    size = t.shape
+    if shape is not None and size != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(size)}")
+    if len(size) != 2 or (t.stride(1) != 1 and size[1] != 1):
         raise ValueError(f"{name} must be 2-D with unit column stride")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+    return t.stride(0) if size[0] > 1 else max(t.stride(0), size[1])
 
 
 def _codes(codes, scales, name, rows=None, K=None):
     """Checks one K-major block-32 operand; returns its rows and K."""
-    torch = _torch()
-    _need_cuda(codes, scales)
-    if codes.dim() != 2:
+    u8, size = _torch().uint8, codes.shape
+    if not (codes.is_cuda and scales.is_cuda):
+        _need_cuda(codes, scales)
+    if len(size) != 2:
         raise ValueError(f"{name}_codes must be 2-D")
-    rows = codes.shape[0] if rows is None else rows
-    K = 2 * codes.shape[1] if K is None else K
-    _need(codes, f"{name}_codes", torch.uint8, (rows, K // 2))
-    _need(scales, f"{name}_scales", torch.uint8, (rows, K // 32))
+    rows = size[0] if rows is None else rows
+    K = 2 * size[1] if K is None else K
+    if (codes.dtype != u8 or scales.dtype != u8 or size != (rows, K // 2)
+            or scales.shape != (rows, K // 32) or not codes.is_contiguous()
+            or not scales.is_contiguous()):
+        _need(codes, f"{name}_codes", u8, (rows, K // 2))  # one of these says which
+        _need(scales, f"{name}_scales", u8, (rows, K // 32))
     return rows, K
 
 
@@ -617,23 +623,24 @@ def gemm_gated(x_codes, x_scales, gate_codes, gate_scales, up_codes, up_scales, 
     one packed array will do).  Returns h (bf16 [M, F]), or (h, gate, up)
     where save is set or gate and up are given; with save alone they are the
     halves of one [M, 2F] tensor."""
-    torch = _torch()
+    bf16 = _torch().bfloat16
     M, K = _codes(x_codes, x_scales, "x")
     F, _ = _codes(gate_codes, gate_scales, "gate", K=K)
     _codes(up_codes, up_scales, "up", F, K)
-    if h is None:
-        h = torch.empty((M, F), dtype=torch.bfloat16, device=x_codes.device)
-    ldh = _rows(h, "h", torch.bfloat16, (M, F))
     if (gate is None) != (up is None):
         raise ValueError("gate and up are given both or neither")
-    if gate is None and save:
-        both = torch.empty((M, 2 * F), dtype=torch.bfloat16, device=x_codes.device)
-        gate, up = both[:, :F], both[:, F:]
     ldgu = 0
     if gate is not None:
-        ldgu = _rows(gate, "gate", torch.bfloat16, (M, F))
-        if _rows(up, "up", torch.bfloat16, (M, F)) != ldgu:
+        ldgu = _rows(gate, "gate", bf16, (M, F))
+        if _rows(up, "up", bf16, (M, F)) != ldgu:
             raise ValueError("gate and up must have the same row stride")
+    elif save:
+        gate, up = x_codes.new_empty((M, 2 * F), dtype=bf16).split(F, 1)
+        ldgu = 2 * F
+    if h is None:
+        h, ldh = x_codes.new_empty((M, F), dtype=bf16), F
+    else:
+        ldh = _rows(h, "h", bf16, (M, F))
     _check(lib().fp4q_gemm_gated(M, F, K, _ptr(x_codes), _ptr(x_scales), _ptr(gate_codes),
                                  _ptr(gate_scales), _ptr(up_codes), _ptr(up_scales), act, _ptr(h),
                                  ldh, _ptr(gate), _ptr(up), ldgu, _stream(stream)))
@@ -646,34 +653,42 @@ def gemm_gated_grad(dy_codes, dy_scales, w_codes, w_scales, gate, up, act=SILU, 
     (fp4q_gemm_gated_grad): dy_codes [M, K/2], w_codes [F, K/2], gate and up
     bf16 [M, F] as gemm_gated returned them.  Returns (d_gate, d_up), bf16,
     the halves of one [M, 2F] tensor unless given."""
-    torch = _torch()
+    bf16 = _torch().bfloat16
     M, K = _codes(dy_codes, dy_scales, "dy")
     F, _ = _codes(w_codes, w_scales, "w", K=K)
-    ldgu = _rows(gate, "gate", torch.bfloat16, (M, F))
-    if _rows(up, "up", torch.bfloat16, (M, F)) != ldgu:
+    ldgu = _rows(gate, "gate", bf16, (M, F))
+    if _rows(up, "up", bf16, (M, F)) != ldgu:
         raise ValueError("gate and up must have the same row stride")
     if (d_gate is None) != (d_up is None):
         raise ValueError("d_gate and d_up are given both or neither")
     if d_gate is None:
-        both = torch.empty((M, 2 * F), dtype=torch.bfloat16, device=dy_codes.device)
-        d_gate, d_up = both[:, :F], both[:, F:]
-    ldd = _rows(d_gate, "d_gate", torch.bfloat16, (M, F))
-    if _rows(d_up, "d_up", torch.bfloat16, (M, F)) != ldd:
-        raise ValueError("d_gate and d_up must have the same row stride")
+        d_gate, d_up = dy_codes.new_empty((M, 2 * F), dtype=bf16).split(F, 1)
+        ldd = 2 * F
+    else:
+        ldd = _rows(d_gate, "d_gate", bf16, (M, F))
+        if _rows(d_up, "d_up", bf16, (M, F)) != ldd:
+            raise ValueError("d_gate and d_up must have the same row stride")
     _check(lib().fp4q_gemm_gated_grad(M, F, K, _ptr(dy_codes), _ptr(dy_scales), _ptr(w_codes),
                                       _ptr(w_scales), act, _ptr(gate), _ptr(up), ldgu,
                                       _ptr(d_gate), _ptr(d_up), ldd, _stream(stream)))
     return d_gate, d_up
 
 
+def _vec(t, name, dtype, n):
+    """Checks a contiguous device vector of n elements (dtype None: any)."""
+    if not t.is_cuda:
+        _need_cuda(t)
+    _need(t, name, t.dtype if dtype is None else dtype, (n,))
+
+
 def _affine(weight, bias, cols):
     """Dtype code of the norm's weight and bias vectors."""
-    for t, name in ((weight, "weight"), (bias, "bias")):
-        if t is not None:
-            _need_cuda(t)
-            _need(t, name, t.dtype, (cols,))
-    if weight is not None and bias is not None and weight.dtype != bias.dtype:
-        raise TypeError("weight and bias must have the same dtype")
+    if weight is not None:
+        _vec(weight, "weight", None, cols)
+    if bias is not None:
+        _vec(bias, "bias", None, cols)
+        if weight is not None and weight.dtype != bias.dtype:
+            raise TypeError("weight and bias must have the same dtype")
     t = weight if weight is not None else bias
     return F32 if t is None else _dt(t)
 
@@ -684,25 +699,30 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, kind=LAYER_NORM, y=None, out
     (y, mean, rstd): y of out_dtype (x's by default), mean and rstd fp32 per
     row for layer_norm_grad (mean None for RMS_NORM, both None without
     stats)."""
-    torch = _torch()
+    f32 = _torch().float32
     ldx = _rows(x, "x")
     R, C = x.shape
+    xdt = ydt = _dt(x)
     wdt = _affine(weight, bias, C)
     if y is None:
-        y = torch.empty((R, C), dtype=x.dtype if out_dtype is None else out_dtype, device=x.device)
-    ldy = _rows(y, "y", shape=(R, C))
-    if stats:
-        if mean is None and kind == LAYER_NORM:
-            mean = torch.empty((R,), dtype=torch.float32, device=x.device)
-        if rstd is None:
-            rstd = torch.empty((R,), dtype=torch.float32, device=x.device)
-    for t, name in ((mean, "mean"), (rstd, "rstd")):
-        if t is not None:
-            _need_cuda(t)
-            _need(t, name, torch.float32, (R,))
-    _check(lib().fp4q_layer_norm(kind, _ptr(x), _dt(x), R, C, ldx, _ptr(weight), _ptr(bias), wdt,
-                                 eps, _ptr(y), _dt(y), ldy, _ptr(mean), _ptr(rstd),
-                                 _stream(stream)))
+        ldy = C
+        if out_dtype is None:
+            y = x.new_empty((R, C))
+        else:
+            y = x.new_empty((R, C), dtype=out_dtype)
+            ydt = _dt(y)
+    else:
+        ldy, ydt = _rows(y, "y", shape=(R, C)), _dt(y)
+    if mean is not None:
+        _vec(mean, "mean", f32, R)
+    elif stats and kind == LAYER_NORM:
+        mean = x.new_empty((R,), dtype=f32)
+    if rstd is not None:
+        _vec(rstd, "rstd", f32, R)
+    elif stats:
+        rstd = x.new_empty((R,), dtype=f32)
+    _check(lib().fp4q_layer_norm(kind, _ptr(x), xdt, R, C, ldx, _ptr(weight), _ptr(bias), wdt, eps,
+                                 _ptr(y), ydt, ldy, _ptr(mean), _ptr(rstd), _stream(stream)))
     return y, mean, rstd
 
 
@@ -715,28 +735,34 @@ def layer_norm_grad(dy, x, weight, mean, rstd, kind=LAYER_NORM, dx=None, want_we
     """Backward pass of layer_norm (fp4q_layer_norm_grad).  Returns (dx,
     dweight, dbias): dx of x's dtype, the others fp32 (None where not
     wanted)."""
-    torch = _torch()
+    f32 = _torch().float32
     ldx = _rows(x, "x")
     R, C = x.shape
     lddy = _rows(dy, "dy", shape=(R, C))
     wdt = _affine(weight, None, C)
     if dx is None:
-        dx = torch.empty((R, C), dtype=x.dtype, device=x.device)
-    lddx = _rows(dx, "dx", x.dtype, (R, C))
-    if dweight is None and want_weight:
-        dweight = torch.empty((C,), dtype=torch.float32, device=x.device)
-    if dbias is None and want_bias:
-        dbias = torch.empty((C,), dtype=torch.float32, device=x.device)
-    for t, name, n in ((mean, "mean", R), (rstd, "rstd", R), (dweight, "dweight", C),
-                       (dbias, "dbias", C)):
-        if t is not None:
-            _need_cuda(t)
-            _need(t, name, torch.float32, (n,))
+        dx, lddx = x.new_empty((R, C)), C
+    else:
+        lddx = _rows(dx, "dx", x.dtype, (R, C))
+    if mean is not None:
+        _vec(mean, "mean", f32, R)
+    if rstd is not None:
+        _vec(rstd, "rstd", f32, R)
+    if dweight is not None:
+        _vec(dweight, "dweight", f32, C)
+    elif want_weight:
+        dweight = x.new_empty((C,), dtype=f32)
+    if dbias is not None:
+        _vec(dbias, "dbias", f32, C)
+    elif want_bias:
+        dbias = x.new_empty((C,), dtype=f32)
     nbytes = 0
     if dweight is not None or dbias is not None:
         if workspace is None:
-            workspace = _scratch(layer_norm_grad_workspace_bytes(R, C), x.device, stream)
-        nbytes = workspace.numel() * workspace.element_size()
+            nbytes = layer_norm_grad_workspace_bytes(R, C)
+            workspace = _scratch(nbytes, x.device, stream)
+        else:
+            nbytes = workspace.numel() * workspace.element_size()
     _check(lib().fp4q_layer_norm_grad(kind, _ptr(dy), _dt(dy), lddy, _ptr(x), _dt(x), R, C, ldx,
                                       _ptr(weight), wdt, _ptr(mean), _ptr(rstd), _ptr(dx), lddx,
                                       _ptr(dweight), _ptr(dbias), _ptr(workspace), nbytes,

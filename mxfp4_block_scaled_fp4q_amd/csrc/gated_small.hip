@@ -61,8 +61,8 @@ __global__ __launch_bounds__(64 * KS) void gated_small_kernel(const GatedCall g,
             const int i = p * 64 * KS + threadIdx.x;
             const int row = m0 + i / (2 * NT), col = n0 + i % (2 * NT) * 8;
             if (i < GROUPS && row < g.M && col < g.F) {
-                gin[p] = load8<0>(g.gate + row * g.ldgu, col, g.F);
-                uin[p] = load8<0>(g.up + row * g.ldgu, col, g.F);
+                gin[p] = load8(g.gate + row * g.ldgu, col, g.F);
+                uin[p] = load8(g.up + row * g.ldgu, col, g.F);
             }
         }
     }
