@@ -42,6 +42,15 @@
 
 namespace fp4q {
 
+// Pointers that come from memory are generic to the compiler, and generic
+// accesses wait on the LDS counter too: global<T>(p) is p in global memory.
+template <class T>
+using Global = T __attribute__((address_space(1))) *;
+template <class T>
+__device__ __forceinline__ Global<T> global(const void* p) {
+    return (Global<T>)p;
+}
+
 constexpr int kTensors = 44;     // descriptors per launch: 4 KB of kernel arguments
 constexpr int kChunk = 4096;     // elements per workgroup
 constexpr int kMaxGroups = 1 << 23;  // workgroups per launch: 2^31 threads
@@ -128,7 +137,7 @@ __device__ __forceinline__ void encode8(const float (&m1)[8], const float (&r1)[
 
 template <int GB>
 __device__ __forceinline__ float grad1(const void* g, int64_t i) {
-    return GB ? as_f32((uint32_t)((const uint16_t*)g)[i] << 16) : ((const float*)g)[i];
+    return GB ? as_f32((uint32_t)global<const uint16_t>(g)[i] << 16) : global<const float>(g)[i];
 }
 __device__ __forceinline__ uint32_t pack_copy(float lo, float hi) {
     const bf16x2_t q = {(__bf16)lo, (__bf16)hi};  // v_cvt_pk_bf16_f32
@@ -141,11 +150,11 @@ struct Grad4 {
     u32x4 w;
     __device__ __forceinline__ void load(const void* g, int64_t i) {
         if (GB) {
-            const u32x2 v = __builtin_nontemporal_load((const u32x2*)((const uint16_t*)g + i));
+            const u32x2 v = __builtin_nontemporal_load(global<const u32x2>((const uint16_t*)g + i));
             w.x = v.x;
             w.y = v.y;
         } else {
-            w = __builtin_nontemporal_load((const u32x4*)((const float*)g + i));
+            w = __builtin_nontemporal_load(global<const u32x4>((const float*)g + i));
         }
     }
     __device__ __forceinline__ float at(int e) const {
@@ -159,8 +168,8 @@ template <int GB>
 __device__ __forceinline__ void chunk32(const AdamwScalars& a, const AdamwArg& d, int64_t i0,
                                         float gscale, float decay) {
     constexpr int U = kChunk / 1024;
-    float* dm = (float*)d.m;
-    float* dv = (float*)d.v;
+    const Global<float> dp = global<float>(d.p), dm = global<float>(d.m), dv = global<float>(d.v);
+    const Global<uint16_t> dc = global<uint16_t>(d.copy);
     const int64_t i = i0 + threadIdx.x * 4;
     const bool whole = i0 + kChunk <= d.n;
     u32x4 p[U], m[U], v[U];
@@ -169,10 +178,10 @@ __device__ __forceinline__ void chunk32(const AdamwScalars& a, const AdamwArg& d
     for (int k = 0; k < U; ++k) {
         const int64_t j = i + k * 1024;
         if (!whole && j + 4 > d.n) continue;
-        p[k] = __builtin_nontemporal_load((const u32x4*)(d.p + j));
+        p[k] = __builtin_nontemporal_load((Global<const u32x4>)(dp + j));
         g[k].load(d.g, j);
-        m[k] = __builtin_nontemporal_load((const u32x4*)(dm + j));
-        v[k] = __builtin_nontemporal_load((const u32x4*)(dv + j));
+        m[k] = __builtin_nontemporal_load((Global<const u32x4>)(dm + j));
+        v[k] = __builtin_nontemporal_load((Global<const u32x4>)(dv + j));
     }
 #pragma unroll
     for (int k = 0; k < U; ++k) {
@@ -188,20 +197,20 @@ __device__ __forceinline__ void chunk32(const AdamwScalars& a, const AdamwArg& d
             m[k][e] = as_u32(m1);
             v[k][e] = as_u32(v1);
         }
-        __builtin_nontemporal_store(p[k], (u32x4*)(d.p + j));
-        __builtin_nontemporal_store(m[k], (u32x4*)(dm + j));
-        __builtin_nontemporal_store(v[k], (u32x4*)(dv + j));
-        if (d.copy)
-            *(u32x2*)(d.copy + j) = (u32x2){pack_copy(p1[0], p1[1]), pack_copy(p1[2], p1[3])};
+        __builtin_nontemporal_store(p[k], (Global<u32x4>)(dp + j));
+        __builtin_nontemporal_store(m[k], (Global<u32x4>)(dm + j));
+        __builtin_nontemporal_store(v[k], (Global<u32x4>)(dv + j));
+        if (dc)
+            *(Global<u32x2>)(dc + j) = (u32x2){pack_copy(p1[0], p1[1]), pack_copy(p1[2], p1[3])};
     }
     const int64_t j = (d.n & ~(int64_t)3) + threadIdx.x;  // what is left past the vectors
     if (whole || j >= d.n) return;
     float m1, v1, r1;
-    const float p1 = adamw_one(a, d.p[j], grad1<GB>(d.g, j) * gscale, dm[j], dv[j], decay, m1, v1, r1);
-    d.p[j] = p1;
+    const float p1 = adamw_one(a, dp[j], grad1<GB>(d.g, j) * gscale, dm[j], dv[j], decay, m1, v1, r1);
+    dp[j] = p1;
     dm[j] = m1;
     dv[j] = v1;
-    if (d.copy) d.copy[j] = (uint16_t)f32_to_bf16_bits(p1);
+    if (dc) dc[j] = (uint16_t)f32_to_bf16_bits(p1);
 }
 
 // The same with 8-bit moments: 8 elements per lane, 2048 at a time.
@@ -210,8 +219,10 @@ __device__ __forceinline__ void chunk8(const AdamwScalars& a, const AdamwArg& d,
                                        float gscale, float decay) {
     constexpr int U = kChunk / 2048;
     const int64_t i = i0 + threadIdx.x * 8;
-    uint8_t* dm = (uint8_t*)d.m;
-    uint8_t* dv = (uint8_t*)d.v;
+    const Global<float> dp = global<float>(d.p);
+    const Global<uint8_t> dm = global<uint8_t>(d.m), dv = global<uint8_t>(d.v);
+    const Global<uint8_t> dms = global<uint8_t>(d.ms), dvs = global<uint8_t>(d.vs);
+    const Global<uint16_t> dc = global<uint16_t>(d.copy);
     const bool whole = i0 + kChunk <= d.n;
     u32x4 p[U][2];
     Grad4<GB> g[U][2];
@@ -223,30 +234,30 @@ __device__ __forceinline__ void chunk8(const AdamwScalars& a, const AdamwArg& d,
         if (whole || j + 8 <= d.n) {
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                p[k][q] = __builtin_nontemporal_load((const u32x4*)(d.p + j + 4 * q));
+                p[k][q] = __builtin_nontemporal_load((Global<const u32x4>)(dp + j + 4 * q));
                 g[k][q].load(d.g, j + 4 * q);
             }
-            m[k] = __builtin_nontemporal_load((const u32x2*)(dm + j));
-            v[k] = __builtin_nontemporal_load((const u32x2*)(dv + j));
+            m[k] = __builtin_nontemporal_load((Global<const u32x2>)(dm + j));
+            v[k] = __builtin_nontemporal_load((Global<const u32x2>)(dv + j));
         } else {  // past the end: zeros, which leave zero moments
             p[k][0] = p[k][1] = g[k][0].w = g[k][1].w = (u32x4){0u, 0u, 0u, 0u};
             m[k] = v[k] = (u32x2){0u, 0u};
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 if (j + e >= d.n) continue;
-                p[k][e >> 2][e & 3] = as_u32(d.p[j + e]);
+                p[k][e >> 2][e & 3] = as_u32(dp[j + e]);
                 if (GB)
-                    g[k][e >> 2].w[(e >> 1) & 1] |= (uint32_t)((const uint16_t*)d.g)[j + e]
+                    g[k][e >> 2].w[(e >> 1) & 1] |= (uint32_t)global<const uint16_t>(d.g)[j + e]
                                                     << (16 * (e & 1));
                 else
-                    g[k][e >> 2].w[e & 3] = ((const uint32_t*)d.g)[j + e];
+                    g[k][e >> 2].w[e & 3] = global<const uint32_t>(d.g)[j + e];
                 m[k][e >> 2] |= (uint32_t)dm[j + e] << (8 * (e & 3));
                 v[k][e >> 2] |= (uint32_t)dv[j + e] << (8 * (e & 3));
             }
         }
         const bool any = whole || j < d.n;
-        sm[k] = any ? e8m0_scale_f32(d.ms[j >> 5]) : 0.0f;
-        sv[k] = any ? e8m0_scale_f32(d.vs[j >> 5]) : 0.0f;
+        sm[k] = any ? e8m0_scale_f32(dms[j >> 5]) : 0.0f;
+        sv[k] = any ? e8m0_scale_f32(dvs[j >> 5]) : 0.0f;
     }
 #pragma unroll
     for (int k = 0; k < U; ++k) {
@@ -279,25 +290,25 @@ __device__ __forceinline__ void chunk8(const AdamwScalars& a, const AdamwArg& d,
                 __builtin_nontemporal_store(
                     (u32x4){as_u32(p1[4 * q]), as_u32(p1[4 * q + 1]), as_u32(p1[4 * q + 2]),
                             as_u32(p1[4 * q + 3])},
-                    (u32x4*)(d.p + j + 4 * q));
-            __builtin_nontemporal_store(cm, (u32x2*)(dm + j));
-            __builtin_nontemporal_store(cr, (u32x2*)(dv + j));
-            if (d.copy)
-                *(u32x4*)(d.copy + j) = (u32x4){pack_copy(p1[0], p1[1]), pack_copy(p1[2], p1[3]),
+                    (Global<u32x4>)(dp + j + 4 * q));
+            __builtin_nontemporal_store(cm, (Global<u32x2>)(dm + j));
+            __builtin_nontemporal_store(cr, (Global<u32x2>)(dv + j));
+            if (dc)
+                *(Global<u32x4>)(dc + j) = (u32x4){pack_copy(p1[0], p1[1]), pack_copy(p1[2], p1[3]),
                                                 pack_copy(p1[4], p1[5]), pack_copy(p1[6], p1[7])};
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 if (j + e >= d.n) continue;
-                d.p[j + e] = p1[e];
+                dp[j + e] = p1[e];
                 dm[j + e] = (uint8_t)(cm[e >> 2] >> (8 * (e & 3)));
                 dv[j + e] = (uint8_t)(cr[e >> 2] >> (8 * (e & 3)));
-                if (d.copy) d.copy[j + e] = (uint16_t)f32_to_bf16_bits(p1[e]);
+                if (dc) dc[j + e] = (uint16_t)f32_to_bf16_bits(p1[e]);
             }
         }
         if ((threadIdx.x & 3) == 0 && (whole || j < d.n)) {
-            d.ms[j >> 5] = (uint8_t)bm;
-            d.vs[j >> 5] = (uint8_t)br;
+            dms[j >> 5] = (uint8_t)bm;
+            dvs[j >> 5] = (uint8_t)br;
         }
     }
 }

@@ -118,13 +118,13 @@ __device__ __forceinline__ float dpp_add(float v) {
 __device__ __forceinline__ float sum16(float v) {
     return dpp_add<0x140>(dpp_add<0x141>(dpp_add<0x4E>(dpp_add<0xB1>(v))));
 }
-__device__ __forceinline__ float wave_sum(float v) {
-    v = sum16(v);
+__device__ __forceinline__ float rows_sum(float v) {  // over the four rows, lane by lane
     const auto a = __builtin_amdgcn_permlane16_swap(as_u32(v), as_u32(v), false, false);
     v = as_f32(a[0]) + as_f32(a[1]);
     const auto b = __builtin_amdgcn_permlane32_swap(as_u32(v), as_u32(v), false, false);
     return as_f32(b[0]) + as_f32(b[1]);
 }
+__device__ __forceinline__ float wave_sum(float v) { return rows_sum(sum16(v)); }
 
 // Sums of N values over the waves that share a row (W of them, at most 16), in
 // every lane.  `red` holds two sets of N * 16 floats that take turns, so one
@@ -392,30 +392,30 @@ __global__ __launch_bounds__(MULTI ? 1024 : 256) void norm_grad_kernel(
     }
 }
 
-// Adds up the rows of partial sums: 64 columns per workgroup, sixteen waves
-// over the rows, then their sums in LDS.
+// Adds up the rows of partial sums: 16 columns per workgroup, 64 groups of 16
+// lanes over the rows, so that few loads follow each other.
 __global__ __launch_bounds__(1024) void norm_grad_join_kernel(const float* __restrict__ part,
                                                               int64_t cols, int slabs,
                                                               float* __restrict__ dw,
                                                               float* __restrict__ db) {
-    __shared__ float red[16][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    __shared__ float red[16][16];
     float* out = blockIdx.y == 0 ? dw : db;
     if (!out) return;
-    const int64_t c = (int64_t)blockIdx.x * 64 + lane;
+    const int l = threadIdx.x & 15, wave = threadIdx.x >> 6;
+    const int64_t c = (int64_t)blockIdx.x * 16 + l;
     float s = 0.0f;
     if (c < cols) {
         const float* p = part + blockIdx.y * cols + c;
 #pragma unroll 8
-        for (int i = wave; i < slabs; i += 16) s += p[(int64_t)i * 2 * cols];
+        for (int i = threadIdx.x >> 4; i < slabs; i += 64) s += p[(int64_t)i * 2 * cols];
     }
-    red[wave][lane] = s;
+    s = rows_sum(s);
+    if ((threadIdx.x & 63) < 16) red[wave][l] = s;
     __syncthreads();
-    if (wave || c >= cols) return;
-    s = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) s += red[i][lane];
-    out[c] = s;
+    if (wave) return;
+    const int r = threadIdx.x >> 4;
+    s = rows_sum((red[r][l] + red[4 + r][l]) + (red[8 + r][l] + red[12 + r][l]));
+    if (threadIdx.x < 16 && c < cols) out[c] = s;
 }
 
 // Rows below 8 columns, or too long for the registers: 256 threads walk over
@@ -521,7 +521,13 @@ constexpr int64_t kAnyGrid = 1 << 16;
 
 // Workgroups of a walk over the rows: what 256 compute units hold of them at
 // `waves` waves each, and at least `min_rows` rows to a workgroup (or to each
-// of its four waves).
+// of its four waves).  Forward, 16, 24 and 32 waves: 16384 x 5120 bf16 118, 80
+// and 85 us (ten waves per row: 16 is one workgroup), fp32 119, 126 and 146.
+// Backward, 16, 24 and 32: 100, 101 and 116 us.  There each row of a walk costs
+// about 1.2 us and each workgroup a row of partial sums: 2, 4, 8, 16 rows
+// take 7.7, 8.8, 10.7, 15.6 us at 300 x 2048, 17.9, 14.8, 16.6, 24.2 at 1999 x
+// 1111 and 29.4, 29.3, 29.5, 26.7 at 8192 x 2048.
+constexpr int kNormWaves = 24, kGradWaves = 16;
 static int norm_groups(const NormShape& sh, int64_t rows, int waves, int min_rows) {
     const int64_t per = (int64_t)min_rows * (sh.multi ? 1 : 4);
     return (int)std::min<int64_t>(256 * (waves * 64 / sh.threads), (rows + per - 1) / per);
@@ -529,7 +535,7 @@ static int norm_groups(const NormShape& sh, int64_t rows, int waves, int min_row
 static int norm_slabs(int64_t rows, int64_t cols) {
     const NormShape sh = norm_shape(rows, cols);
     if (sh.nv == 0) return (int)std::min<int64_t>(128, (rows + 63) / 64);
-    return norm_groups(sh, rows, 16, 8);
+    return norm_groups(sh, rows, kGradWaves, rows <= 512 ? 2 : rows <= 4096 ? 4 : sh.multi ? 16 : 8);
 }
 
 size_t norm_grad_workspace_bytes(int64_t rows, int64_t cols) {
@@ -542,7 +548,7 @@ static void go_norm(const NormShape sh, const void* x, int64_t rows, int64_t col
                     float* mean, float* rstd, hipStream_t s) {
 #define FP4Q_GO(MULTI, NV)                                                                        \
     if (sh.multi == (bool)MULTI && sh.nv == NV)                                                   \
-    FP4Q_LAUNCH((norm_kernel<XB, YB, MULTI, NV>), dim3((unsigned)norm_groups(sh, rows, 32, 1)),   \
+    FP4Q_LAUNCH((norm_kernel<XB, YB, MULTI, NV>), dim3((unsigned)norm_groups(sh, rows, kNormWaves, 1)),   \
                 dim3((unsigned)sh.threads), 0, s, x, rows, (int)cols, ldx, w, b, wb, eps, rms, y, \
                 ldy, mean, rstd)
     FP4Q_GO(0, 1);
@@ -602,7 +608,7 @@ static void go_grad(const NormShape sh, const void* dy, int64_t lddy, const void
         if (slabs == 1) return;
     }
     if (dw || db)
-        FP4Q_LAUNCH(norm_grad_join_kernel, dim3((unsigned)((cols + 63) / 64), 2), dim3(1024), 0, s,
+        FP4Q_LAUNCH(norm_grad_join_kernel, dim3((unsigned)((cols + 15) / 16), 2), dim3(1024), 0, s,
                     part, cols, slabs, dw, db);
 }
 
