@@ -10,11 +10,12 @@
 // in registers from its load to its last use, in chunks of 8 elements per
 // lane; the sums run over lanes, and over waves through LDS, in fp32, and the
 // squares are summed around the mean that is already known.  A workgroup
-// walks over rows and loads the next row before it works on the present one;
-// the weight and bias stay in registers, and in the backward pass the lane's
-// partial column sums do too, so dw and db cost no second read of x and dy:
-// each workgroup leaves one row of partial sums, which a second, small kernel
-// adds up.  No atomics: the order of every sum is fixed by the sizes.
+// walks over rows and loads the next row (short rows: the next two) before it
+// works on the present one; the weight and bias stay in registers, and in the
+// backward pass the lane's partial column sums do too, so dw and db cost no
+// second read of x and dy: each workgroup leaves one row of partial sums,
+// which a second, small kernel adds up.  No atomics: the order of every sum is
+// fixed by the sizes.
 //
 // A row's last chunk, where 8 does not divide C, is read 8 elements wide from
 // C - 8; its first elements belong to the chunk before it and are left out of
@@ -147,26 +148,38 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float* red, int W, int& 
 }
 
 // A row is held by one wave (MULTI = 0; 256 threads work on four rows) or by
-// all W waves of its workgroup, NV chunks per lane.  Chunks below kl are whole
-// in every lane; chunk kl, the row's last, begins at `tail` in this lane and
-// its first `skip` elements are the chunk's before it (8: nothing here).
+// all W waves of its workgroup, NV chunks per lane.  The last chunk begins at
+// `tail` in this lane and its first `skip` elements are another lane's; a lane
+// past the row's end holds that row's last chunk again, with skip = 8.
+//
+// Every lane loads and stores all its chunks, and past the last row loads that
+// row again: a load or store under a condition would leave the compiler not
+// knowing how many are in flight, and it would wait for the rows ahead too.
+// Elements that two lanes hold are stored by both, with the same bits.
+template <int NV>
 struct Place {
-    int W, t, step, kl, tail, skip;
+    int W, t, step, tail, skip;
     template <int MULTI>
     __device__ __forceinline__ static Place make(int cols) {
         Place p;
         p.W = MULTI ? (int)(blockDim.x >> 6) : 1;
         p.t = (MULTI ? (int)threadIdx.x : (int)(threadIdx.x & 63)) * 8;
         p.step = p.W * 512;
-        p.kl = (cols - 1) / p.step;
-        const int c0 = p.kl * p.step + p.t;
+        const int c0 = (NV - 1) * p.step + p.t;
         p.tail = min(c0, cols - 8);
         p.skip = c0 < cols ? c0 - p.tail : 8;
         return p;
     }
-    __device__ __forceinline__ int start(int k) const { return k < kl ? k * step + t : tail; }
-    __device__ __forceinline__ bool has(int k) const { return k < kl || (k == kl && skip < 8); }
+    __device__ __forceinline__ int start(int k) const { return k < NV - 1 ? k * step + t : tail; }
+    __device__ __forceinline__ bool owns(int k, int e) const { return k < NV - 1 || e >= skip; }
 };
+
+// First row of this wave's (or workgroup's) walk, a scalar.
+template <int MULTI>
+__device__ __forceinline__ int64_t first_row() {
+    if (MULTI) return blockIdx.x;
+    return (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+}
 
 template <int XB, int YB, int MULTI, int NV>
 __global__ __launch_bounds__(MULTI ? 1024 : 256) void norm_kernel(
@@ -174,47 +187,51 @@ __global__ __launch_bounds__(MULTI ? 1024 : 256) void norm_kernel(
     const void* __restrict__ b, int wb, float eps, int rms, void* __restrict__ y, int64_t ldy,
     float* __restrict__ mean, float* __restrict__ rstd) {
     __shared__ float red[MULTI ? 2 * 16 : 1];
-    const Place pl = Place::make<MULTI>(cols);
+    const Place<NV> pl = Place<NV>::template make<MULTI>(cols);
     const int64_t step = MULTI ? gridDim.x : gridDim.x * 4;
-    int64_t r = MULTI ? blockIdx.x : blockIdx.x * 4 + (threadIdx.x >> 6);
+    int64_t r = first_row<MULTI>();
     if (r >= rows) return;  // whole waves, and whole workgroups where they share a row
     int turn = 0;
-    Chunk<XB> xn[NV] = {};
+    constexpr int AHEAD = NV == 1 ? 2 : 1;  // rows in flight
+    Chunk<XB> xr[AHEAD][NV];
+    auto fetch = [&](int64_t row, Chunk<XB>(&xn)[NV]) __attribute__((always_inline)) {
+        row = min(row, rows - 1);
 #pragma unroll
-    for (int k = 0; k < NV; ++k)
-        if (pl.has(k)) xn[k].load(x, r * ldx + pl.start(k));
+        for (int k = 0; k < NV; ++k) xn[k].load(x, row * ldx + pl.start(k));
+    };
+#pragma unroll
+    for (int a = 0; a < AHEAD; ++a) fetch(r + a * step, xr[a]);
     float wv[NV][8], bv[NV][8];
 #pragma unroll
-    for (int k = 0; k < NV; ++k)
-        if (pl.has(k)) {
-            load_vec8(w, wb, pl.start(k), 1.0f, wv[k]);
-            load_vec8(b, wb, pl.start(k), 0.0f, bv[k]);
-        }
+    for (int k = 0; k < NV; ++k) {
+        load_vec8(w, wb, pl.start(k), 1.0f, wv[k]);
+        load_vec8(b, wb, pl.start(k), 0.0f, bv[k]);
+    }
     const float n = (float)cols;
-    for (; r < rows; r += step) {
+    float mu = 0.0f, rs = 0.0f;
+    // the statistics of a row are stored ahead of the next row's loads
+    auto stats = [&](int64_t row) __attribute__((always_inline)) {
+        if (pl.t) return;
+        if (mean && !rms) mean[row] = mu;
+        if (rstd) rstd[row] = rs;
+    };
+    int64_t last = -1;
+    auto one = [&](int64_t r, Chunk<XB>(&xn)[NV]) __attribute__((always_inline)) {
         float xf[NV][8];
 #pragma unroll
         for (int k = 0; k < NV; ++k)
 #pragma unroll
             for (int e = 0; e < 8; ++e) xf[k][e] = xn[k].at(e);
-        if (r + step < rows) {
-#pragma unroll
-            for (int k = 0; k < NV; ++k)
-                if (pl.has(k)) xn[k].load(x, (r + step) * ldx + pl.start(k));
-        }
-        float mu = 0.0f;
+        if (last >= 0) stats(last);
+        last = r;
+        fetch(r + AHEAD * step, xn);
         if (!rms) {
             float s[1] = {0.0f};
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
                 float p = 0.0f;
-                if (k < pl.kl) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) p += xf[k][e];
-                } else if (k == pl.kl) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) p += e >= pl.skip ? xf[k][e] : 0.0f;
-                }
+                for (int e = 0; e < 8; ++e) p += pl.owns(k, e) ? xf[k][e] : 0.0f;
                 s[0] += p;
             }
             row_sums<MULTI>(s, red, pl.W, turn);
@@ -225,31 +242,28 @@ __global__ __launch_bounds__(MULTI ? 1024 : 256) void norm_kernel(
         for (int k = 0; k < NV; ++k) {
             float p = 0.0f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) xf[k][e] -= mu;
-            if (k < pl.kl) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) p += xf[k][e] * xf[k][e];
-            } else if (k == pl.kl) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) p += e >= pl.skip ? xf[k][e] * xf[k][e] : 0.0f;
+            for (int e = 0; e < 8; ++e) {
+                const float d = xf[k][e] -= mu;
+                p += pl.owns(k, e) ? d * d : 0.0f;
             }
             q[0] += p;
         }
         row_sums<MULTI>(q, red, pl.W, turn);
-        const float rs = 1.0f / sqrtf(q[0] / n + eps);
+        rs = 1.0f / sqrtf(q[0] / n + eps);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            if (!pl.has(k)) continue;
             float f[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) f[e] = (xf[k][e] * rs) * wv[k][e] + bv[k][e];
-            store_own<YB>(y, r * ldy + pl.start(k), f, k < pl.kl ? 0 : pl.skip);
+            store_chunk<YB>(y, r * ldy + pl.start(k), f);
         }
-        if (pl.t == 0) {
-            if (mean && !rms) mean[r] = mu;
-            if (rstd) rstd[r] = rs;
-        }
+    };
+    for (; r < rows; r += AHEAD * step) {
+#pragma unroll
+        for (int a = 0; a < AHEAD; ++a)
+            if (a == 0 || r + a * step < rows) one(r + a * step, xr[a]);
     }
+    stats(last);
 }
 
 // dw and db (or either, or neither, null) get this workgroup's column sums:
@@ -265,13 +279,18 @@ __global__ __launch_bounds__(MULTI ? 1024 : 256) void norm_grad_kernel(
     constexpr bool kLds = MULTI && NV == 2;
     __shared__ __attribute__((aligned(16))) float red[MULTI ? 4 * 16 : 4 * 512];
     __shared__ u32x4 sums[kLds ? 2 * 2 * NV * 1024 : 1];
-    const Place pl = Place::make<MULTI>(cols);
+    const Place<NV> pl = Place<NV>::template make<MULTI>(cols);
     const int64_t step = MULTI ? gridDim.x : gridDim.x * 4;
-    int64_t r = MULTI ? blockIdx.x : blockIdx.x * 4 + (threadIdx.x >> 6);
+    int64_t r = first_row<MULTI>();
     int turn = 0;
-    Chunk<XB> xn[NV] = {};
-    Chunk<DB> dn[NV] = {};
-    float wv[NV][8] = {}, aw[NV][8] = {}, ab[NV][8] = {};
+    constexpr int AHEAD = NV == 1 ? 2 : 1;
+    struct Row {
+        Chunk<XB> x[NV];
+        Chunk<DB> d[NV];
+        float mu, rs;
+    };
+    Row in[AHEAD];
+    float wv[NV][8], aw[NV][8] = {}, ab[NV][8] = {};
     // this lane's sums of chunk k in LDS, half h of dw's (o = 0) or db's eight
     auto slot = [&](int o, int k, int h) __attribute__((always_inline)) -> u32x4& {
         return sums[((o * NV + k) * 2 + h) * 1024 + threadIdx.x];
@@ -280,61 +299,63 @@ __global__ __launch_bounds__(MULTI ? 1024 : 256) void norm_grad_kernel(
 #pragma unroll
         for (int i = 0; i < 4 * NV; ++i) slot(i >> 2, (i >> 1) & 1, i & 1) = (u32x4){0u, 0u, 0u, 0u};
     }
-    float mun = 0.0f, rsn = 0.0f;
-    auto fetch = [&](int64_t row) __attribute__((always_inline)) {
-        if (row >= rows) return;
-        if (!rms) mun = mean[row];
-        rsn = rstd[row];
+    auto fetch = [&](int64_t row, Row& n) __attribute__((always_inline)) {
+        row = min(row, rows - 1);
+        n.mu = rms ? 0.0f : mean[row];
+        n.rs = rstd[row];
 #pragma unroll
-        for (int k = 0; k < NV; ++k)
-            if (pl.has(k)) {
-                xn[k].load(x, row * ldx + pl.start(k));
-                dn[k].load(dy, row * lddy + pl.start(k));
-            }
+        for (int k = 0; k < NV; ++k) {
+            n.x[k].load(x, row * ldx + pl.start(k));
+            n.d[k].load(dy, row * lddy + pl.start(k));
+        }
     };
-    fetch(r);
+#pragma unroll
+    for (int a = 0; a < AHEAD; ++a) fetch(r + a * step, in[a]);
 #pragma unroll
     for (int k = 0; k < NV; ++k)
-        if (pl.has(k)) load_vec8(w, wb, pl.start(k), 1.0f, wv[k]);
+        load_vec8(w, wb, pl.start(k), 1.0f, wv[k]);
     const float n = (float)cols;
-    for (; r < rows; r += step) {
-        const float mu = mun, rs = rsn;
+    auto one = [&](int64_t r, Row& now) __attribute__((always_inline)) {
+        const float mu = now.mu, rs = now.rs;
         float xh[NV][8], d[NV][8];
 #pragma unroll
         for (int k = 0; k < NV; ++k)
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                xh[k][e] = (xn[k].at(e) - mu) * rs;
-                // zero for elements that are another chunk's, so no sum holds them twice
-                d[k][e] = k < pl.kl || e >= pl.skip ? dn[k].at(e) : 0.0f;
+                xh[k][e] = (now.x[k].at(e) - mu) * rs;
+                d[k][e] = now.d[k].at(e);
             }
-        fetch(r + step);
+        fetch(r + AHEAD * step, now);
         float s[2] = {0.0f, 0.0f};  // of t xh, and of t
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             float p0 = 0.0f, p1 = 0.0f;
+            float own[8];  // zero for elements that are another lane's: no sum holds them twice
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                if (!kLds) {
-                    aw[k][e] += d[k][e] * xh[k][e];
-                    ab[k][e] += d[k][e];
-                } else if ((e & 3) == 3) {
-                    u32x4 &sw = slot(0, k, e >> 2), &sb = slot(1, k, e >> 2), vw = sw, vb = sb;
+            for (int e = 0; e < 8; ++e) own[e] = pl.owns(k, e) ? d[k][e] : 0.0f;
+            if (kLds) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    u32x4 vw = slot(0, k, h), vb = slot(1, k, h);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float g = d[k][e - 3 + i];
-                        vw[i] = as_u32(as_f32(vw[i]) + g * xh[k][e - 3 + i]);
-                        vb[i] = as_u32(as_f32(vb[i]) + g);
+                        vw[i] = as_u32(as_f32(vw[i]) + own[4 * h + i] * xh[k][4 * h + i]);
+                        vb[i] = as_u32(as_f32(vb[i]) + own[4 * h + i]);
                     }
-                    sw = vw;
-                    sb = vb;
+                    slot(0, k, h) = vw;
+                    slot(1, k, h) = vb;
                 }
             }
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
+                if (!kLds) {
+                    aw[k][e] += own[e] * xh[k][e];
+                    ab[k][e] += own[e];
+                }
+                own[e] *= wv[k][e];
+                p0 += own[e] * xh[k][e];
+                p1 += own[e];
                 d[k][e] *= wv[k][e];
-                p0 += d[k][e] * xh[k][e];
-                p1 += d[k][e];
             }
             s[0] += p0;
             s[1] += p1;
@@ -343,12 +364,16 @@ __global__ __launch_bounds__(MULTI ? 1024 : 256) void norm_grad_kernel(
         const float mx = s[0] / n, mt = rms ? 0.0f : s[1] / n;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            if (!pl.has(k)) continue;
             float f[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) f[e] = rs * (d[k][e] - mt - xh[k][e] * mx);
-            store_own<XB>(dx, r * lddx + pl.start(k), f, k < pl.kl ? 0 : pl.skip);
+            store_chunk<XB>(dx, r * lddx + pl.start(k), f);
         }
+    };
+    for (; r < rows; r += AHEAD * step) {
+#pragma unroll
+        for (int a = 0; a < AHEAD; ++a)
+            if (a == 0 || r + a * step < rows) one(r + a * step, in[a]);
     }
 #pragma unroll
     for (int o = 0; o < 2; ++o) {
@@ -357,13 +382,12 @@ __global__ __launch_bounds__(MULTI ? 1024 : 256) void norm_grad_kernel(
         out += blockIdx.x * part_stride;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            if (k > pl.kl) continue;
             float(&a)[8] = o == 0 ? aw[k] : ab[k];
             if (kLds) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) a[e] = as_f32(slot(o, k, e >> 2)[e & 3]);
             }
-            const int skip = k < pl.kl ? 0 : pl.skip, c = pl.start(k);
+            const int skip = k < NV - 1 ? 0 : pl.skip, c = pl.start(k);
             if (MULTI) {
                 store_own<0>(out, c, a, skip);
                 continue;
