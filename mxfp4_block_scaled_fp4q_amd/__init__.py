@@ -141,10 +141,10 @@ def _ptr(t):
 
 
 def _dt(t):
-    torch = _torch()
-    if t.dtype == torch.bfloat16:
+    torch = _torch_module or _torch()
+    if t.dtype is torch.bfloat16:
         return BF16
-    if t.dtype == torch.float32:
+    if t.dtype is torch.float32:
         return F32
     raise TypeError(f"libfp4q takes bf16 or fp32 tensors, got {t.dtype}")
 
@@ -587,11 +587,13 @@ def occ_spmm(row_ptr, col_idx, vals, w, y, stream=None):
 def _rows(t, name, dtype=None, shape=None):
     """Row stride of a 2-D device tensor with unit column stride (the stride
     of a single row, or of columns one element wide, is free)."""
-    if not t.is_cuda:
-        _need_cuda(t)
+    size = t.shape
+    if (t.is_cuda and len(size) == 2 and t.is_contiguous() and (dtype is None or t.dtype is dtype)
+            and (shape is None or size == shape)):
+        return size[1]
+    _need_cuda(t)
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    size = t.shape
     if shape is not None and size != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(size)}")
     if len(size) != 2 or (t.stride(1) != 1 and size[1] != 1):
@@ -602,17 +604,20 @@ def _rows(t, name, dtype=None, shape=None):
 def _codes(codes, scales, name, rows=None, K=None):
     """Checks one K-major block-32 operand; returns its rows and K."""
     u8, size = _torch().uint8, codes.shape
-    if not (codes.is_cuda and scales.is_cuda):
-        _need_cuda(codes, scales)
+    if len(size) == 2:
+        if rows is None:
+            rows = size[0]
+        if K is None:
+            K = 2 * size[1]
+        if (codes.dtype is u8 and scales.dtype is u8 and size == (rows, K // 2)
+                and scales.shape == (rows, K // 32) and codes.is_contiguous()
+                and scales.is_contiguous() and codes.is_cuda and scales.is_cuda):
+            return rows, K
+    _need_cuda(codes, scales)  # one of these says what is wrong
     if len(size) != 2:
         raise ValueError(f"{name}_codes must be 2-D")
-    rows = size[0] if rows is None else rows
-    K = 2 * size[1] if K is None else K
-    if (codes.dtype != u8 or scales.dtype != u8 or size != (rows, K // 2)
-            or scales.shape != (rows, K // 32) or not codes.is_contiguous()
-            or not scales.is_contiguous()):
-        _need(codes, f"{name}_codes", u8, (rows, K // 2))  # one of these says which
-        _need(scales, f"{name}_scales", u8, (rows, K // 32))
+    _need(codes, f"{name}_codes", u8, (rows, K // 2))
+    _need(scales, f"{name}_scales", u8, (rows, K // 32))
     return rows, K
 
 
@@ -641,9 +646,12 @@ def gemm_gated(x_codes, x_scales, gate_codes, gate_scales, up_codes, up_scales, 
         h, ldh = x_codes.new_empty((M, F), dtype=bf16), F
     else:
         ldh = _rows(h, "h", bf16, (M, F))
-    _check(lib().fp4q_gemm_gated(M, F, K, _ptr(x_codes), _ptr(x_scales), _ptr(gate_codes),
-                                 _ptr(gate_scales), _ptr(up_codes), _ptr(up_scales), act, _ptr(h),
-                                 ldh, _ptr(gate), _ptr(up), ldgu, _stream(stream)))
+    status = lib().fp4q_gemm_gated(
+        M, F, K, x_codes.data_ptr(), x_scales.data_ptr(), gate_codes.data_ptr(),
+        gate_scales.data_ptr(), up_codes.data_ptr(), up_scales.data_ptr(), act, h.data_ptr(), ldh,
+        _ptr(gate), _ptr(up), ldgu, _stream(stream))
+    if status:
+        _check(status)
     return h if gate is None else (h, gate, up)
 
 
@@ -668,16 +676,20 @@ def gemm_gated_grad(dy_codes, dy_scales, w_codes, w_scales, gate, up, act=SILU, 
         ldd = _rows(d_gate, "d_gate", bf16, (M, F))
         if _rows(d_up, "d_up", bf16, (M, F)) != ldd:
             raise ValueError("d_gate and d_up must have the same row stride")
-    _check(lib().fp4q_gemm_gated_grad(M, F, K, _ptr(dy_codes), _ptr(dy_scales), _ptr(w_codes),
-                                      _ptr(w_scales), act, _ptr(gate), _ptr(up), ldgu,
-                                      _ptr(d_gate), _ptr(d_up), ldd, _stream(stream)))
+    status = lib().fp4q_gemm_gated_grad(
+        M, F, K, dy_codes.data_ptr(), dy_scales.data_ptr(), w_codes.data_ptr(), w_scales.data_ptr(),
+        act, gate.data_ptr(), up.data_ptr(), ldgu, d_gate.data_ptr(), d_up.data_ptr(), ldd,
+        _stream(stream))
+    if status:
+        _check(status)
     return d_gate, d_up
 
 
 def _vec(t, name, dtype, n):
     """Checks a contiguous device vector of n elements (dtype None: any)."""
-    if not t.is_cuda:
-        _need_cuda(t)
+    if t.shape == (n,) and t.is_cuda and t.is_contiguous() and (dtype is None or t.dtype is dtype):
+        return
+    _need_cuda(t)
     _need(t, name, t.dtype if dtype is None else dtype, (n,))
 
 
@@ -685,12 +697,12 @@ def _affine(weight, bias, cols):
     """Dtype code of the norm's weight and bias vectors."""
     if weight is not None:
         _vec(weight, "weight", None, cols)
-    if bias is not None:
-        _vec(bias, "bias", None, cols)
-        if weight is not None and weight.dtype != bias.dtype:
-            raise TypeError("weight and bias must have the same dtype")
-    t = weight if weight is not None else bias
-    return F32 if t is None else _dt(t)
+    if bias is None:
+        return F32 if weight is None else _dt(weight)
+    _vec(bias, "bias", None, cols)
+    if weight is not None and weight.dtype != bias.dtype:
+        raise TypeError("weight and bias must have the same dtype")
+    return _dt(bias)
 
 
 def layer_norm(x, weight=None, bias=None, eps=1e-5, kind=LAYER_NORM, y=None, out_dtype=None,
@@ -721,8 +733,11 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, kind=LAYER_NORM, y=None, out
         _vec(rstd, "rstd", f32, R)
     elif stats:
         rstd = x.new_empty((R,), dtype=f32)
-    _check(lib().fp4q_layer_norm(kind, _ptr(x), xdt, R, C, ldx, _ptr(weight), _ptr(bias), wdt, eps,
-                                 _ptr(y), ydt, ldy, _ptr(mean), _ptr(rstd), _stream(stream)))
+    status = lib().fp4q_layer_norm(kind, x.data_ptr(), xdt, R, C, ldx, _ptr(weight), _ptr(bias), wdt,
+                                   eps, y.data_ptr(), ydt, ldy, _ptr(mean), _ptr(rstd),
+                                   _stream(stream))
+    if status:
+        _check(status)
     return y, mean, rstd
 
 

@@ -53,7 +53,11 @@ __device__ __forceinline__ Global<T> global(const void* p) {
 
 constexpr int kTensors = 44;     // descriptors per launch: 4 KB of kernel arguments
 constexpr int kChunk = 4096;     // elements per workgroup
-constexpr int kMaxGroups = 1 << 23;  // workgroups per launch: 2^31 threads
+// Threads of a workgroup.  With 8-bit moments a lane has one set of 8 elements
+// (of 16 with 256 threads): its random numbers and roundings are a long chain,
+// which is all that a few small tensors wait for (4191 elements 6.7 and 5.2 us).
+constexpr int group_threads(int bits) { return bits == 8 ? 512 : 256; }
+constexpr int kMaxGroups = 1 << 22;  // workgroups per launch: 2^31 threads
 
 struct AdamwArg {
     float* p;
@@ -91,13 +95,23 @@ __device__ __forceinline__ uint32_t sr_e4m3(float y, uint32_t u) {
     return y >= 0.015625f ? normal : sub;
 }
 
-// The update of one element; v is v or (8-bit) r squared.
+// The update of one element; v is v or (8-bit) r squared.  With 8-bit moments,
+// whose random numbers and roundings keep the vector units busy four fifths of
+// the time, root and quotient are the hardware's (1 ulp each; the root's
+// argument kept out of the subnormals, which it would flush, and the quotient's
+// never is one: a root is at least 2^-75).
+template <int BITS>
 __device__ __forceinline__ float adamw_one(const AdamwScalars& a, float p, float g, float m, float v,
                                            float decay, float& m1, float& v1, float& r1) {
     m1 = a.b1 * m + a.a1 * g;
     v1 = a.b2 * v + a.a2 * g * g;
-    r1 = sqrtf(v1);
-    return p * decay - a.lr * m1 / (r1 * a.rc2 + a.eps);
+    if (BITS == 32) {
+        r1 = sqrtf(v1);
+        return p * decay - a.lr * m1 / (r1 * a.rc2 + a.eps);
+    }
+    const bool tiny = v1 < 0x1p-96f;
+    r1 = __builtin_amdgcn_sqrtf(tiny ? v1 * 0x1p64f : v1) * (tiny ? 0x1p-32f : 1.0f);
+    return p * decay - a.lr * m1 * __builtin_amdgcn_rcpf(r1 * a.rc2 + a.eps);
 }
 
 // Scale bytes of the block of 32 whose magnitudes this lane and its three
@@ -191,7 +205,7 @@ __device__ __forceinline__ void chunk32(const AdamwScalars& a, const AdamwArg& d
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             float m1, v1;
-            p1[e] = adamw_one(a, as_f32(p[k][e]), g[k].at(e) * gscale, as_f32(m[k][e]),
+            p1[e] = adamw_one<32>(a, as_f32(p[k][e]), g[k].at(e) * gscale, as_f32(m[k][e]),
                               as_f32(v[k][e]), decay, m1, v1, r1);
             p[k][e] = as_u32(p1[e]);
             m[k][e] = as_u32(m1);
@@ -206,18 +220,18 @@ __device__ __forceinline__ void chunk32(const AdamwScalars& a, const AdamwArg& d
     const int64_t j = (d.n & ~(int64_t)3) + threadIdx.x;  // what is left past the vectors
     if (whole || j >= d.n) return;
     float m1, v1, r1;
-    const float p1 = adamw_one(a, dp[j], grad1<GB>(d.g, j) * gscale, dm[j], dv[j], decay, m1, v1, r1);
+    const float p1 = adamw_one<32>(a, dp[j], grad1<GB>(d.g, j) * gscale, dm[j], dv[j], decay, m1, v1, r1);
     dp[j] = p1;
     dm[j] = m1;
     dv[j] = v1;
     if (dc) dc[j] = (uint16_t)f32_to_bf16_bits(p1);
 }
 
-// The same with 8-bit moments: 8 elements per lane, 2048 at a time.
+// The same with 8-bit moments: 8 elements per lane, the whole chunk at a time.
 template <int GB>
 __device__ __forceinline__ void chunk8(const AdamwScalars& a, const AdamwArg& d, int64_t i0,
                                        float gscale, float decay) {
-    constexpr int U = kChunk / 2048;
+    constexpr int SPAN = 8 * group_threads(8), U = kChunk / SPAN;
     const int64_t i = i0 + threadIdx.x * 8;
     const Global<float> dp = global<float>(d.p);
     const Global<uint8_t> dm = global<uint8_t>(d.m), dv = global<uint8_t>(d.v);
@@ -230,7 +244,7 @@ __device__ __forceinline__ void chunk8(const AdamwScalars& a, const AdamwArg& d,
     float sm[U], sv[U];
 #pragma unroll
     for (int k = 0; k < U; ++k) {
-        const int64_t j = i + k * 2048;
+        const int64_t j = i + k * SPAN;
         if (whole || j + 8 <= d.n) {
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
@@ -261,7 +275,7 @@ __device__ __forceinline__ void chunk8(const AdamwScalars& a, const AdamwArg& d,
     }
 #pragma unroll
     for (int k = 0; k < U; ++k) {
-        const int64_t j = i + k * 2048;
+        const int64_t j = i + k * SPAN;
         float m1[8], r1[8], p1[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -277,7 +291,7 @@ __device__ __forceinline__ void chunk8(const AdamwScalars& a, const AdamwArg& d,
                                       : __builtin_amdgcn_cvt_f32_fp8(wv, 3);
             const float r = vf * sv[k];
             float v1;
-            p1[e] = adamw_one(a, as_f32(p[k][e >> 2][b]), g[k][e >> 2].at(b) * gscale, mf * sm[k],
+            p1[e] = adamw_one<8>(a, as_f32(p[k][e >> 2][b]), g[k][e >> 2].at(b) * gscale, mf * sm[k],
                               r * r, decay, m1[e], v1, r1[e]);
             if (!whole && j + e >= d.n) m1[e] = r1[e] = 0.0f;
         }
@@ -325,7 +339,7 @@ __device__ __forceinline__ void adamw_group(const AdamwScalars& h, const AdamwAr
 }
 
 template <int GB, int BITS>
-__global__ __launch_bounds__(256) void adamw_kernel(const AdamwArgs a) {
+__global__ __launch_bounds__(group_threads(BITS)) void adamw_kernel(const AdamwArgs a) {
     // the group's tensor: the last that starts at or before it, found by all
     // lanes at once
     const int l = threadIdx.x & 63;
@@ -334,7 +348,7 @@ __global__ __launch_bounds__(256) void adamw_kernel(const AdamwArgs a) {
     adamw_group<GB, BITS>(a.h, a.t[t], blockIdx.x);
 }
 template <int GB, int BITS>
-__global__ __launch_bounds__(256) void adamw_table_kernel(const AdamwArg* __restrict__ table,
+__global__ __launch_bounds__(group_threads(BITS)) void adamw_table_kernel(const AdamwArg* __restrict__ table,
                                                           const uint32_t* __restrict__ owner,
                                                           uint32_t group0, const AdamwScalars h) {
     const uint32_t group = group0 + blockIdx.x;
@@ -382,14 +396,14 @@ static uint64_t rounded(int64_t n) { return (uint64_t)((n + 31) / 32) * 32; }
     do {                                                                          \
         if (bits == 8) {                                                          \
             if (gdtype == BF16)                                                   \
-                FP4Q_LAUNCH((KERNEL<1, 8>), grid, dim3(256), 0, s, __VA_ARGS__);  \
+                FP4Q_LAUNCH((KERNEL<1, 8>), grid, dim3(group_threads(8)), 0, s, __VA_ARGS__);  \
             else                                                                  \
-                FP4Q_LAUNCH((KERNEL<0, 8>), grid, dim3(256), 0, s, __VA_ARGS__);  \
+                FP4Q_LAUNCH((KERNEL<0, 8>), grid, dim3(group_threads(8)), 0, s, __VA_ARGS__);  \
         } else {                                                                  \
             if (gdtype == BF16)                                                   \
-                FP4Q_LAUNCH((KERNEL<1, 32>), grid, dim3(256), 0, s, __VA_ARGS__); \
+                FP4Q_LAUNCH((KERNEL<1, 32>), grid, dim3(group_threads(32)), 0, s, __VA_ARGS__); \
             else                                                                  \
-                FP4Q_LAUNCH((KERNEL<0, 32>), grid, dim3(256), 0, s, __VA_ARGS__); \
+                FP4Q_LAUNCH((KERNEL<0, 32>), grid, dim3(group_threads(32)), 0, s, __VA_ARGS__); \
         }                                                                         \
         const hipError_t e_ = hipGetLastError();                                  \
         if (e_ != hipSuccess) return e_;                                          \
