@@ -23,33 +23,62 @@
 
 namespace fp4q {
 
-// 256 x 128 and 128 x 128 tiles, four waves of 128 x 64 or 64 x 64.
+// 256 x 128 and 128 x 128 tiles, four waves of 128 x 64 or 64 x 64.  A K step is
+// 256 elements, 128 bytes of each row: loads take whole cache lines (8 rows x
+// 128 bytes each) and there is half as much waiting as with half the step.
 template <int ROWS>
 struct MidLayout {
     static constexpr int WAVES = 4, WM = 2, WN = 2, TM = ROWS / 64, TN = 2;
     static constexpr int WROWS = 32 * TM, WCOLS = 32 * TN, BM = WM * WROWS, BN = WN * WCOLS;
-    static constexpr int RA = BM / 16, RB = BN / 16;  // 1 KB code regions per step
-    static constexpr int RPW_A = RA / WAVES, RPW_B = RB / WAVES;
-    static constexpr int OFF_B = RA * REGION;
-    static constexpr int SPW_A = BM / 128;            // 32-row scale pieces of A per wave
+    static constexpr int RPW_A = BM / 32, RPW_B = BN / 32;  // 1 KB code regions per wave and step
+    static constexpr int OFF_B = BM * 128;                  // B codes within a stage
+    static constexpr int STAGES = ROWS == 128 ? 4 : 3;
 };
 template <>
 struct Layout<2> : MidLayout<256> {};
 template <>
 struct Layout<3> : MidLayout<128> {};
 
-// LDS of the four-wave form: a ring of four K steps of codes and four groups
-// of scales (8 bytes per row: two steps, or, where K % 128 == 64 and scale rows
-// are only 2-byte aligned, one step whose two halves fill a dword each).
-constexpr int MSTAGE = 24 * REGION, MSCALE = 384 * 8;
-__shared__ __attribute__((aligned(16))) uint8_t mt0[MSTAGE];
-__shared__ __attribute__((aligned(16))) uint8_t mt1[MSTAGE];
-__shared__ __attribute__((aligned(16))) uint8_t mt2[MSTAGE];
-__shared__ __attribute__((aligned(16))) uint8_t mt3[MSTAGE];
-__shared__ __attribute__((aligned(16))) uint8_t ms0[MSCALE];
-__shared__ __attribute__((aligned(16))) uint8_t ms1[MSCALE];
-__shared__ __attribute__((aligned(16))) uint8_t ms2[MSCALE];
-__shared__ __attribute__((aligned(16))) uint8_t ms3[MSCALE];
+// Their LDS: a ring of STAGES steps, codes and behind them scales.  A row's
+// scales of a step are 8 bytes, or, where K % 128 == 64 (TAIL) and scale rows
+// are only 2-byte aligned, four halves of a dword each.  At 256 rows TAIL has
+// room for two steps of scales only, in buffers of their own.  Few objects, and
+// each named at compile time: the compiler then tells reads from the loads in
+// flight into other ones, and does not wait for those.
+constexpr int MBK = 128;  // operand bytes per row per step
+constexpr int MSTAGE3 = 256 * MBK, MSTAGE2 = 384 * MBK;
+template <int CFG, int TAIL>
+constexpr int scale_ring() { return CFG == 2 && TAIL ? 2 : Layout<CFG>::STAGES; }
+__shared__ __attribute__((aligned(16))) uint8_t ma0[MSTAGE3 + 256 * 16];
+__shared__ __attribute__((aligned(16))) uint8_t ma1[MSTAGE3 + 256 * 16];
+__shared__ __attribute__((aligned(16))) uint8_t ma2[MSTAGE3 + 256 * 16];
+__shared__ __attribute__((aligned(16))) uint8_t ma3[MSTAGE3 + 256 * 16];
+__shared__ __attribute__((aligned(16))) uint8_t mb0[MSTAGE2 + 384 * 8];
+__shared__ __attribute__((aligned(16))) uint8_t mb1[MSTAGE2 + 384 * 8];
+__shared__ __attribute__((aligned(16))) uint8_t mb2[MSTAGE2 + 384 * 8];
+__shared__ __attribute__((aligned(16))) uint8_t mc0[MSTAGE2];
+__shared__ __attribute__((aligned(16))) uint8_t mc1[MSTAGE2];
+__shared__ __attribute__((aligned(16))) uint8_t mc2[MSTAGE2];
+__shared__ __attribute__((aligned(16))) uint8_t ms0[384 * 16];
+__shared__ __attribute__((aligned(16))) uint8_t ms1[384 * 16];
+// Stage and scale buffer of step number I.
+template <int CFG, int TAIL, int I>
+__device__ __forceinline__ uint8_t* mid_stage() {
+    constexpr int i = I % Layout<CFG>::STAGES;
+    if constexpr (CFG == 3)
+        return i == 0 ? ma0 : i == 1 ? ma1 : i == 2 ? ma2 : ma3;
+    else if constexpr (TAIL)
+        return i == 0 ? mc0 : i == 1 ? mc1 : mc2;
+    else
+        return i == 0 ? mb0 : i == 1 ? mb1 : mb2;
+}
+template <int CFG, int TAIL, int I>
+__device__ __forceinline__ uint8_t* mid_sbuf() {
+    if constexpr (CFG == 2 && TAIL)
+        return I % 2 ? ms1 : ms0;
+    else
+        return mid_stage<CFG, TAIL, I>() + (CFG == 3 ? MSTAGE3 : MSTAGE2);
+}
 
 template <int CFG>
 struct LaneMap {
@@ -68,75 +97,86 @@ struct LaneMap {
 
 #if defined(__HIP_DEVICE_COMPILE__)  // the host pass cannot instantiate buffer resources
 
-// Load sources, as Src of gemm_core.h: resources that end at the operand's
-// last row inside the tile, per-lane offsets, and the K step's scalar offset.
-// PAIR: B's 32-row groups alternate between the two operands, so group 2w
-// holds 32 rows of the first and group 2w + 1 the same rows of the second; a
-// wave's code regions all belong to one of them (the parity of wave / 2), its
-// scale rows to one (the parity of wave).
+// Load sources: buffer resources that end at the operand's last row inside the
+// tile, and per-lane offsets that advance with K, so that the range check
+// covers every byte (what lies past a row's end is the next row or zeros, and
+// is not multiplied).  PAIR: B's 32-row groups alternate between the two
+// operands, so group 2w holds 32 rows of the first and group 2w + 1 the same
+// rows of the second.
+//
+// In LDS a region is 8 rows x 128 bytes; 16-byte chunk c of row j lies in slot
+// 8 j + (c ^ j ^ (region's parity)), so that the 16 rows that are read together
+// spread over all banks.
 template <int CFG, int TAIL, int PAIR>
 struct MidSrc {
     using G = Layout<CFG>;
-    __amdgpu_buffer_rsrc_t ra, rb, rsa, rsb;
-    uint32_t va[G::RPW_A], vb[G::RPW_B], vsa[G::SPW_A], vsb;
-    int soff;
+    static constexpr int SROWS = TAIL ? 16 : 32;        // rows of a scale load, 64 / SROWS lanes each
+    static constexpr int SPW_A = G::BM / SROWS / 4, SPW_B = G::BN / SROWS / 4;
+    static constexpr int LC = G::RPW_A + G::RPW_B, LS = SPW_A + SPW_B;  // loads per wave and step
+    __amdgpu_buffer_rsrc_t ra, rb, rb2, rsa, rsb;
+    uint32_t va[G::RPW_A], vb[G::RPW_B], vsa[SPW_A], vsb[SPW_B];
 
     __device__ __forceinline__ void init(const GatedCall& o, int m0, int n0, const LaneMap<CFG>& l) {
         const int kbytes = o.K / 2, kscale = o.K / 32;
         const int rows_a = min(o.M - m0, G::BM), rows_b = min(o.F - n0, PAIR ? G::BN / 2 : G::BN);
-        const uint8_t* bc = PAIR && ((l.wave >> 1) & 1) ? o.bc2 : o.bc;
-        const uint8_t* bs = PAIR && (l.wave & 1) ? o.bs2 : o.bs;
         auto res = [](const uint8_t* p, int64_t first, int bytes) __attribute__((always_inline)) {
             return __builtin_amdgcn_make_buffer_rsrc((void*)(p + first), (short)0, bytes, BUF_FLAGS);
         };
+        // scale loads of B: TAIL's are half a 32-row group, two of which a wave takes
+        const bool second = PAIR && (TAIL ? (l.wave >> 1) & 1 : l.wave & 1);
         ra = res(o.ac, (int64_t)m0 * kbytes, rows_a * kbytes);
-        rb = res(bc, (int64_t)n0 * kbytes, rows_b * kbytes);
+        rb = res(o.bc, (int64_t)n0 * kbytes, rows_b * kbytes);
+        rb2 = PAIR ? res(o.bc2, (int64_t)n0 * kbytes, rows_b * kbytes) : rb;
         rsa = res(o.as, (int64_t)m0 * kscale, rows_a * kscale);
-        rsb = res(bs, (int64_t)n0 * kscale, rows_b * kscale);
-        // lane 4j + p of a region loads chunk p ^ ((j / 4) % 4) of row j
-        const int j = l.lane >> 2, c = ((l.lane & 3) ^ ((j >> 2) & 3)) * 16;
+        rsb = res(second ? o.bs2 : o.bs, (int64_t)n0 * kscale, rows_b * kscale);
+        const int j = l.lane >> 3, c = ((l.lane & 7) ^ j ^ (l.wave & 1)) * 16;
 #pragma unroll
         for (int q = 0; q < G::RPW_A; ++q)
-            va[q] = (uint32_t)(((q * G::WAVES + l.wave) * 16 + j) * kbytes + c);
+            va[q] = (uint32_t)(((q * 4 + l.wave) * 8 + j) * kbytes + c);
 #pragma unroll
-        for (int q = 0; q < G::RPW_B; ++q) {
-            const int row = PAIR ? q * 32 + (l.wave & 1) * 16 : (q * G::WAVES + l.wave) * 16;
+        for (int q = 0; q < G::RPW_B; ++q) {  // region 4 q + wave: group q
+            const int row = (PAIR ? q >> 1 : q) * 32 + l.wave * 8;
             vb[q] = (uint32_t)((row + j) * kbytes + c);
         }
-        // a scale piece is 32 rows, two lanes each: pieces wave (and wave + 4) of
-        // A's, and piece wave of B's four
-        const int part = (l.lane & 1) * (TAIL ? 2 : 4), row = l.lane >> 1;
+        const int srow = l.lane / (64 / SROWS), part = l.lane % (64 / SROWS) * (TAIL ? 2 : 4);
 #pragma unroll
-        for (int q = 0; q < G::SPW_A; ++q)
-            vsa[q] = (uint32_t)(((q * 4 + l.wave) * 32 + row) * kscale + part);
-        vsb = (uint32_t)(((PAIR ? l.wave >> 1 : l.wave) * 32 + row) * kscale + part);
-        soff = 0;
+        for (int q = 0; q < SPW_A; ++q)
+            vsa[q] = (uint32_t)(((q * 4 + l.wave) * SROWS + srow) * kscale + part);
+#pragma unroll
+        for (int q = 0; q < SPW_B; ++q) {
+            const int row = !PAIR ? (q * 4 + l.wave) * SROWS
+                            : TAIL ? q * 32 + (l.wave & 1) * 16 : (l.wave >> 1) * 32;
+            vsb[q] = (uint32_t)((row + srow) * kscale + part);
+        }
     }
     // Direct-to-LDS loads of the K step the sources point at; they then advance
     // unless that was the last one (re-issued past the end of K, so that every
     // step issues the same number of loads).
     __device__ __forceinline__ void codes(uint8_t* stage, int wave, bool advance) {
+        const uint32_t by = advance ? MBK : 0;
 #pragma unroll
-        for (int q = 0; q < G::RPW_A; ++q)
+        for (int q = 0; q < G::RPW_A; ++q) {
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                ra, (lds_ptr_t)(stage + (q * G::WAVES + wave) * REGION), 16, va[q], soff, 0, 0);
+                ra, (lds_ptr_t)(stage + (q * 4 + wave) * REGION), 16, va[q], 0, 0, 0);
+            va[q] += by;
+        }
 #pragma unroll
-        for (int q = 0; q < G::RPW_B; ++q)
+        for (int q = 0; q < G::RPW_B; ++q) {
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                rb, (lds_ptr_t)(stage + G::OFF_B + (q * G::WAVES + wave) * REGION), 16, vb[q], soff, 0,
-                0);
-        soff += advance ? BKB : 0;
+                PAIR && (q & 1) ? rb2 : rb, (lds_ptr_t)(stage + G::OFF_B + (q * 4 + wave) * REGION), 16,
+                vb[q], 0, 0, 0);
+            vb[q] += by;
+        }
     }
-    // Scales of group g: row R's 8 LDS bytes at 8 R.  The group's offset is part
-    // of the lane's, so the range check covers it.
-    __device__ __forceinline__ void scales(uint8_t* buf, int wave, int g) {
-        uint32_t off = (uint32_t)g * (TAIL ? 4 : 8);
+    // Scales of step t: row R's 8 (TAIL: 16) LDS bytes at that times R.
+    __device__ __forceinline__ void scales(uint8_t* buf, int wave, int t) {
+        uint32_t off = (uint32_t)t * 8;
         asm volatile("" : "+s"(off));  // one scalar; no hoisted vector offsets
 #pragma unroll
-        for (int q = 0; q <= G::SPW_A; ++q) {
-            const bool b = q == G::SPW_A;
-            lds_ptr_t dst = (lds_ptr_t)(buf + (b ? G::BM / 32 + wave : q * 4 + wave) * 256);
-            const uint32_t v = (b ? vsb : vsa[b ? 0 : q]) + off;
+        for (int q = 0; q < SPW_A + SPW_B; ++q) {
+            const bool b = q >= SPW_A;
+            lds_ptr_t dst = (lds_ptr_t)(buf + (q * 4 + wave) * 256);
+            const uint32_t v = (b ? vsb[b ? q - SPW_A : 0] : vsa[b ? 0 : q]) + off;
             if constexpr (TAIL)
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(b ? rsb : rsa, dst, 2, v, 0, 0, 0);
             else
@@ -145,108 +185,129 @@ struct MidSrc {
     }
 };
 
-// Scale words of step word w of a group for this lane's rows.
-template <int CFG, int TAIL>
-__device__ __forceinline__ void mid_scales(const uint8_t* buf, int w, const LaneMap<CFG>& l,
-                                           uint32_t (&sa)[Layout<CFG>::TM],
-                                           uint32_t (&sb)[Layout<CFG>::TN]) {
-    using G = Layout<CFG>;
-    auto word = [&](int row) __attribute__((always_inline)) -> uint32_t {
-        if (TAIL) {
-            const u32x2 d = *(const u32x2*)(buf + row * 8);
-            return (d.x & 0xFFFFu) | (d.y << 16);
-        }
-        return *(const uint32_t*)(buf + row * 8 + w * 4);
-    };
-#pragma unroll
-    for (int i = 0; i < G::TM; ++i) sa[i] = word(l.wm * G::WROWS + i * 32 + l.l32);
-#pragma unroll
-    for (int j = 0; j < G::TN; ++j) sb[j] = word(G::BM + l.wn * G::WCOLS + j * 32 + l.l32);
-}
-
-// The K loop of the four-wave form.  Step t multiplies two halves (64 elements
-// each) of its stage; it issues the code loads of step t + 3 into the stage of
-// step t - 1, which every wave finished reading before the last barrier, and,
-// ahead of them, the scales of step t + 3 where that opens a group.  So what
-// is behind the codes of step t + 1, which have to land before step t's
-// barrier, is the codes of two steps and one group of scales (TAIL: two), the
-// same in every step.  Order within a step, fenced against the compiler's
-// scheduler: read the fragments of the second half, issue loads, multiply the
-// first half; wait, barrier; read the scales and the first fragments of step
-// t + 1, multiply the second half.  Eight steps are unrolled, so that every
-// buffer is named at compile time (the compiler then sees that loads in flight
-// and reads touch different LDS objects).
+// The K loop of the four-wave form.  Step t multiplies four quarters (64
+// elements each) of its stage; it issues the codes of the step one ring ahead
+// into the stage of step t - 1, which every wave finished reading before the
+// last barrier, and ahead of them that step's scales; so a count of the loads
+// issued since tells that all of step t + 1 has landed.  A quarter's fragments
+// are read while the one before is multiplied, the first quarter's of step t +
+// 1 after the barrier, while the last of step t is.
 template <int CFG, int TAIL, int PAIR>
-__device__ __forceinline__ void mid_kloop(v16f (&acc)[Layout<CFG>::TM][Layout<CFG>::TN],
-                                          const GatedCall& o, int m0, int n0,
-                                          const LaneMap<CFG>& l) {
+struct MidLoop {
     using G = Layout<CFG>;
-    constexpr int SG = TAIL ? 1 : 2;
-    constexpr int BEHIND = 2 * (G::RPW_A + G::RPW_B) + (TAIL ? 2 : 1) * (G::SPW_A + 1);
-    const int ksteps = (o.K / 2 + BKB - 1) / BKB;
-    const int off0 = (l.l32 >> 4) * REGION + region_slot(l.l32 & 15, l.half) * 16;
-    const int off1 = (l.l32 >> 4) * REGION + region_slot(l.l32 & 15, 2 + l.half) * 16;
-    MidSrc<CFG, TAIL, PAIR> src;
-    src.init(o, m0, n0, l);
+    using Src = MidSrc<CFG, TAIL, PAIR>;
+    static constexpr int R = G::STAGES, SR = scale_ring<CFG, TAIL>(), D = R - 1, SD = SR - 1;
+    static constexpr int UNROLL = R % SR == 0 ? R : R * SR;
+    static constexpr int BEHIND = SD == D ? (D - 1) * (Src::LC + Src::LS) : (D - 1) * Src::LC;
+    static_assert(SD == D || (D == 2 && SD == 1), "the order of loads that BEHIND counts");
+    Src src;
     Frags<CFG> FA, FB;
-    uint32_t sa[G::TM], ra[G::TM], sb[G::TN], rb[G::TN];
-    const int sh = 8 * l.half;
-    src.scales(ms0, l.wave, 0);
-    src.codes(mt0, l.wave, 1 < ksteps);
-    if (TAIL) src.scales(ms1, l.wave, 1);
-    src.codes(mt1, l.wave, 2 < ksteps);
-    src.scales(TAIL ? ms2 : ms1, l.wave, TAIL ? 2 : 1);
-    src.codes(mt2, l.wave, 3 < ksteps);
-    FP4Q_WAIT_VMCNT(BEHIND);
-    __builtin_amdgcn_s_barrier();
-    mid_scales<CFG, TAIL>(ms0, 0, l, ra, rb);
-    read_frags<CFG>(mt0, off0, l.wm, l.wn, FA);
+    uint32_t ra[2][G::TM], rb[2][G::TN], sa[G::TM], sb[G::TN];  // scale words: raw, shifted
+    int pa[4], pb[4];  // this lane's offsets of A's and B's quarters in a stage
+    int sh, wm, wn, l32, wave, ksteps, quarters;
 
-#define FP4Q_SBUF(P) (((P) / SG) % 4 == 0 ? ms0 : ((P) / SG) % 4 == 1 ? ms1 : ((P) / SG) % 4 == 2 ? ms2 : ms3)
-#define FP4Q_MSTEP(P, CUR, NEXT1, NEXTL)                                                \
-    do {                                                                                \
-        const int t_ = kt + (P);                                                        \
-        __builtin_amdgcn_sched_barrier(0);                                              \
-        shift_scales<CFG>(ra, rb, sh, sa, sb);                                          \
-        read_frags<CFG>(CUR, off1, l.wm, l.wn, FB);                                     \
-        if (((P) + 3) % SG == 0) src.scales(FP4Q_SBUF((P) + 3), l.wave, (t_ + 3) / SG); \
-        src.codes(NEXTL, l.wave, t_ + 4 < ksteps);                                      \
-        __builtin_amdgcn_sched_barrier(0);                                              \
-        mfma_half<CFG, 0, 0>(FA, sa, sb, acc);                                          \
-        __builtin_amdgcn_sched_barrier(0);                                              \
-        FP4Q_WAIT_VMCNT(BEHIND);                                                        \
-        __builtin_amdgcn_s_waitcnt(0xC07F);                                             \
-        __builtin_amdgcn_s_barrier();                                                   \
-        __builtin_amdgcn_sched_barrier(0);                                              \
-        mid_scales<CFG, TAIL>(FP4Q_SBUF((P) + 1), ((P) + 1) % SG, l, ra, rb);           \
-        read_frags<CFG>(NEXT1, off0, l.wm, l.wn, FA);                                   \
-        if (!TAIL || t_ != ksteps - 1) mfma_half<CFG, 0, 1>(FB, sa, sb, acc);           \
-    } while (0)
-#define FP4Q_MTURN(O, GUARD)                                     \
-    do {                                                         \
-        if (GUARD(O + 0)) FP4Q_MSTEP(O + 0, mt0, mt1, mt3);      \
-        if (GUARD(O + 1)) FP4Q_MSTEP(O + 1, mt1, mt2, mt0);      \
-        if (GUARD(O + 2)) FP4Q_MSTEP(O + 2, mt2, mt3, mt1);      \
-        if (GUARD(O + 3)) FP4Q_MSTEP(O + 3, mt3, mt0, mt2);      \
-    } while (0)
-#define FP4Q_ALL(P) true
-#define FP4Q_EXISTS(P) (kt + (P) < ksteps)
-    int kt = 0;
-    for (; kt + 8 <= ksteps; kt += 8) {
-        FP4Q_MTURN(0, FP4Q_ALL);
-        FP4Q_MTURN(4, FP4Q_ALL);
+    // Fragments of quarter kk of a stage: row lane % 32 of each 32-row group,
+    // chunk 2 kk + lane / 32.
+    __device__ __forceinline__ void read(const uint8_t* stage, int kk, Frags<CFG>& f) {
+#pragma unroll
+        for (int i = 0; i < G::TM; ++i) f.a[i] = *(const u32x4*)&stage[pa[kk] + i * 4096];
+#pragma unroll
+        for (int j = 0; j < G::TN; ++j) f.b[j] = *(const u32x4*)&stage[pb[kk] + j * 4096];
     }
-    if (kt < ksteps) {
-        FP4Q_MTURN(0, FP4Q_EXISTS);
-        FP4Q_MTURN(4, FP4Q_EXISTS);
+    __device__ __forceinline__ void read_scales(const uint8_t* buf) {
+        auto words = [&](int row, uint32_t& w0, uint32_t& w1) __attribute__((always_inline)) {
+            if (TAIL) {
+                const u32x4 d = *(const u32x4*)(buf + row * 16);
+                w0 = (d.x & 0xFFFFu) | (d.y << 16);
+                w1 = (d.z & 0xFFFFu) | (d.w << 16);
+            } else {
+                const u32x2 d = *(const u32x2*)(buf + row * 8);
+                w0 = d.x;
+                w1 = d.y;
+            }
+        };
+#pragma unroll
+        for (int i = 0; i < G::TM; ++i) words(wm * G::WROWS + i * 32 + l32, ra[0][i], ra[1][i]);
+#pragma unroll
+        for (int j = 0; j < G::TN; ++j)
+            words(G::BM + wn * G::WCOLS + j * 32 + l32, rb[0][j], rb[1][j]);
     }
-#undef FP4Q_MTURN
-#undef FP4Q_MSTEP
-#undef FP4Q_SBUF
-#undef FP4Q_ALL
-#undef FP4Q_EXISTS
-    FP4Q_WAIT_VMCNT(0);  // the re-issued loads past the end of K have landed
-}
+    // ALL: not the last step.
+    template <int P, bool ALL>
+    __device__ __forceinline__ void step(int t, v16f (&acc)[G::TM][G::TN]) {
+        uint8_t* cur = mid_stage<CFG, TAIL, P>();
+        const bool last = !ALL && t == ksteps - 1;
+        __builtin_amdgcn_sched_barrier(0);
+        shift_scales<CFG>(ra[0], rb[0], sh, sa, sb);
+        read(cur, 1, FB);
+        __builtin_amdgcn_sched_barrier(0);
+        mfma_half<CFG, 0, 0>(FA, sa, sb, acc);
+        __builtin_amdgcn_sched_barrier(0);
+        read(cur, 2, FA);
+        if (!last || quarters > 1) mfma_half<CFG, 0, 1>(FB, sa, sb, acc);
+        __builtin_amdgcn_sched_barrier(0);
+        read(cur, 3, FB);
+        src.scales(mid_sbuf<CFG, TAIL, P + SD>(), wave, t + SD);
+        src.codes(mid_stage<CFG, TAIL, P + D>(), wave, t + D + 1 < ksteps);
+        shift_scales<CFG>(ra[1], rb[1], sh, sa, sb);
+        if (!last || quarters > 2) mfma_half<CFG, 0, 0>(FA, sa, sb, acc);
+        __builtin_amdgcn_sched_barrier(0);
+        FP4Q_WAIT_VMCNT(BEHIND);
+        __builtin_amdgcn_s_waitcnt(0xC07F);
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        read_scales(mid_sbuf<CFG, TAIL, P + 1>());
+        read(mid_stage<CFG, TAIL, P + 1>(), 0, FA);
+        if (!last || quarters > 3) mfma_half<CFG, 0, 1>(FB, sa, sb, acc);
+    }
+    template <int P, bool ALL>
+    __device__ __forceinline__ void turn(int kt, v16f (&acc)[G::TM][G::TN]) {
+        // each step inside the one before's condition: where paths with and without
+        // a step's loads met again, the compiler would wait for all of them
+        if (!ALL && kt + P >= ksteps) return;
+        step<P, ALL>(kt + P, acc);
+        if constexpr (P + 1 < UNROLL) turn<P + 1, ALL>(kt, acc);
+    }
+    __device__ __forceinline__ void run(v16f (&acc)[G::TM][G::TN], const GatedCall& o, int m0, int n0,
+                                        const LaneMap<CFG>& l) {
+        src.init(o, m0, n0, l);
+        wm = l.wm;
+        wn = l.wn;
+        l32 = l.l32;
+        wave = l.wave;
+        sh = 8 * l.half;
+        ksteps = (o.K + 255) / 256;
+        quarters = (o.K / 64 - 1) % 4 + 1;  // of the last step
+        const int j = l32 & 7, reg = l32 >> 3;
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+            const int p = reg * REGION + j * 128 + (((2 * kk + l.half) ^ j ^ (reg & 1)) * 16);
+            pa[kk] = p + wm * G::TM * 4096;
+            pb[kk] = p + wn * G::TN * 4096 + G::OFF_B;
+            // opaque: rewritten as a longer chain of additions from the stage, a
+            // read would lose the compiler's note of which LDS object it is of,
+            // and wait for all loads in flight
+            asm volatile("" : "+v"(pa[kk]), "+v"(pb[kk]));
+        }
+        src.scales(mid_sbuf<CFG, TAIL, 0>(), wave, 0);
+        src.codes(mid_stage<CFG, TAIL, 0>(), wave, 1 < ksteps);
+        if constexpr (SD > 1) src.scales(mid_sbuf<CFG, TAIL, 1>(), wave, 1);
+        src.codes(mid_stage<CFG, TAIL, 1>(), wave, 2 < ksteps);
+        if constexpr (D > 2) {
+            src.scales(mid_sbuf<CFG, TAIL, 2>(), wave, 2);
+            src.codes(mid_stage<CFG, TAIL, 2>(), wave, 3 < ksteps);
+        }
+        FP4Q_WAIT_VMCNT(BEHIND);
+        __builtin_amdgcn_s_barrier();
+        read_scales(mid_sbuf<CFG, TAIL, 0>());
+        read(mid_stage<CFG, TAIL, 0>(), 0, FA);
+        int kt = 0;
+        const int whole = quarters == 4 ? ksteps : ksteps - 1;
+        for (; kt + UNROLL <= whole; kt += UNROLL) turn<0, true>(kt, acc);
+        turn<0, false>(kt, acc);
+        FP4Q_WAIT_VMCNT(0);  // the re-issued loads past the end of K have landed
+    }
+};
 
 // The tile's K loop in either form.
 template <int CFG, int TAIL, int PAIR>
@@ -266,22 +327,23 @@ __device__ __forceinline__ void tile_kloop(v16f (&acc)[Layout<CFG>::TM][Layout<C
                                      l.lane, l.wm, l.wn, l.half, l.l32, off0, off1, (l.l32 >> 3) & 3,
                                      o.bc2, o.bs2);
     } else {
-        mid_kloop<CFG, TAIL, PAIR>(acc, o, m0, n0, l);
+        MidLoop<CFG, TAIL, PAIR> loop;
+        loop.run(acc, o, m0, n0, l);
     }
     __syncthreads();  // all waves are done with the operand stages
 }
 
 // This wave's private part of the operand stages, EREG bytes, free once the
 // K loop's last barrier has passed.
-template <int CFG, int EREG>
+template <int CFG, int TAIL, int EREG>
 __device__ __forceinline__ uint8_t* wave_stage(int wave) {
-    static_assert(EREG % 16 == 0 && 2 * EREG <= (CFG == 0 ? STAGE : MSTAGE), "two to a stage");
+    static_assert(EREG % 16 == 0 && 2 * EREG <= STAGE, "two to a stage");
     const int s = wave >> 1;
     uint8_t* st;
     if constexpr (CFG == 0)
         st = s == 0 ? st0 : s == 1 ? st1 : s == 2 ? st2 : st3;
     else
-        st = s == 0 ? mt0 : mt1;
+        st = s == 0 ? mid_stage<CFG, TAIL, 0>() : mid_stage<CFG, TAIL, 1>();
     return st + (wave & 1) * EREG;
 }
 #endif
@@ -313,7 +375,7 @@ __global__ __launch_bounds__(64 * Layout<CFG>::WAVES, 1) void gemm_gated_kernel(
 
     constexpr int NOUT = SAVE ? 3 : 1;
     constexpr int PITCH = NOUT * 64 + 16;  // 32 bf16 of each output per row
-    uint8_t* reg = wave_stage<CFG, 32 * PITCH>(l.wave);
+    uint8_t* reg = wave_stage<CFG, TAIL, 32 * PITCH>(l.wave);
     const int row0 = m0 + l.wm * G::WROWS;
     const int col = n0 + l.wn * 32 + (l.lane & 3) * 8;
 #pragma unroll
@@ -378,11 +440,8 @@ __global__ __launch_bounds__(64 * Layout<CFG>::WAVES, 1) void gemm_gated_grad_ke
     };
     auto fetch = [&](int i, Pair& q) __attribute__((always_inline)) {
 #pragma unroll
-        for (int p = 0; p < PASSES; ++p) {
-            const int row = row0 + i * 32 + p * 8;
-            q.g[p] = q.u[p] = (u32x4){0u, 0u, 0u, 0u};
-            if (row >= o.M || col >= o.F) continue;
-            const int64_t at = (int64_t)row * o.ldgu;
+        for (int p = 0; p < PASSES; ++p) {  // past M, the last row again: no load is conditional
+            const int64_t at = (int64_t)min(row0 + i * 32 + p * 8, o.M - 1) * o.ldgu;
             q.g[p] = load8(o.gate + at, col, o.F);
             q.u[p] = load8(o.up + at, col, o.F);
         }
@@ -395,7 +454,7 @@ __global__ __launch_bounds__(64 * Layout<CFG>::WAVES, 1) void gemm_gated_grad_ke
     v16f acc[G::TM][G::TN];
     tile_kloop<CFG, TAIL, 0>(acc, o, m0, n0, l);
 
-    uint8_t* reg = wave_stage<CFG, 32 * PITCH>(l.wave);
+    uint8_t* reg = wave_stage<CFG, TAIL, 32 * PITCH>(l.wave);
     if (!kEarly) {
         fetch(0, in[0]);
         fetch(1, in[1]);
@@ -467,18 +526,16 @@ static int64_t tiles_of(const GatedCall& g, int bm, int bn) {
 
 // The form is the one with the largest tiles that still finish in one round of
 // the compute units, since larger tiles load less but a tile's K loop takes
-// the same time on an idle chip.  Forward, us (small, 128-row, 256-row, 256 x 256):
-//   M x F x K          64 x 1408 x 960    4.2   6.1   9.0  11.0
-//                     512 x 1408 x 960    7.3   6.4   9.8  12.6
-//                    2048 x 1408 x 960   20.6  13.3  10.8  13.3
-//                    4096 x 1408 x 960   37.8  20.9  20.6  14.3
-//                      1 x 5632 x 2048    7.1   7.3  11.5  14.5
-//                    128 x 13824 x 5120   84.8  27.5  31.0  43.6
+// the same time on an idle chip.  Forward, us (128-row, 256-row, 256 x 256):
+//   M x F x K         512 x 1408 x 960    6.7   9.8  12.6
+//                    2048 x 1408 x 960   13.3  10.8  13.3
+//                    4096 x 1408 x 960   20.9  20.6  14.3
+//                     128 x 13824 x 5120 25.8  31.0  43.6
+//                     256 x 13824 x 5120 50.6  33.2  50.3
 // and of the gradient:
-//                     256 x 1408 x 960    4.7   9.2  15.7  23.1
-//                    2048 x 1408 x 960   13.8  11.1  16.9  24.1
-//                    1024 x 5632 x 2048  58.6  25.3  22.7  30.4
-//                    2048 x 5632 x 2048   107  40.6  44.5  37.2
+//                    2048 x 1408 x 960   11.3  16.9  24.1
+//                    1024 x 5632 x 2048  25.3  23.6  30.4
+//                    2048 x 5632 x 2048  40.6  44.5  35.2
 constexpr int64_t kOneRound = 256;
 
 template <int GELU>

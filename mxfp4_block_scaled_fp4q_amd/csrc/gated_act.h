@@ -78,14 +78,15 @@ __device__ __forceinline__ void store8(uint16_t* p, u32x4 v, int n) {
         if (n & 1) q[n & 2] = (uint16_t)((n & 2) ? ((n & 4) ? v.w : v.y) : w);
     }
 }
-// Elements col .. col + 7 of a row of F, in two steps, so that no lane waits
+// Elements col .. col + 7 of a row of F >= 8, in two steps, so that no lane waits
 // for its data where it loads them: the row's last ones come from F - 8 and are
-// shifted into place at their use.  (Rows shorter than 8 go one by one.)  They
-// are read once: non-temporal (gradient 4096 x 5632 x 2048 68 us, 81 without).
+// shifted into place at their use.  They are read once: non-temporal (gradient
+// 4096 x 5632 x 2048 68 us, 81 without).
 __device__ __forceinline__ u32x4 load8(const uint16_t* row, int col, int F) {
-    if (F >= 8) {
-        return __builtin_nontemporal_load((const u32x4_a2*)(row + min(col, F - 8)));
-    }
+    return __builtin_nontemporal_load((const u32x4_a2*)(row + min(col, F - 8)));
+}
+// The same of a shorter row, one by one and in place.
+__device__ __forceinline__ u32x4 load_short(const uint16_t* row, int col, int F) {
     uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
     for (int e = 0; e < 8; ++e)

@@ -61,8 +61,9 @@ __global__ __launch_bounds__(64 * KS) void gated_small_kernel(const GatedCall g,
             const int i = p * 64 * KS + threadIdx.x;
             const int row = m0 + i / (2 * NT), col = n0 + i % (2 * NT) * 8;
             if (i < GROUPS && row < g.M && col < g.F) {
-                gin[p] = load8(g.gate + row * g.ldgu, col, g.F);
-                uin[p] = load8(g.up + row * g.ldgu, col, g.F);
+                const uint16_t *gr = g.gate + row * g.ldgu, *ur = g.up + row * g.ldgu;
+                gin[p] = g.F >= 8 ? load8(gr, col, g.F) : load_short(gr, col, g.F);
+                uin[p] = g.F >= 8 ? load8(ur, col, g.F) : load_short(ur, col, g.F);
             }
         }
     }
@@ -191,15 +192,25 @@ static void go(const GatedCall& g, hipStream_t s) {
                 dim3(64 * KS), 0, s, g, tiles_m);
 }
 
-// The smallest tiles first: each is taken up to where the next larger form was
-// faster.  That is set by the operand loads of all workgroups together
-// (workgroups times K; the same fragment is loaded by every tile that needs
-// it) or, for the gradient, by the workgroups a round holds.  Measured around
-// the limits, us, at F x K = 1408 x 960 except where stated:
-//   forward   M = 64:  16 x 16 4.2, 32 x 32 4.2, LDS tiles 6.1;  128: 5.0, 4.2, 6.0;
-//             512: 10.1, 7.3, 6.4;  (M = 1, 5632 x 2048: 7.1, 7.3, 7.3)
-//   gradient  M = 64: 16 x 32 3.4, 32 x 32 3.7, 32 x 64 4.4, LDS tiles 8.4;
-//             128: 4.3, 3.7, 4.5, 9.0;  512: 9.1, 6.4, 6.1, 9.6;  2048: 30.6, 19.2, 14.6, 11.1
+// The smallest tiles first: each is taken while its workgroups are one round of
+// the 256 compute units, where it takes about 2.5 us and 1.4 ns an element of K
+// (32 rows: 1.9 ns, 32 x 32: 2.9 ns; gradient 1.4, 1.9 and 2.9), against 4 us and
+// 2.2 ns (gradient 6 and 2.6) of the LDS tiles of gated.hip.  Around the limits,
+// us, small tiles in the order below and LDS tiles (groups of the first):
+//   forward   M x F x K    64 x 704 x 5120   (176)   9.6, 11.9, 16.1; 14.6
+//                         128 x 704 x 5120   (352)  16.3, 12.1, 16.2; 15.7
+//                          64 x 1408 x 960   (352)   4.2,  4.7,  4.2;  6.1
+//                         128 x 1408 x 960   (704)   5.0,  5.9,  4.2;  6.1
+//                         256 x 704 x 2048   (704)  10.9, 10.8,  8.4;  8.2
+//                           1 x 6660 x 4032  (417)   9.7, 10.4, 10.4; 14.4
+//                          16 x 5632 x 2048  (352)   8.6,  8.9,  7.8;  7.8
+//   gradient              128 x 704 x 5120   (176)   9.8, 12.0, 16.8; 18.2
+//                         128 x 1408 x 4096  (352)  14.0, 10.6, 14.4; 16.9
+//                         256 x 1408 x 4096  (704)  19.7, 18.0, 14.9; 17.0
+//                         512 x 1408 x 960  (1408)   9.1,  6.4,  6.1;  9.5
+//                         512 x 1408 x 2048 (1408)  20.8, 14.7, 14.8; 12.1
+// Up to 16 rows a second round is taken too, since what larger tiles would share
+// are rows of A, and at short K, where the LDS tiles' start counts for more.
 bool launch_gated_small(const GatedCall& g, bool grad, int gelu, hipStream_t s) {
     auto groups = [&](int64_t bm, int64_t bn) { return (g.M + bm - 1) / bm * ((g.F + bn - 1) / bn); };
     const int64_t K = g.K;
@@ -208,12 +219,16 @@ bool launch_gated_small(const GatedCall& g, bool grad, int gelu, hipStream_t s) 
     if (grad) {
         if (groups(16, 32) <= 256) return FP4Q_GO(1, 0, 1, 2, 8), true;
         if (groups(32, 32) <= 256) return FP4Q_GO(1, 0, 2, 2, 4), true;
-        if (groups(32, 64) * K <= 365000) return FP4Q_GO(1, 0, 2, 4, 4), true;
+        // (rows below 8 elements are this form's alone)
+        if (groups(32, 64) <= 256 || groups(32, 64) * K <= 365000 || g.F < 8)
+            return FP4Q_GO(1, 0, 2, 4, 4), true;
         return false;
     }
-    if (groups(16, 16) <= 512 && groups(16, 16) * K <= 345000)
+    if (groups(16, 16) <= 256 || (groups(16, 16) <= 512 && (g.M <= 16 || K <= 1024)))
         return g.gate ? FP4Q_GO(0, 1, 1, 1, 4) : FP4Q_GO(0, 0, 1, 1, 4), true;
-    if (groups(32, 32) * K <= 250000)
+    if (groups(32, 16) <= 256)
+        return g.gate ? FP4Q_GO(0, 1, 2, 1, 8) : FP4Q_GO(0, 0, 2, 1, 8), true;
+    if (groups(32, 32) <= 256 && K <= 1536)
         return g.gate ? FP4Q_GO(0, 1, 2, 2, 4) : FP4Q_GO(0, 0, 2, 2, 4), true;
 #undef FP4Q_GO
     return false;

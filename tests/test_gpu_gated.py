@@ -189,6 +189,16 @@ def test_grad_tiled_forms(orc, M, F, K, act):
     grad_check(orc, M, F, K, act, pad=3, rows=some_rows(M))
 
 
+@pytest.mark.parametrize("M,F,K", [(40, 300, 2112), (200, 100, 1088), (70, 200, 4160), (500, 70, 320),
+                                   (3, 6000, 192), (2500, 5, 128), (700, 7, 64)])
+def test_small_tiles_and_short_rows(orc, M, F, K):
+    """Each tile of the small form, and rows of fewer than 8 elements."""
+    x, g, u = quant(orc, M, K, M, 1.0), quant(orc, F, K, F + 7, 0.05), quant(orc, F, K, F + 9, 0.05)
+    for act in (fq.SILU, fq.GELU):
+        forward_check(orc, x, g, u, act, save=True, pad=1, rows=some_rows(M))
+        grad_check(orc, M, F, K, act, pad=1, rows=some_rows(M))
+
+
 @pytest.mark.parametrize("act", [fq.SILU, fq.GELU])
 def test_grad_far_arguments(orc, act):
     """Gates far out on both sides: the sigmoid's ends and products that vanish."""
