@@ -346,6 +346,15 @@ __device__ __forceinline__ uint8_t* wave_stage(int wave) {
         st = s == 0 ? mid_stage<CFG, TAIL, 0>() : mid_stage<CFG, TAIL, 1>();
     return st + (wave & 1) * EREG;
 }
+// Of EREG bytes for each pair of waves: a stage each.
+template <int CFG, int TAIL, int EREG>
+__device__ __forceinline__ uint8_t* pair_stage(int pair) {
+    static_assert(EREG % 16 == 0 && EREG <= STAGE, "a pair to a stage");
+    if constexpr (CFG == 0)
+        return pair == 0 ? st0 : pair == 1 ? st1 : pair == 2 ? st2 : st3;
+    else
+        return pair == 0 ? mid_stage<CFG, TAIL, 0>() : mid_stage<CFG, TAIL, 1>();
+}
 #endif
 
 // Origin of tile number t, bm x bn outputs: XCD-contiguous, then grouped along M.
@@ -373,37 +382,41 @@ __global__ __launch_bounds__(64 * Layout<CFG>::WAVES, 1) void gemm_gated_kernel(
     v16f acc[G::TM][G::TN];
     tile_kloop<CFG, TAIL, 1>(acc, o, m0, n0, l);
 
+    // Two neighbouring waves hold 64 columns of every output, whole cache lines.
+    // They meet in LDS, 32 rows at a time (in two regions in turn, so one barrier
+    // is enough), and each stores 16 of the rows.
     constexpr int NOUT = SAVE ? 3 : 1;
-    constexpr int PITCH = NOUT * 64 + 16;  // 32 bf16 of each output per row
-    uint8_t* reg = wave_stage<CFG, TAIL, 32 * PITCH>(l.wave);
-    const int row0 = m0 + l.wm * G::WROWS;
-    const int col = n0 + l.wn * 32 + (l.lane & 3) * 8;
+    constexpr int PITCH = NOUT * 128 + 16;
+    uint8_t* reg = pair_stage<CFG, TAIL, 2 * 32 * PITCH>(l.wave >> 1);
+    const int row0 = m0 + l.wm * G::WROWS + (l.wn & 1) * 16 + (l.lane >> 3);
+    const int col = n0 + (l.wn >> 1) * 64 + (l.lane & 7) * 8;
 #pragma unroll
     for (int i = 0; i < G::TM; ++i) {
+        uint8_t* buf = reg + (i & 1) * 32 * PITCH;
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
             float hv[4];
             const v16f &ga = acc[i][0], &ua = acc[i][1];
 #pragma unroll
             for (int r = 0; r < 4; ++r) hv[r] = act_value<GELU>(ga[4 * g + r]) * ua[4 * g + r];
-            uint8_t* dst = reg + l.l32 * PITCH + (8 * g + 4 * l.half) * 2;
+            uint8_t* dst = buf + l.l32 * PITCH + ((l.wn & 1) * 32 + 8 * g + 4 * l.half) * 2;
             *(u32x2*)dst = (u32x2){pack_rne(hv[0], hv[1]), pack_rne(hv[2], hv[3])};
             if (SAVE) {
-                *(u32x2*)(dst + 64) = (u32x2){pack_rne(ga[4 * g], ga[4 * g + 1]),
-                                              pack_rne(ga[4 * g + 2], ga[4 * g + 3])};
-                *(u32x2*)(dst + 128) = (u32x2){pack_rne(ua[4 * g], ua[4 * g + 1]),
+                *(u32x2*)(dst + 128) = (u32x2){pack_rne(ga[4 * g], ga[4 * g + 1]),
+                                               pack_rne(ga[4 * g + 2], ga[4 * g + 3])};
+                *(u32x2*)(dst + 256) = (u32x2){pack_rne(ua[4 * g], ua[4 * g + 1]),
                                                pack_rne(ua[4 * g + 2], ua[4 * g + 3])};
             }
         }
         __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this wave's LDS writes done
-        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_s_barrier();        // (stores stay in flight)
 #pragma unroll
         for (int out = 0; out < NOUT; ++out)
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
-                const int rl = p * 16 + (l.lane >> 2);
-                const u32x4 v = *(const u32x4*)(reg + rl * PITCH + out * 64 + (l.lane & 3) * 16);
-                const int row = row0 + i * 32 + rl;
+                const int rl = (l.wn & 1) * 16 + p * 8 + (l.lane >> 3);
+                const u32x4 v = *(const u32x4*)(buf + rl * PITCH + out * 128 + (l.lane & 7) * 16);
+                const int row = row0 + i * 32 + p * 8;
                 if (row >= o.M) continue;
                 uint16_t* base = out == 0 ? o.h : out == 1 ? o.gate : o.up;
                 base += (int64_t)row * (out == 0 ? o.ldh : o.ldgu) + col;
@@ -412,7 +425,6 @@ __global__ __launch_bounds__(64 * Layout<CFG>::WAVES, 1) void gemm_gated_kernel(
                 else
                     store8<0>(base, v, o.F - col);
             }
-        __builtin_amdgcn_wave_barrier();
     }
 #endif
 }
