@@ -119,10 +119,10 @@ __device__ __forceinline__ void gated_grad8(const float (&d)[8], u32x4 g, u32x4 
     for (int e = 0; e < 8; ++e) {
         const float gv = (e & 1) ? bf16_hi(g[e >> 1]) : bf16_lo(g[e >> 1]);
         const float uv = (e & 1) ? bf16_hi(u[e >> 1]) : bf16_lo(u[e >> 1]);
-        const float s = act_sigma<GELU>(gv), a = gv * s, rest = a * (1.0f - s);
-        const float dz =
-            GELU ? __builtin_fmaf(3.0f * kGeluA * kGeluB, fminf(gv * gv, 1e30f), kGeluA) : 1.0f;
-        og[e] = d[e] * uv * __builtin_fmaf(rest, dz, s);
+        const float s = act_sigma<GELU>(gv), a = gv * s;
+        float rest = 1.0f - s;
+        if (GELU) rest *= __builtin_fmaf(3.0f * kGeluA * kGeluB, fminf(gv * gv, 1e30f), kGeluA);
+        og[e] = d[e] * uv * __builtin_fmaf(a, rest, s);
         ou[e] = d[e] * a;
     }
     dg = (u32x4){pack_rne(og[0], og[1]), pack_rne(og[2], og[3]), pack_rne(og[4], og[5]),

@@ -547,10 +547,11 @@ constexpr int64_t kAnyGrid = 1 << 16;
 // `waves` waves each, and at least `min_rows` rows to a workgroup (or to each
 // of its four waves).  Forward, 16, 24 and 32 waves: 16384 x 5120 bf16 118, 80
 // and 85 us (ten waves per row: 16 is one workgroup), fp32 119, 126 and 146.
-// Backward, 16, 24 and 32: 100, 101 and 116 us.  There each row of a walk costs
-// about 1.2 us and each workgroup a row of partial sums: 2, 4, 8, 16 rows
-// take 7.7, 8.8, 10.7, 15.6 us at 300 x 2048, 17.9, 14.8, 16.6, 24.2 at 1999 x
-// 1111 and 29.4, 29.3, 29.5, 26.7 at 8192 x 2048.
+// Backward, 16, 24 and 32: 100, 101 and 116 us.  There a walk costs a latency
+// per row and each workgroup a row of partial sums to write and join: 2, 4, 8,
+// 16 rows take 7.2, 7.3, 9.1, 13.5 us at 400 x 1024, 17.4, 14.0, 12.0, 15.1 at
+// 1999 x 1111, 9.9, 8.3, 9.2, 12.0 at 4000 x 300 (four rows at a time) and 29.4,
+// 29.3, 29.5, 26.7 at 8192 x 2048.
 constexpr int kNormWaves = 24, kGradWaves = 16;
 static int norm_groups(const NormShape& sh, int64_t rows, int waves, int min_rows) {
     const int64_t per = (int64_t)min_rows * (sh.multi ? 1 : 4);
@@ -559,7 +560,8 @@ static int norm_groups(const NormShape& sh, int64_t rows, int waves, int min_row
 static int norm_slabs(int64_t rows, int64_t cols) {
     const NormShape sh = norm_shape(rows, cols);
     if (sh.nv == 0) return (int)std::min<int64_t>(128, (rows + 63) / 64);
-    return norm_groups(sh, rows, kGradWaves, rows <= 512 ? 2 : rows <= 4096 ? 4 : sh.multi ? 16 : 8);
+    const int min_rows = rows <= 1024 ? 2 : sh.multi ? (rows <= 4096 ? 8 : 16) : rows <= 12000 ? 4 : 8;
+    return norm_groups(sh, rows, kGradWaves, min_rows);
 }
 
 size_t norm_grad_workspace_bytes(int64_t rows, int64_t cols) {
