@@ -157,6 +157,30 @@ def _stream(stream):
     return c._cuda_getCurrentRawStream(c._cuda_getDevice())
 
 
+_empty_strided_cuda = None
+
+
+def _allocator(t):
+    """An f(size, stride, dtype) that makes uninitialised contiguous tensors on
+    t's device: torch's shortest way to one where this torch has it and the
+    device is the current one (0.7 us a tensor against 1.4), else new_empty."""
+    global _empty_strided_cuda
+    c = _torch()._C
+    if _empty_strided_cuda is None:
+        guards = getattr(getattr(c, "_dynamo", None), "guards", None)
+        _empty_strided_cuda = getattr(guards, "_empty_strided_cuda", False)
+    if _empty_strided_cuda and t.get_device() == c._cuda_getDevice():
+        return _empty_strided_cuda
+    return lambda size, stride, dtype: t.new_empty(size, dtype=dtype)
+
+
+def _halves(t, rows, cols):
+    """The two [rows, cols] halves of one bf16 [rows, 2 cols] tensor."""
+    ld = 2 * cols
+    both = _allocator(t)((rows, ld), (ld, 1), _torch().bfloat16)
+    return both.as_strided((rows, cols), (ld, 1)), both.as_strided((rows, cols), (ld, 1), cols)
+
+
 def _need_cuda(*ts):
     for t in ts:
         if t is not None and not t.is_cuda:
@@ -640,10 +664,10 @@ def gemm_gated(x_codes, x_scales, gate_codes, gate_scales, up_codes, up_scales, 
         if _rows(up, "up", bf16, (M, F)) != ldgu:
             raise ValueError("gate and up must have the same row stride")
     elif save:
-        gate, up = x_codes.new_empty((M, 2 * F), dtype=bf16).split(F, 1)
+        gate, up = _halves(x_codes, M, F)
         ldgu = 2 * F
     if h is None:
-        h, ldh = x_codes.new_empty((M, F), dtype=bf16), F
+        h, ldh = _allocator(x_codes)((M, F), (F, 1), bf16), F
     else:
         ldh = _rows(h, "h", bf16, (M, F))
     status = lib().fp4q_gemm_gated(
@@ -670,7 +694,7 @@ def gemm_gated_grad(dy_codes, dy_scales, w_codes, w_scales, gate, up, act=SILU, 
     if (d_gate is None) != (d_up is None):
         raise ValueError("d_gate and d_up are given both or neither")
     if d_gate is None:
-        d_gate, d_up = dy_codes.new_empty((M, 2 * F), dtype=bf16).split(F, 1)
+        d_gate, d_up = _halves(dy_codes, M, F)
         ldd = 2 * F
     else:
         ldd = _rows(d_gate, "d_gate", bf16, (M, F))
@@ -716,23 +740,22 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, kind=LAYER_NORM, y=None, out
     R, C = x.shape
     xdt = ydt = _dt(x)
     wdt = _affine(weight, bias, C)
+    empty = _allocator(x)
     if y is None:
         ldy = C
-        if out_dtype is None:
-            y = x.new_empty((R, C))
-        else:
-            y = x.new_empty((R, C), dtype=out_dtype)
+        y = empty((R, C), (C, 1), x.dtype if out_dtype is None else out_dtype)
+        if out_dtype is not None:
             ydt = _dt(y)
     else:
         ldy, ydt = _rows(y, "y", shape=(R, C)), _dt(y)
     if mean is not None:
         _vec(mean, "mean", f32, R)
     elif stats and kind == LAYER_NORM:
-        mean = x.new_empty((R,), dtype=f32)
+        mean = empty((R,), (1,), f32)
     if rstd is not None:
         _vec(rstd, "rstd", f32, R)
     elif stats:
-        rstd = x.new_empty((R,), dtype=f32)
+        rstd = empty((R,), (1,), f32)
     status = lib().fp4q_layer_norm(kind, x.data_ptr(), xdt, R, C, ldx, _ptr(weight), _ptr(bias), wdt,
                                    eps, y.data_ptr(), ydt, ldy, _ptr(mean), _ptr(rstd),
                                    _stream(stream))
@@ -755,8 +778,9 @@ def layer_norm_grad(dy, x, weight, mean, rstd, kind=LAYER_NORM, dx=None, want_we
     R, C = x.shape
     lddy = _rows(dy, "dy", shape=(R, C))
     wdt = _affine(weight, None, C)
+    empty = _allocator(x)
     if dx is None:
-        dx, lddx = x.new_empty((R, C)), C
+        dx, lddx = empty((R, C), (C, 1), x.dtype), C
     else:
         lddx = _rows(dx, "dx", x.dtype, (R, C))
     if mean is not None:
@@ -766,22 +790,26 @@ def layer_norm_grad(dy, x, weight, mean, rstd, kind=LAYER_NORM, dx=None, want_we
     if dweight is not None:
         _vec(dweight, "dweight", f32, C)
     elif want_weight:
-        dweight = x.new_empty((C,), dtype=f32)
+        dweight = empty((C,), (1,), f32)
     if dbias is not None:
         _vec(dbias, "dbias", f32, C)
     elif want_bias:
-        dbias = x.new_empty((C,), dtype=f32)
+        dbias = empty((C,), (1,), f32)
     nbytes = 0
     if dweight is not None or dbias is not None:
         if workspace is None:
-            nbytes = layer_norm_grad_workspace_bytes(R, C)
-            workspace = _scratch(nbytes, x.device, stream)
+            nbytes = lib().fp4q_layer_norm_grad_workspace_bytes(R, C)
+            workspace = empty((nbytes,), (1,), _torch().uint8)
+            if stream is not None:
+                workspace.record_stream(stream)  # as _scratch
         else:
             nbytes = workspace.numel() * workspace.element_size()
-    _check(lib().fp4q_layer_norm_grad(kind, _ptr(dy), _dt(dy), lddy, _ptr(x), _dt(x), R, C, ldx,
-                                      _ptr(weight), wdt, _ptr(mean), _ptr(rstd), _ptr(dx), lddx,
-                                      _ptr(dweight), _ptr(dbias), _ptr(workspace), nbytes,
-                                      _stream(stream)))
+    status = lib().fp4q_layer_norm_grad(kind, dy.data_ptr(), _dt(dy), lddy, x.data_ptr(), _dt(x), R, C,
+                                        ldx, _ptr(weight), wdt, _ptr(mean), _ptr(rstd),
+                                        dx.data_ptr(), lddx, _ptr(dweight), _ptr(dbias),
+                                        _ptr(workspace), nbytes, _stream(stream))
+    if status:
+        _check(status)
     return dx, dweight, dbias
 
 
