@@ -23,7 +23,11 @@
 // chunk of 4096 elements of one tensor; a whole chunk's loads are issued ahead
 // of its arithmetic, 16 bytes per lane (8-bit moments: 8 bytes of codes, for 8
 // elements per lane, so that 4 lanes hold a block of 32).  A tensor's last
-// chunk takes its last elements, fewer than a vector, one by one.
+// chunk takes its last elements, fewer than a vector, one by one.  173M
+// elements with 32-bit moments and the copy 937 us (5.5 TB/s), 212M with 8-bit
+// ones 531 us (5.7): loads and stores are non-temporal (neither so 965 and 539
+// us, the loads alone 954 and 550, the stores alone 979 and 538); chunks of
+// 8192 elements 980 and 557 us.
 //
 // Up to kTensors descriptors travel in the kernel arguments, so that such a
 // call copies nothing to the device.  More come in a table in device memory
@@ -95,23 +99,39 @@ __device__ __forceinline__ uint32_t sr_e4m3(float y, uint32_t u) {
     return y >= 0.015625f ? normal : sub;
 }
 
-// The update of one element; v is v or (8-bit) r squared.  With 8-bit moments,
-// whose random numbers and roundings keep the vector units busy four fifths of
-// the time, root and quotient are the hardware's (1 ulp each; the root's
-// argument kept out of the subnormals, which it would flush, and the quotient's
-// never is one: a root is at least 2^-75).
-template <int BITS>
+// The update of one element with 32-bit moments.
 __device__ __forceinline__ float adamw_one(const AdamwScalars& a, float p, float g, float m, float v,
-                                           float decay, float& m1, float& v1, float& r1) {
+                                           float decay, float& m1, float& v1) {
     m1 = a.b1 * m + a.a1 * g;
     v1 = a.b2 * v + a.a2 * g * g;
-    if (BITS == 32) {
-        r1 = sqrtf(v1);
-        return p * decay - a.lr * m1 / (r1 * a.rc2 + a.eps);
+    return p * decay - a.lr * m1 / (sqrtf(v1) * a.rc2 + a.eps);
+}
+
+// Roots of 8 values that are not negative (or NaN), rounded to nearest: a root
+// that is a unit off lets a stochastic rounding now and then take the other
+// code, and where r is small the next step moves the parameter by that much.
+// y ~ 1/sqrt(x) is within a unit, s = x y within two, so that x - s^2 is exact
+// in an fma and one Newton step s + (x - s^2) y / 2 is off by 2^-45 of s before
+// its rounding.  Values outside [2^-96, infinity), where a step of that could
+// leave the normal numbers, take sqrtf; one test for the wave's 8 x 64.
+__device__ __forceinline__ void roots8(const float (&x)[8], float (&r)[8]) {
+    uint32_t lo = as_u32(x[0]), hi = lo;
+#pragma unroll
+    for (int e = 1; e < 8; ++e) {
+        lo = min(lo, as_u32(x[e]));
+        hi = max(hi, as_u32(x[e]));
     }
-    const bool tiny = v1 < 0x1p-96f;
-    r1 = __builtin_amdgcn_sqrtf(tiny ? v1 * 0x1p64f : v1) * (tiny ? 0x1p-32f : 1.0f);
-    return p * decay - a.lr * m1 * __builtin_amdgcn_rcpf(r1 * a.rc2 + a.eps);
+    if (__any(lo < (31u << 23) || hi >= 0x7F800000u)) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) r[e] = sqrtf(x[e]);
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float y = __builtin_amdgcn_rsqf(x[e]);
+        const float s = x[e] * y;
+        r[e] = __builtin_fmaf(__builtin_fmaf(-s, s, x[e]), 0.5f * y, s);
+    }
 }
 
 // Scale bytes of the block of 32 whose magnitudes this lane and its three
@@ -201,12 +221,12 @@ __device__ __forceinline__ void chunk32(const AdamwScalars& a, const AdamwArg& d
     for (int k = 0; k < U; ++k) {
         const int64_t j = i + k * 1024;
         if (!whole && j + 4 > d.n) continue;
-        float p1[4], r1;
+        float p1[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             float m1, v1;
-            p1[e] = adamw_one<32>(a, as_f32(p[k][e]), g[k].at(e) * gscale, as_f32(m[k][e]),
-                              as_f32(v[k][e]), decay, m1, v1, r1);
+            p1[e] = adamw_one(a, as_f32(p[k][e]), g[k].at(e) * gscale, as_f32(m[k][e]),
+                              as_f32(v[k][e]), decay, m1, v1);
             p[k][e] = as_u32(p1[e]);
             m[k][e] = as_u32(m1);
             v[k][e] = as_u32(v1);
@@ -219,8 +239,8 @@ __device__ __forceinline__ void chunk32(const AdamwScalars& a, const AdamwArg& d
     }
     const int64_t j = (d.n & ~(int64_t)3) + threadIdx.x;  // what is left past the vectors
     if (whole || j >= d.n) return;
-    float m1, v1, r1;
-    const float p1 = adamw_one<32>(a, dp[j], grad1<GB>(d.g, j) * gscale, dm[j], dv[j], decay, m1, v1, r1);
+    float m1, v1;
+    const float p1 = adamw_one(a, dp[j], grad1<GB>(d.g, j) * gscale, dm[j], dv[j], decay, m1, v1);
     dp[j] = p1;
     dm[j] = m1;
     dv[j] = v1;
@@ -276,7 +296,7 @@ __device__ __forceinline__ void chunk8(const AdamwScalars& a, const AdamwArg& d,
 #pragma unroll
     for (int k = 0; k < U; ++k) {
         const int64_t j = i + k * SPAN;
-        float m1[8], r1[8], p1[8];
+        float m1[8], v1[8], r1[8], p1[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const uint32_t wm = m[k][e >> 2], wv = v[k][e >> 2];
@@ -289,10 +309,16 @@ __device__ __forceinline__ void chunk8(const AdamwScalars& a, const AdamwArg& d,
                              : b == 1 ? __builtin_amdgcn_cvt_f32_fp8(wv, 1)
                              : b == 2 ? __builtin_amdgcn_cvt_f32_fp8(wv, 2)
                                       : __builtin_amdgcn_cvt_f32_fp8(wv, 3);
-            const float r = vf * sv[k];
-            float v1;
-            p1[e] = adamw_one<8>(a, as_f32(p[k][e >> 2][b]), g[k][e >> 2].at(b) * gscale, mf * sm[k],
-                              r * r, decay, m1[e], v1, r1[e]);
+            const float r = vf * sv[k], gr = g[k][e >> 2].at(b) * gscale;
+            m1[e] = a.b1 * (mf * sm[k]) + a.a1 * gr;
+            v1[e] = a.b2 * (r * r) + a.a2 * gr * gr;
+        }
+        roots8(v1, r1);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            // the quotient is the hardware's, a unit off at most: it leaves in p only
+            p1[e] = as_f32(p[k][e >> 2][e & 3]) * decay -
+                    a.lr * m1[e] * __builtin_amdgcn_rcpf(r1[e] * a.rc2 + a.eps);
             if (!whole && j + e >= d.n) m1[e] = r1[e] = 0.0f;
         }
         uint32_t bm, br;

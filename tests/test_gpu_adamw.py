@@ -296,3 +296,35 @@ def test_table_gives_the_same_bits_as_arguments(bits, gdt):
         return [t for t in (prob.p, prob.m, prob.v, prob.c, prob.ms, prob.vs) if t is not None]
     for a, b in zip(run(True), run(False)):
         assert torch.equal(a, b)
+
+
+def test_8bit_states_are_the_formula_in_fp32_bit_for_bit():
+    """Every product, sum and root of the moments is rounded once, to nearest, so
+    codes and scale bytes are those of the formula in fp32: a root that is a unit
+    off changes a code in some hundred thousand.  Zeros and values whose squares
+    are subnormal are among them."""
+    f = np.float32
+    n, step, seed = (1 << 23) + 13, 40, 99
+    prob = Problem([n], 8, torch.float32, False, seed=5)
+    prob.V[0][: 4096].zero_()
+    prob.G[0][: 2048].mul_(1e-17)
+    prob.G[0][2048:3000].zero_()
+    b = [t[0].cpu().numpy() for t in (prob.G, prob.M, prob.V, prob.MS, prob.VS)]
+    fq.adamw_step(prob.plan(0.1), step=step, seed=seed, **HYPER)
+    torch.cuda.synchronize()
+    g, r = b[0], ob.decode8(b[2], b[4]).astype(f)
+    a1, a2 = f(1 - HYPER["beta1"]), f(1 - HYPER["beta2"])
+    m = f(HYPER["beta1"]) * ob.decode8(b[1], b[3]).astype(f) + a1 * g
+    r = np.sqrt(f(HYPER["beta2"]) * (r * r) + a2 * g * g)
+    assert m.dtype == r.dtype == f
+    w = ob.philox_words(np.arange(n), step, seed)
+    for what, x, u, codes, scales in (("m", m, w & np.uint64(0xFFFF), prob.M, prob.MS),
+                                      ("r", r, w >> np.uint64(16), prob.V, prob.VS)):
+        ax = np.abs(x).astype(np.float64)
+        s = ob.e4m3_scale_byte(np.pad(ax, (0, -n % 32)).reshape(-1, 32).max(1))
+        assert np.array_equal(scales[0].cpu().numpy(), s), f"{what}: scale bytes"
+        c = ob.sr_e4m3(ax / np.repeat(2.0 ** (s - 127.0), 32)[:n], u.astype(np.int64))
+        got = codes[0].cpu().numpy()
+        bad = (got & 127) != c
+        assert not bad.any(), f"{what}: {int(bad.sum())} codes; first at {int(np.argmax(bad))}"
+        assert np.array_equal(got >> 7, np.signbit(x).astype(np.uint8)), f"{what}: signs"
