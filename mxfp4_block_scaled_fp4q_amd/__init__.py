@@ -160,11 +160,26 @@ def _stream(stream):
 _empty_strided_cuda = None
 
 
-def _allocator(t):
+def _allocator(t, stream):
     """An f(size, stride, dtype) that makes uninitialised contiguous tensors on
     t's device: torch's shortest way to one where this torch has it and the
-    device is the current one (0.7 us a tensor against 1.4), else new_empty."""
+    device is the current one (0.7 us a tensor against 1.4), else new_empty.
+
+    The tensors belong to `stream`, which the call's kernels run on: memory of
+    the current stream's pool may still be in use by that stream's pending work,
+    and would go back there when a result is dropped, written or not.  They are
+    recorded on the current stream, where the caller may read them."""
     global _empty_strided_cuda
+    if stream is not None:
+        cuda = _torch().cuda
+        current = cuda.current_stream()
+        if current.cuda_stream != stream.cuda_stream:
+            def on_stream(size, stride, dtype):
+                with cuda.stream(stream):
+                    out = t.new_empty(size, dtype=dtype)
+                out.record_stream(current)
+                return out
+            return on_stream
     c = _torch()._C
     if _empty_strided_cuda is None:
         guards = getattr(getattr(c, "_dynamo", None), "guards", None)
@@ -174,10 +189,10 @@ def _allocator(t):
     return lambda size, stride, dtype: t.new_empty(size, dtype=dtype)
 
 
-def _halves(t, rows, cols):
+def _halves(t, rows, cols, stream):
     """The two [rows, cols] halves of one bf16 [rows, 2 cols] tensor."""
     ld = 2 * cols
-    both = _allocator(t)((rows, ld), (ld, 1), _torch().bfloat16)
+    both = _allocator(t, stream)((rows, ld), (ld, 1), _torch().bfloat16)
     return both.as_strided((rows, cols), (ld, 1)), both.as_strided((rows, cols), (ld, 1), cols)
 
 
@@ -664,10 +679,10 @@ def gemm_gated(x_codes, x_scales, gate_codes, gate_scales, up_codes, up_scales, 
         if _rows(up, "up", bf16, (M, F)) != ldgu:
             raise ValueError("gate and up must have the same row stride")
     elif save:
-        gate, up = _halves(x_codes, M, F)
+        gate, up = _halves(x_codes, M, F, stream)
         ldgu = 2 * F
     if h is None:
-        h, ldh = _allocator(x_codes)((M, F), (F, 1), bf16), F
+        h, ldh = _allocator(x_codes, stream)((M, F), (F, 1), bf16), F
     else:
         ldh = _rows(h, "h", bf16, (M, F))
     status = lib().fp4q_gemm_gated(
@@ -694,7 +709,7 @@ def gemm_gated_grad(dy_codes, dy_scales, w_codes, w_scales, gate, up, act=SILU, 
     if (d_gate is None) != (d_up is None):
         raise ValueError("d_gate and d_up are given both or neither")
     if d_gate is None:
-        d_gate, d_up = _halves(dy_codes, M, F)
+        d_gate, d_up = _halves(dy_codes, M, F, stream)
         ldd = 2 * F
     else:
         ldd = _rows(d_gate, "d_gate", bf16, (M, F))
@@ -740,7 +755,7 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, kind=LAYER_NORM, y=None, out
     R, C = x.shape
     xdt = ydt = _dt(x)
     wdt = _affine(weight, bias, C)
-    empty = _allocator(x)
+    empty = _allocator(x, stream)
     if y is None:
         ldy = C
         y = empty((R, C), (C, 1), x.dtype if out_dtype is None else out_dtype)
@@ -778,7 +793,7 @@ def layer_norm_grad(dy, x, weight, mean, rstd, kind=LAYER_NORM, dx=None, want_we
     R, C = x.shape
     lddy = _rows(dy, "dy", shape=(R, C))
     wdt = _affine(weight, None, C)
-    empty = _allocator(x)
+    empty = _allocator(x, stream)
     if dx is None:
         dx, lddx = empty((R, C), (C, 1), x.dtype), C
     else:
@@ -800,8 +815,6 @@ def layer_norm_grad(dy, x, weight, mean, rstd, kind=LAYER_NORM, dx=None, want_we
         if workspace is None:
             nbytes = lib().fp4q_layer_norm_grad_workspace_bytes(R, C)
             workspace = empty((nbytes,), (1,), _torch().uint8)
-            if stream is not None:
-                workspace.record_stream(stream)  # as _scratch
         else:
             nbytes = workspace.numel() * workspace.element_size()
     status = lib().fp4q_layer_norm_grad(kind, dy.data_ptr(), _dt(dy), lddy, x.data_ptr(), _dt(x), R, C,

@@ -1,0 +1,105 @@
+"""Whose memory the gated, norm and AdamW bindings hand to the kernels, on the
+host: the library is replaced by a recorder and device tensors by host ones
+that say they are on a device, with a pool that remembers the stream each was
+allocated on and recorded on."""
+import contextlib
+
+import pytest
+import torch
+
+import mxfp4_block_scaled_fp4q_amd as fq
+
+MADE = []
+
+
+class Dev(torch.Tensor):
+    is_cuda = property(lambda self: True)
+
+    def new_empty(self, size, **kw):
+        t = dev(torch.zeros(size, dtype=kw.get("dtype", self.dtype)))
+        t.owner, t.recorded = torch.cuda.current_stream().name, set()
+        MADE.append(t)
+        return t
+
+    def record_stream(self, stream):
+        self.recorded.add(stream.name)
+
+
+class Stream:
+    def __init__(self, name, handle):
+        self.name, self.cuda_stream = name, handle
+
+
+def dev(t):
+    return t.as_subclass(Dev)
+
+
+class Recorder:
+    """Stands for the library: every call succeeds; remembers the last one."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        def call(*a):
+            self.calls.append((name, a))
+            return 64 if name.endswith("_bytes") else 0
+        return call
+
+
+@pytest.fixture
+def world(monkeypatch):
+    MADE.clear()
+    streams = dict(main=Stream("main", 0x10), side=Stream("side", 0x20))
+    state = dict(now=streams["main"])
+
+    @contextlib.contextmanager
+    def stream(s):
+        before, state["now"] = state["now"], s
+        yield
+        state["now"] = before
+    monkeypatch.setattr(torch.cuda, "stream", stream)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: state["now"])
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: state["now"].cuda_stream)
+    monkeypatch.setattr(fq, "_empty_strided_cuda", False)
+    monkeypatch.setattr(fq, "_lib", Recorder())
+    return streams
+
+
+def u8(*shape):
+    return dev(torch.zeros(shape, dtype=torch.uint8))
+
+
+def gated(**kw):
+    return fq.gemm_gated(u8(4, 64), u8(4, 4), u8(8, 64), u8(8, 4), u8(8, 64), u8(8, 4), save=True, **kw)
+
+
+def gated_grad(**kw):
+    g = dev(torch.zeros(4, 8, dtype=torch.bfloat16))
+    return fq.gemm_gated_grad(u8(4, 64), u8(4, 4), u8(8, 64), u8(8, 4), g, g, **kw)
+
+
+def norm(**kw):
+    return fq.layer_norm(dev(torch.zeros(4, 8)), **kw)
+
+
+def norm_grad(**kw):
+    x, s = dev(torch.zeros(4, 8)), dev(torch.zeros(4))
+    return fq.layer_norm_grad(x, x, None, s, s, **kw)
+
+
+@pytest.mark.parametrize("call,made", [(gated, 2), (gated_grad, 1), (norm, 3), (norm_grad, 4)])
+def test_what_a_call_allocates_belongs_to_its_stream(world, call, made):
+    """Memory from the current stream's pool may still be in use by that
+    stream's pending work, and a result that is dropped at once goes back there
+    while the other stream's kernel has yet to write it."""
+    call(stream=world["side"])
+    assert len(MADE) == made
+    assert all(t.owner == "side" and "main" in t.recorded for t in MADE)
+    assert fq._lib.calls[-1][1][-1] == world["side"].cuda_stream
+    MADE.clear()
+    call()
+    call(stream=world["main"])
+    assert len(MADE) == 2 * made
+    assert all(t.owner == "main" and not t.recorded for t in MADE)
