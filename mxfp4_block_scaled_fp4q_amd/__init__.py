@@ -835,7 +835,7 @@ class AdamwPlan:
     def __init__(self, array, n, bits, grad_dtype, tensors):
         self.array, self.n, self.bits, self.grad_dtype = array, n, bits, grad_dtype
         self.tensors = tensors
-        self.table, self.chunks = None, 0
+        self.table, self.chunks, self.streams = None, 0, set()
         if n > self.ARGUMENTS:
             torch = _torch()
             size, chunks = _ct.c_size_t(0), _ct.c_int64(0)
@@ -845,6 +845,14 @@ class AdamwPlan:
             host = host[-host.data_ptr() % 16:][:size.value]
             _check(fill(array, n, bits, host.data_ptr(), _ct.byref(size), _ct.byref(chunks)))
             self.table, self.chunks = host.to(tensors[0][0].device), chunks.value
+            self.streams.add(_stream(None))
+
+    def read_on(self, handle, stream):
+        """The table is about to be read on a stream: its memory is not to be
+        reused before that work is done, should the plan be dropped."""
+        if handle not in self.streams:
+            self.table.record_stream(_torch().cuda.current_stream() if stream is None else stream)
+            self.streams.add(handle)
 
 
 def adamw_state(param, bits=32):
@@ -912,14 +920,18 @@ def adamw_step(plan, lr, step, beta1=0.9, beta2=0.999, eps=1e-8, seed=0, grad_sc
                stream=None):
     """One AdamW step over the plan's tensors, in place (fp4q_adamw_step).
     step counts from 1; seed: the stochastic rounding of 8-bit moments;
-    grad_scale: a device fp32 scalar that multiplies the gradients."""
+    grad_scale: a device fp32 scalar that multiplies the gradients.  A graph
+    that captured the step reads the plan's memory at every replay: the plan is
+    kept as long as the graph."""
     if grad_scale is not None:
         _need_cuda(grad_scale)
         _need(grad_scale, "grad_scale", _torch().float32)
+    handle = _stream(stream)
     if plan.table is None:
         _check(lib().fp4q_adamw_step(plan.array, plan.n, plan.bits, plan.grad_dtype, lr, beta1, beta2,
-                                     eps, step, seed, _ptr(grad_scale), _stream(stream)))
+                                     eps, step, seed, _ptr(grad_scale), handle))
     else:
+        plan.read_on(handle, stream)
         _check(lib().fp4q_adamw_step_table(plan.table.data_ptr(), plan.n, plan.chunks, plan.bits,
                                            plan.grad_dtype, lr, beta1, beta2, eps, step, seed,
-                                           _ptr(grad_scale), _stream(stream)))
+                                           _ptr(grad_scale), handle))

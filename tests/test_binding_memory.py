@@ -103,3 +103,33 @@ def test_what_a_call_allocates_belongs_to_its_stream(world, call, made):
     call(stream=world["main"])
     assert len(MADE) == 2 * made
     assert all(t.owner == "main" and not t.recorded for t in MADE)
+
+
+def plan(n=50, **kw):
+    t = [dev(torch.zeros(8)) for _ in range(n)]
+    return fq.adamw_plan(t, t, t, t, **kw)
+
+
+def test_a_plans_table_outlives_the_steps_that_read_it(world, monkeypatch):
+    """A step on another stream than the one that made the table still reads it
+    when the plan is dropped: the pool has to know of that stream."""
+    def tables(*a):
+        a[4]._obj.value, a[5]._obj.value = 4096, 50
+        return 0
+    fq._lib.fp4q_adamw_table = tables
+    made = dev(torch.zeros(4096, dtype=torch.uint8))
+    made.recorded = set()
+    monkeypatch.setattr(torch.Tensor, "to", lambda self, device: made)
+    p = plan()
+    assert p.table is made
+    fq.adamw_step(p, 1e-3, 1)
+    fq.adamw_step(p, 1e-3, 1, stream=world["main"])
+    assert not made.recorded
+    fq.adamw_step(p, 1e-3, 2, stream=world["side"])
+    assert made.recorded == {"side"}
+    made.recorded.clear()
+    p = plan()
+    with torch.cuda.stream(world["side"]):
+        fq.adamw_step(p, 1e-3, 1)
+    assert made.recorded == {"side"}
+    assert fq._lib.calls[-1][1][-1] == world["side"].cuda_stream
