@@ -828,7 +828,8 @@ def layer_norm_grad(dy, x, weight, mean, rstd, kind=LAYER_NORM, dx=None, want_we
 
 class AdamwPlan:
     """The tensors of an AdamW step, checked once (see adamw_plan).  Holds
-    references to them and, for more tensors than one launch takes as kernel
+    their memory (through tensors of its own, which a later `param.data = ...`
+    leaves as they are) and, for more tensors than one launch takes as kernel
     arguments, their table in device memory."""
     ARGUMENTS = 44
 
@@ -876,7 +877,13 @@ def adamw_plan(params, grads, exp_avg, exp_avg_sq, exp_avg_scales=None, exp_avg_
     dtype; exp_avg, exp_avg_sq: fp32, or uint8 (E4M3 codes of m and of
     sqrt(v)) with the uint8 scales, ceil(numel/32) per tensor; copies: bf16
     tensors to receive the new params, or None; weight_decay: a number, or
-    one per tensor."""
+    one per tensor.
+
+    A plan is of addresses and holds the memory behind them.  It is made anew
+    when a tensor gets other memory (gradients that are set to None and made
+    again, param.data = ...): an old plan would step with the old gradients and
+    write to the old parameters.  Gradients that are zeroed in place, or
+    written over as layer_norm_grad's dweight= and gemm's c= do, keep theirs."""
     torch = _torch()
     n = len(params)
     bits = 8 if exp_avg_scales is not None else 32
@@ -913,7 +920,8 @@ def adamw_plan(params, grads, exp_avg, exp_avg_sq, exp_avg_scales=None, exp_avg_
         array[i] = AdamwTensor(*(0 if t is None else t.data_ptr() for t in (p, g, m, v, ms, vs, c)),
                                k, wd)
     return AdamwPlan(array, n, bits, BF16 if gdtype == torch.bfloat16 else F32,
-                     list(zip(*list(cols.values())[:-1])))
+                     [tuple(t if t is None else t.detach() for t in row)
+                      for row in zip(*list(cols.values())[:-1])])
 
 
 def adamw_step(plan, lr, step, beta1=0.9, beta2=0.999, eps=1e-8, seed=0, grad_scale=None,

@@ -133,3 +133,17 @@ def test_a_plans_table_outlives_the_steps_that_read_it(world, monkeypatch):
         fq.adamw_step(p, 1e-3, 1)
     assert made.recorded == {"side"}
     assert fq._lib.calls[-1][1][-1] == world["side"].cuda_stream
+
+
+def test_a_plan_holds_the_memory_it_writes_to(world):
+    """A tensor may be given other memory (param.data = ...) behind the plan's
+    back: what the plan's addresses name stays allocated all the same."""
+    new = [dev(torch.zeros(8)) for _ in range(6)]
+    new[5] = new[5].bfloat16()
+    p = fq.adamw_plan(*([t] for t in new[:4]), copies=[new[5]])
+    for t in new:
+        t.data = torch.ones(8, dtype=t.dtype)
+    at = p.array[0]
+    held = [t for t in p.tensors[0] if t is not None]
+    assert [t.data_ptr() for t in held] == [at.param, at.grad, at.exp_avg, at.exp_avg_sq, at.copy]
+    assert at.param != new[0].data_ptr()
