@@ -816,6 +816,8 @@ def layer_norm_grad(dy, x, weight, mean, rstd, kind=LAYER_NORM, dx=None, want_we
             nbytes = lib().fp4q_layer_norm_grad_workspace_bytes(R, C)
             workspace = empty((nbytes,), (1,), _torch().uint8)
         else:
+            _need_cuda(workspace)
+            _need(workspace, "workspace", workspace.dtype)
             nbytes = workspace.numel() * workspace.element_size()
     status = lib().fp4q_layer_norm_grad(kind, dy.data_ptr(), _dt(dy), lddy, x.data_ptr(), _dt(x), R, C,
                                         ldx, _ptr(weight), wdt, _ptr(mean), _ptr(rstd),

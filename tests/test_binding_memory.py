@@ -147,3 +147,17 @@ def test_a_plan_holds_the_memory_it_writes_to(world):
     held = [t for t in p.tensors[0] if t is not None]
     assert [t.data_ptr() for t in held] == [at.param, at.grad, at.exp_avg, at.exp_avg_sq, at.copy]
     assert at.param != new[0].data_ptr()
+
+
+def test_norm_grad_refuses_workspaces_that_are_not_device_bytes(world):
+    """A host workspace, or one whose elements do not lie one behind the other
+    (expanded: many elements in the memory of one)."""
+    with pytest.raises(ValueError, match="device"):
+        norm_grad(workspace=torch.zeros(4096, dtype=torch.uint8))
+    for bad in (u8(1).expand(4096), u8(8192)[::2]):
+        with pytest.raises(ValueError, match="contiguous"):
+            norm_grad(workspace=bad)
+    assert not fq._lib.calls
+    norm_grad(workspace=u8(4096))
+    norm_grad(workspace=dev(torch.zeros(32, 32)))
+    assert [a[-2] for _, a in fq._lib.calls] == [4096, 4096]
