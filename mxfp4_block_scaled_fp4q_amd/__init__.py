@@ -936,6 +936,8 @@ def adamw_step(plan, lr, step, beta1=0.9, beta2=0.999, eps=1e-8, seed=0, grad_sc
     if grad_scale is not None:
         _need_cuda(grad_scale)
         _need(grad_scale, "grad_scale", _torch().float32)
+        if grad_scale.numel() != 1:
+            raise ValueError(f"grad_scale must have one element, got {grad_scale.numel()}")
     handle = _stream(stream)
     if plan.table is None:
         _check(lib().fp4q_adamw_step(plan.array, plan.n, plan.bits, plan.grad_dtype, lr, beta1, beta2,

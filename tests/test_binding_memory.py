@@ -161,3 +161,15 @@ def test_norm_grad_refuses_workspaces_that_are_not_device_bytes(world):
     norm_grad(workspace=u8(4096))
     norm_grad(workspace=dev(torch.zeros(32, 32)))
     assert [a[-2] for _, a in fq._lib.calls] == [4096, 4096]
+
+
+def test_grad_scale_is_one_element(world):
+    """Of an empty tensor the address is null, which stands for a scale of 1."""
+    p = plan(2)
+    for bad in (dev(torch.zeros(0)), dev(torch.ones(2))):
+        with pytest.raises(ValueError, match="one element"):
+            fq.adamw_step(p, 1e-3, 1, grad_scale=bad)
+    assert not fq._lib.calls
+    for good in (dev(torch.tensor(0.5)), dev(torch.ones(1))):
+        fq.adamw_step(p, 1e-3, 1, grad_scale=good)
+        assert fq._lib.calls[-1][1][-2] == good.data_ptr()
