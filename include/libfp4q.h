@@ -540,7 +540,7 @@ fp4q_status_t fp4q_gemm_gated(int64_t M, int64_t F, int64_t K, const uint8_t* x_
  *   a quantisation of that buffer is the operand of the input gradient,
  *   fp4q_gemm over K = 2F, and of the weight gradients.
  *   D is not rounded before the products.  Sizes and alignment as
- *   fp4q_gemm_gated (w_scales 16-byte aligned).
+ *   fp4q_gemm_gated (w_scales 16-byte aligned); with F < 8, M <= 2^29 - 32.
  */
 fp4q_status_t fp4q_gemm_gated_grad(int64_t M, int64_t F, int64_t K, const uint8_t* dy_codes,
                                    const uint8_t* dy_scales, const uint8_t* w_codes,

@@ -44,7 +44,8 @@ static_assert(fp4q::kHcpStaticScratchBytes == FP4Q_HCP_NOALLOC_MAX_BYTES,
 constexpr int64_t kMaxElems = (int64_t)1 << 33;
 
 // Sizes that the gated calls share (as fp4q_gemm's; a launch holds below 2^32
-// threads, 512 to a tile).
+// threads: 512 to a tile, but for the gradient of rows below 8 elements, which
+// takes tiles of 32 rows and 256 threads whatever M is).
 fp4q_status_t gated_sizes(const char* who, int64_t M, int64_t F, int64_t K) {
     if (M <= 0 || F <= 0 || K <= 0) return fail(FP4Q_ERR_INVALID, "%s: bad sizes", who);
     if (K % 64) return fail(FP4Q_ERR_INVALID, "%s: K %% 64 != 0", who);
@@ -745,6 +746,8 @@ fp4q_status_t fp4q_gemm_gated_grad(int64_t M, int64_t F, int64_t K, const uint8_
         return fail(FP4Q_ERR_INVALID, "gemm_gated_grad: bad act %d", (int)act);
     const fp4q_status_t e = gated_sizes("gemm_gated_grad", M, F, K);
     if (e != FP4Q_OK) return e;
+    if (F < 8 && (M + 31) / 32 >= ((int64_t)1 << 24))
+        return fail(FP4Q_ERR_UNSUPPORTED, "gemm_gated_grad: too many tiles");
     if (ld_gu < F || ld_d < F)
         return fail(FP4Q_ERR_INVALID, "gemm_gated_grad: row stride below F");
     if (!aligned16(dy_codes) || !aligned16(dy_scales) || !aligned16(w_codes) ||

@@ -184,3 +184,13 @@ def test_adamw_step_table_refusals(L, kw, status):
     assert L.fp4q_adamw_step_table(*a.values(), NUL) == status
     assert "adamw_step_table" in L.fp4q_last_error().decode()
     assert L.fp4q_adamw_step_table(NUL, 0, 0, 32, 0, 1e-3, 0.9, 0.95, 1e-8, 1, 0, NUL, NUL) == 0
+
+
+@pytest.mark.parametrize("F", [1, 7])
+def test_gated_grad_rows_below_8_elements_have_a_row_limit(L, F):
+    """Such rows are 32 to a workgroup of 256 threads, and a launch holds below
+    2^32 threads."""
+    for M in (1 << 29, (1 << 29) - 31, (1 << 30) - 1):
+        assert L.fp4q_gemm_gated_grad(M, F, 64, FAKE, FAKE, FAKE, FAKE, 0, FAKE, FAKE, F, FAKE, FAKE, F,
+                                      NUL) == 2
+        assert "too many tiles" in L.fp4q_last_error().decode()
