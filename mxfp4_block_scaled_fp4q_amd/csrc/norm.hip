@@ -417,16 +417,19 @@ __global__ __launch_bounds__(MULTI ? 1024 : 256) void norm_grad_kernel(
 }
 
 // Adds up the rows of partial sums: 16 columns per workgroup, 64 groups of 16
-// lanes over the rows, so that few loads follow each other.
+// lanes over the rows, so that few loads follow each other.  group0: the first
+// workgroup's number, since a launch holds below 2^32 threads.
+constexpr int64_t kJoinGroups = 1 << 21;
 __global__ __launch_bounds__(1024) void norm_grad_join_kernel(const float* __restrict__ part,
                                                               int64_t cols, int slabs,
                                                               float* __restrict__ dw,
-                                                              float* __restrict__ db) {
+                                                              float* __restrict__ db,
+                                                              int64_t group0) {
     __shared__ float red[16][16];
     float* out = blockIdx.y == 0 ? dw : db;
     if (!out) return;
     const int l = threadIdx.x & 15, wave = threadIdx.x >> 6;
-    const int64_t c = (int64_t)blockIdx.x * 16 + l;
+    const int64_t c = (group0 + blockIdx.x) * 16 + l;
     float s = 0.0f;
     if (c < cols) {
         const float* p = part + blockIdx.y * cols + c;
@@ -633,9 +636,10 @@ static void go_grad(const NormShape sh, const void* dy, int64_t lddy, const void
 #undef FP4Q_GO
         if (slabs == 1) return;
     }
-    if (dw || db)
-        FP4Q_LAUNCH(norm_grad_join_kernel, dim3((unsigned)((cols + 15) / 16), 2), dim3(1024), 0, s,
-                    part, cols, slabs, dw, db);
+    const int64_t groups = dw || db ? (cols + 15) / 16 : 0;
+    for (int64_t g = 0; g < groups; g += kJoinGroups)
+        FP4Q_LAUNCH(norm_grad_join_kernel, dim3((unsigned)std::min(groups - g, kJoinGroups), 2),
+                    dim3(1024), 0, s, part, cols, slabs, dw, db, g);
 }
 
 hipError_t launch_norm_grad(const void* dy, int dydtype, int64_t lddy, const void* x, int xdtype,
