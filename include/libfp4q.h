@@ -558,7 +558,12 @@ fp4q_status_t fp4q_gemm_gated_grad(int64_t M, int64_t F, int64_t K, const uint8_
  *   w_dtype, NULL for ones and zeros; mean, rstd: fp32 [rows], written for
  *   the gradient, NULL to skip (mean is not written with FP4Q_RMS_NORM).
  *   The squares are summed around the mean, in fp32.  eps >= 0.  Any cols;
- *   every pointer needs only its element's alignment.  A row holding Inf or NaN gives NaN in that row alone.
+ *   every pointer needs only its element's alignment.  Inf and NaN stay in
+ *   their row.  A NaN, and with FP4Q_LAYER_NORM an Inf, makes the whole row
+ *   NaN.  With FP4Q_RMS_NORM an Inf makes rstd 0: y is NaN at the Inf and the
+ *   bias elsewhere.  Finite elements whose squares overflow fp32 make rstd 0
+ *   too (either kind), and y the bias throughout; where their sum overflows,
+ *   FP4Q_LAYER_NORM gives a NaN row.
  */
 typedef enum { FP4Q_LAYER_NORM = 0, FP4Q_RMS_NORM = 1 } fp4q_norm_t;
 fp4q_status_t fp4q_layer_norm(fp4q_norm_t kind, const void* x, fp4q_dtype_t x_dtype, int64_t rows,

@@ -246,3 +246,29 @@ def test_other_stream_and_graph_replays():
         torch.cuda.synchronize()
         assert all(np.array_equal(host_bits(a), c) for a, c in zip(out, want))
         step()
+
+
+@pytest.mark.parametrize("C", [5, 300, 1500, 20000])
+def test_rms_rows_with_an_infinity_and_overflowing_squares(C):
+    """RMS norm: the sum of squares is infinite, so rstd is 0, the infinity
+    itself NaN and the row's finite elements the bias; a NaN takes the row.
+    Squares beyond fp32 act alike in either kind, with no NaN."""
+    w, b = torch.randn(2, C, device="cuda")
+    for dt in (torch.bfloat16, torch.float32):
+        x = torch.randn(5, C, device="cuda").to(dt)
+        ref = fq.layer_norm(x, w, b, kind=fq.RMS_NORM)[0]
+        x2 = x.clone()
+        x2[1, C // 2], x2[3, C - 1] = float("-inf"), float("nan")
+        y, _, rstd = fq.layer_norm(x2, w, b, kind=fq.RMS_NORM)
+        want = b.to(dt).clone()
+        want[C // 2] = float("nan")
+        assert torch.equal(y[1].isnan(), want.isnan())
+        assert torch.equal(y[1].nan_to_num(), want.nan_to_num()) and rstd[1] == 0
+        assert y[3].isnan().all() and rstd[3].isnan()
+        assert torch.equal(y[[0, 2, 4]], ref[[0, 2, 4]])
+        for kind in KINDS:
+            x2 = x.clone()
+            x2[2, 0] = 1e25
+            y, _, rstd = fq.layer_norm(x2, w, b, kind=kind)
+            assert rstd[2] == 0 and torch.equal(y[2], b.to(dt))
+            assert torch.isfinite(y).all()
