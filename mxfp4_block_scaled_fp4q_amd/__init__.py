@@ -164,6 +164,8 @@ def _allocator(t, stream):
     """An f(size, stride, dtype) that makes uninitialised contiguous tensors on
     t's device: torch's shortest way to one where this torch has it and the
     device is the current one (0.7 us a tensor against 1.4), else new_empty.
+    The short way passes the dispatcher by, so it is not taken where a dispatch
+    mode watches or deterministic algorithms ask for memory that is filled.
 
     The tensors belong to `stream`, which the call's kernels run on: memory of
     the current stream's pool may still be in use by that stream's pending work,
@@ -183,8 +185,10 @@ def _allocator(t, stream):
     c = _torch()._C
     if _empty_strided_cuda is None:
         guards = getattr(getattr(c, "_dynamo", None), "guards", None)
-        _empty_strided_cuda = getattr(guards, "_empty_strided_cuda", False)
-    if _empty_strided_cuda and t.get_device() == c._cuda_getDevice():
+        _empty_strided_cuda = (hasattr(c, "_len_torch_dispatch_stack")
+                               and getattr(guards, "_empty_strided_cuda", False))
+    if (_empty_strided_cuda and t.get_device() == c._cuda_getDevice()
+            and not c._len_torch_dispatch_stack() and not c._get_deterministic_algorithms()):
         return _empty_strided_cuda
     return lambda size, stride, dtype: t.new_empty(size, dtype=dtype)
 

@@ -173,3 +173,35 @@ def test_grad_scale_is_one_element(world):
     for good in (dev(torch.tensor(0.5)), dev(torch.ones(1))):
         fq.adamw_step(p, 1e-3, 1, grad_scale=good)
         assert fq._lib.calls[-1][1][-2] == good.data_ptr()
+
+
+def test_dispatch_modes_and_deterministic_fill_see_the_allocations(world, monkeypatch):
+    """torch's short way to an allocation passes the dispatcher by; a call goes
+    the long way where somebody watches it or wants fresh memory filled."""
+    from torch.utils._python_dispatch import TorchDispatchMode
+
+    class Watch(TorchDispatchMode):
+        def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+            return func(*args, **(kwargs or {}))
+    short = []
+
+    def shortest(size, stride, dtype):
+        short.append(size)
+        return dev(torch.zeros(size, dtype=dtype))
+    monkeypatch.setattr(fq, "_empty_strided_cuda", shortest)
+    monkeypatch.setattr(Dev, "get_device", lambda self: 0)
+    norm()
+    gated()
+    assert len(short) == 5 and not MADE
+    with Watch():
+        norm()
+        gated()
+    assert len(short) == 5 and len(MADE) == 5
+    torch.use_deterministic_algorithms(True)
+    try:
+        norm()
+    finally:
+        torch.use_deterministic_algorithms(False)
+    assert len(short) == 5 and len(MADE) == 8
+    norm()
+    assert len(short) == 8
