@@ -703,7 +703,8 @@ def gemm_gated_grad(dy_codes, dy_scales, w_codes, w_scales, gate, up, act=SILU, 
     """Gradients of the gated block's two products behind its down projection
     (fp4q_gemm_gated_grad): dy_codes [M, K/2], w_codes [F, K/2], gate and up
     bf16 [M, F] as gemm_gated returned them.  Returns (d_gate, d_up), bf16,
-    the halves of one [M, 2F] tensor unless given."""
+    the halves of one [M, 2F] tensor unless given (not in gate's or up's
+    memory)."""
     bf16 = _torch().bfloat16
     M, K = _codes(dy_codes, dy_scales, "dy")
     F, _ = _codes(w_codes, w_scales, "w", K=K)

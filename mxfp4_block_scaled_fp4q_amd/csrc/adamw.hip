@@ -13,8 +13,8 @@
 // moves by far less than half of E4M3's step (1/8 to 1/16), so rounding to
 // nearest would leave it where it is, while the stochastic one moves it by
 // the right amount on average.  The random bits are Philox4x32-10 with the
-// seed as key, counter (position / 4, 0, step, 0), one 32-bit word per
-// element: the low half rounds m, the high half r.  An element's position is
+// seed as key, counter (low and high word of position / 4, step, 0), one
+// 32-bit word per element: the low half rounds m, the high half r.  An element's position is
 // its index plus the rounded-up-to-32 sizes of the tensors before it.
 //
 // Bound by memory: param, gradient and moments are read once and written once

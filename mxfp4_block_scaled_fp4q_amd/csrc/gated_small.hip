@@ -210,7 +210,14 @@ static void go(const GatedCall& g, hipStream_t s) {
 //                         512 x 1408 x 960  (1408)   9.1,  6.4,  6.1;  9.5
 //                         512 x 1408 x 2048 (1408)  20.8, 14.7, 14.8; 12.1
 // Up to 16 rows a second round is taken too, since what larger tiles would share
-// are rows of A, and at short K, where the LDS tiles' start counts for more.
+// are rows of A: 5632 x 2048 (352 groups) with 1, 4, 8 and 16 rows 7.1, 7.5, 7.8
+// and 8.5 us, 32 x 32 tiles 7.3, 7.5, 7.7 and 7.9, LDS tiles 7.8 to 8.0; so at 16
+// rows the rule gives away 0.5 us there, and at 6660 x 4032 (417) 0.6 of 14.4.  At
+// short K a second round is taken too, where the LDS tiles' start counts for more.
+// The gradient's 32 x 64 tiles past one round: where groups and K together stay
+// below what 352 groups take at K = 1024 (512 x 1408: 6.0 us against 9.2 of the LDS
+// tiles at K = 960, 8.8 and 9.1 at 1024; at 1088, past the limit, 6.6 and 9.8, but
+// 2000 x 2000 x 192, as much in more groups, 14.8 and 11.3).
 bool launch_gated_small(const GatedCall& g, bool grad, int gelu, hipStream_t s) {
     auto groups = [&](int64_t bm, int64_t bn) { return (g.M + bm - 1) / bm * ((g.F + bn - 1) / bn); };
     const int64_t K = g.K;

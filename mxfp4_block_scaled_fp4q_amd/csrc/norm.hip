@@ -548,13 +548,19 @@ constexpr int64_t kAnyGrid = 1 << 16;
 
 // Workgroups of a walk over the rows: what 256 compute units hold of them at
 // `waves` waves each, and at least `min_rows` rows to a workgroup (or to each
-// of its four waves).  Forward, 16, 24 and 32 waves: 16384 x 5120 bf16 118, 80
-// and 85 us (ten waves per row: 16 is one workgroup), fp32 119, 126 and 146.
-// Backward, 16, 24 and 32: 100, 101 and 116 us.  There a walk costs a latency
-// per row and each workgroup a row of partial sums to write and join: 2, 4, 8,
-// 16 rows take 7.2, 7.3, 9.1, 13.5 us at 400 x 1024, 17.4, 14.0, 12.0, 15.1 at
-// 1999 x 1111, 9.9, 8.3, 9.2, 12.0 at 4000 x 300 (four rows at a time) and 29.4,
-// 29.3, 29.5, 26.7 at 8192 x 2048.
+// of its four waves).  Forward, 16, 24 and 32 waves: 16384 x 5120 bf16 77, 66
+// and 72 us (ten waves per row: 16 is one workgroup), fp32 125, 129 and 151,
+// 16384 x 8192 bf16 101, 98 and 96, 8192 x 2048 15.8, 14.8 and 14.7.  Backward:
+// 16384 x 5120 bf16 98, 105 and 112, fp32 184, 195 and 203, 16384 x 8192 152,
+// 153 and 164.  There a walk costs a latency per row and each workgroup a row
+// of partial sums to write and join: 2, 4, 8, 16 rows take 7.3, 7.2, 8.9, 13.3
+// us at 400 x 1024, 18.0, 15.3, 13.6, 17.8 at 1999 x 1111 fp32, 9.8, 8.6, 9.3,
+// 12.2 at 4000 x 300 fp32 (four rows at a time) and 26.3, 26.2, 26.2, 25.3 at
+// 8192 x 2048.  The width hardly moves the best: 19.0, 18.9, 18.4, 23.7 at
+// 1024 x 5120, 19.3, 19.2, 18.7, 24.1 with a row more, 21.9, 21.7, 21.7, 25.5 at
+// 2040 x 5120, 30.3 to 30.6 at 4096 x 5120 and 19.6, 18.4, 19.5, 28.2 at 500 x
+// 8192, so the rule asks for the rows alone (its step past 1024 rows, 256 to 129
+// workgroups at 5120 columns, costs nothing).
 constexpr int kNormWaves = 24, kGradWaves = 16;
 static int norm_groups(const NormShape& sh, int64_t rows, int waves, int min_rows) {
     const int64_t per = (int64_t)min_rows * (sh.multi ? 1 : 4);
