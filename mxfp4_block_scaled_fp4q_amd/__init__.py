@@ -152,7 +152,7 @@ def _dt(t):
 def _stream(stream):
     if stream is not None:
         return stream.cuda_stream
-    c = _torch()._C
+    c = (_torch_module or _torch())._C
     # the current stream's handle, without building a Stream object per call
     return c._cuda_getCurrentRawStream(c._cuda_getDevice())
 
@@ -182,7 +182,7 @@ def _allocator(t, stream):
                 out.record_stream(current)
                 return out
             return on_stream
-    c = _torch()._C
+    c = (_torch_module or _torch())._C
     if _empty_strided_cuda is None:
         guards = getattr(getattr(c, "_dynamo", None), "guards", None)
         _empty_strided_cuda = (hasattr(c, "_len_torch_dispatch_stack")
@@ -193,10 +193,11 @@ def _allocator(t, stream):
     return lambda size, stride, dtype: t.new_empty(size, dtype=dtype)
 
 
-def _halves(t, rows, cols, stream):
-    """The two [rows, cols] halves of one bf16 [rows, 2 cols] tensor."""
+def _halves(empty, rows, cols, dtype):
+    """The two [rows, cols] halves of one [rows, 2 cols] tensor that `empty`
+    (an _allocator) makes."""
     ld = 2 * cols
-    both = _allocator(t, stream)((rows, ld), (ld, 1), _torch().bfloat16)
+    both = empty((rows, ld), (ld, 1), dtype)
     return both.as_strided((rows, cols), (ld, 1)), both.as_strided((rows, cols), (ld, 1), cols)
 
 
@@ -677,16 +678,16 @@ def gemm_gated(x_codes, x_scales, gate_codes, gate_scales, up_codes, up_scales, 
     _codes(up_codes, up_scales, "up", F, K)
     if (gate is None) != (up is None):
         raise ValueError("gate and up are given both or neither")
-    ldgu = 0
+    ldgu, empty = 0, _allocator(x_codes, stream)
     if gate is not None:
         ldgu = _rows(gate, "gate", bf16, (M, F))
         if _rows(up, "up", bf16, (M, F)) != ldgu:
             raise ValueError("gate and up must have the same row stride")
     elif save:
-        gate, up = _halves(x_codes, M, F, stream)
+        gate, up = _halves(empty, M, F, bf16)
         ldgu = 2 * F
     if h is None:
-        h, ldh = _allocator(x_codes, stream)((M, F), (F, 1), bf16), F
+        h, ldh = empty((M, F), (F, 1), bf16), F
     else:
         ldh = _rows(h, "h", bf16, (M, F))
     status = lib().fp4q_gemm_gated(
@@ -714,7 +715,7 @@ def gemm_gated_grad(dy_codes, dy_scales, w_codes, w_scales, gate, up, act=SILU, 
     if (d_gate is None) != (d_up is None):
         raise ValueError("d_gate and d_up are given both or neither")
     if d_gate is None:
-        d_gate, d_up = _halves(dy_codes, M, F, stream)
+        d_gate, d_up = _halves(_allocator(dy_codes, stream), M, F, bf16)
         ldd = 2 * F
     else:
         ldd = _rows(d_gate, "d_gate", bf16, (M, F))
