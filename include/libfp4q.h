@@ -29,7 +29,8 @@
  * All pointers must be 16-byte aligned and every row stride (in bytes) a
  * multiple of 16, or the call returns FP4Q_ERR_ALIGNMENT; the one exception
  * is fp4q_gemm's C, which only needs its element alignment (any ld_c >= N),
- * besides what the gated, norm and AdamW calls state for themselves.
+ * besides what the gated, norm, gradient-norm and AdamW calls state for
+ * themselves.
  */
 #ifndef LIBFP4Q_H
 #define LIBFP4Q_H
@@ -592,6 +593,119 @@ fp4q_status_t fp4q_layer_norm_grad(fp4q_norm_t kind, const void* dy, fp4q_dtype_
                                    fp4q_dtype_t w_dtype, const float* mean, const float* rstd,
                                    void* dx, int64_t ld_dx, float* dweight, float* dbias,
                                    void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * fp4q_residual_norm -- the norms behind and in front of a block, fused with
+ * the block's gate and the residual sum:
+ *   n     = post(branch)                        post: post_kind, post_weight, post_bias
+ *   x_out = x_scale x + branch_scale gate n
+ *   y     = norm(x_out)                         norm: kind, weight, bias
+ *   (the norms as in fp4q_layer_norm; with post_kind FP4Q_NO_NORM n = branch and
+ *   post_weight and post_bias are NULL)
+ *   x: bf16 or fp32 [rows, cols], row stride ld_x; branch: bf16 or fp32 (either
+ *   with either), row stride ld_b; x_out: of x_dtype, row stride ld_xo (may be
+ *   x's memory, element for element).  y is formed from x_out before its
+ *   rounding.
+ *   gate: of gate_dtype, NULL for ones; row r of the operands takes row
+ *   r / gate_rows of the gate, which has ceil(rows / gate_rows) rows of stride
+ *   ld_gate: gate_rows >= rows for one vector, 1 for a gate per row, the length
+ *   of a sequence for a gate per sequence.
+ *   post_weight, post_bias, weight, bias: [cols] of w_dtype, NULL for ones and
+ *   zeros.  One eps for both norms, eps >= 0.
+ *   The result is y (bf16 or fp32, row stride ld_y), or, where y is NULL, codes
+ *   [rows, cols/2] and scales [rows, cols/32]: exactly fp4q_quantize(y in fp32,
+ *   block 32, FP4Q_BLOCK_ROW, FP4Q_RNE).  Codes need cols % 32 == 0 and 16-byte
+ *   aligned codes; other pointers need their element's alignment.
+ *   post_mean, post_rstd, mean, rstd: fp32 [rows], written for the gradient, NULL
+ *   to skip (means are not written with FP4Q_RMS_NORM, the first two not with
+ *   FP4Q_NO_NORM).
+ *   Any rows and cols below 2^31.  Inf and NaN stay in their row, in which they
+ *   act as in fp4q_layer_norm.
+ */
+#define FP4Q_NO_NORM ((fp4q_norm_t)2)
+fp4q_status_t fp4q_residual_norm(int64_t rows, int64_t cols, const void* x, fp4q_dtype_t x_dtype,
+                                 int64_t ld_x, const void* branch, fp4q_dtype_t b_dtype,
+                                 int64_t ld_b, fp4q_norm_t post_kind, const void* post_weight,
+                                 const void* post_bias, const void* gate, fp4q_dtype_t gate_dtype,
+                                 int64_t gate_rows, int64_t ld_gate, double x_scale,
+                                 double branch_scale, fp4q_norm_t kind, const void* weight,
+                                 const void* bias, fp4q_dtype_t w_dtype, double eps, void* x_out,
+                                 int64_t ld_xo, void* y, fp4q_dtype_t y_dtype, int64_t ld_y,
+                                 uint8_t* codes, uint8_t* scales, float* post_mean,
+                                 float* post_rstd, float* mean, float* rstd, void* stream);
+
+/*
+ * fp4q_residual_norm_grad -- its backward pass, from dy and the gradient dx_out
+ * that arrives at x_out along the residual stream (NULL for none).  With
+ * xh = (x_out - mean) rstd, t = dy weight, nh = (branch - post_mean) post_rstd
+ * (nh = branch with FP4Q_NO_NORM):
+ *   D  = dx_out + rstd (t - mean_c(t) - xh mean_c(t xh))     dx = x_scale D
+ *   u  = branch_scale gate D post_weight
+ *   dbranch = post_rstd (u - mean_c(u) - nh mean_c(u nh))    (FP4Q_NO_NORM: u)
+ *   (FP4Q_RMS_NORM: without its mean_c(t) or mean_c(u))
+ *   dweight = sum over rows of dy xh,  dbias = sum over rows of dy
+ *   dpost_weight, dpost_bias = sums over rows of branch_scale gate D nh and of
+ *   branch_scale gate D;  dgate = sum over the rows of each gate row of
+ *   branch_scale D n, n = nh post_weight + post_bias
+ *   dy: bf16 or fp32; dx_out and dx: of x_dtype; branch and dbranch: of b_dtype;
+ *   each with its row stride.  dx may be dx_out's memory, dbranch branch's, and
+ *   either dy's where the types agree, element for element.  x_out and the
+ *   statistics as the forward call wrote them, the other operands as it was
+ *   given them.  branch may be NULL with FP4Q_NO_NORM where dgate is NULL.
+ *   dpost_weight, dpost_bias, dweight, dbias: fp32 [cols]; dgate: fp32 [gate
+ *   rows, cols], dense; all written (not added to), NULL to skip any (the first
+ *   two are NULL with FP4Q_NO_NORM, dgate without a gate).
+ *   workspace >= fp4q_residual_norm_grad_workspace_bytes(rows, cols, gate_rows)
+ *   device bytes (gate_rows = 0 without a gate), 16-byte aligned.  Sums in fp32
+ *   in an order that depends on the sizes alone.
+ */
+size_t fp4q_residual_norm_grad_workspace_bytes(int64_t rows, int64_t cols, int64_t gate_rows);
+fp4q_status_t fp4q_residual_norm_grad(
+    int64_t rows, int64_t cols, const void* dy, fp4q_dtype_t dy_dtype, int64_t ld_dy,
+    const void* dx_out, int64_t ld_dxo, const void* x_out, fp4q_dtype_t x_dtype, int64_t ld_xo,
+    const void* branch, fp4q_dtype_t b_dtype, int64_t ld_b, fp4q_norm_t post_kind,
+    const void* post_weight, const void* post_bias, const void* gate, fp4q_dtype_t gate_dtype,
+    int64_t gate_rows, int64_t ld_gate, double x_scale, double branch_scale, fp4q_norm_t kind,
+    const void* weight, fp4q_dtype_t w_dtype, const float* post_mean, const float* post_rstd,
+    const float* mean, const float* rstd, void* dx, int64_t ld_dx, void* dbranch, int64_t ld_db,
+    float* dpost_weight, float* dpost_bias, float* dgate, float* dweight, float* dbias,
+    void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * fp4q_grad_norm -- the norm of many gradients taken as one vector, and the
+ * factor that clips it:
+ *   norm  = sqrt(sum g^2) (FP4Q_NORM_L2) or max |g| (FP4Q_NORM_MAX)
+ *   scale = min(1, max_norm / (norm + eps))
+ *   tensors: HOST array of n descriptors, read during the call only: `numel`
+ *   consecutive elements of fp32 or bf16 each, element-aligned; numel = 0 is
+ *   skipped.  No tensor, or no element, has norm 0.
+ *   norm, scale: device fp32, written; either may be NULL.  scale is what
+ *   fp4q_adamw_step takes as grad_scale, or fp4q_grad_scale below.
+ *   max_norm, eps >= 0 and finite.  Squares and sums in 64 bits, so that no
+ *   fp32 gradient overflows; a NaN in a gradient makes both results NaN, an Inf
+ *   (and no NaN) the norm Inf and the scale 0.
+ *   workspace >= fp4q_grad_norm_workspace_bytes(tensors, n) device bytes,
+ *   16-byte aligned.  The descriptors travel as kernel arguments (192 tensors to
+ *   a launch), so a call can be captured into a graph.  Deterministic.
+ */
+typedef enum { FP4Q_NORM_L2 = 0, FP4Q_NORM_MAX = 1 } fp4q_norm_order_t;
+typedef struct fp4q_tensor {
+    void* data;
+    int64_t numel;
+    int64_t dtype; /* fp4q_dtype_t */
+} fp4q_tensor_t;
+size_t fp4q_grad_norm_workspace_bytes(const fp4q_tensor_t* tensors, int32_t n);
+fp4q_status_t fp4q_grad_norm(const fp4q_tensor_t* tensors, int32_t n, fp4q_norm_order_t order,
+                             double max_norm, double eps, float* norm, float* scale,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * fp4q_grad_scale -- every element of the tensors times *scale (device fp32), in
+ * place, each rounded to its type.  Tensors as in fp4q_grad_norm; those of one
+ * call must not overlap.  With *scale = 1 nothing is read or written.
+ */
+fp4q_status_t fp4q_grad_scale(const fp4q_tensor_t* tensors, int32_t n, const float* scale,
+                              void* stream);
 
 /*
  * fp4q_adamw_step -- one AdamW step over many tensors:

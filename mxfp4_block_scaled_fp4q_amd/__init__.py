@@ -17,7 +17,8 @@ ROW, COL = 0, 1
 RNE, SR = 0, 1
 STE, DGE = 0, 1
 SILU, GELU = 0, 1
-LAYER_NORM, RMS_NORM = 0, 1
+LAYER_NORM, RMS_NORM, NO_NORM = 0, 1, 2
+NORM_L2, NORM_MAX = 0, 1
 
 STATUS = {0: "FP4Q_OK", 1: "FP4Q_ERR_INVALID", 2: "FP4Q_ERR_UNSUPPORTED",
           3: "FP4Q_ERR_ALIGNMENT", 4: "FP4Q_ERR_WORKSPACE", 5: "FP4Q_ERR_HIP"}
@@ -32,7 +33,9 @@ EXPORTS = ["fp4q_channel_mask", "fp4q_quantize_masked", "fp4q_gemm_hcp_split",
            "fp4q_occ_workspace_bytes", "fp4q_occ_quantize", "fp4q_occ_spmm",
            "fp4q_gemm_gated", "fp4q_gemm_gated_grad", "fp4q_layer_norm",
            "fp4q_layer_norm_grad_workspace_bytes", "fp4q_layer_norm_grad", "fp4q_adamw_step",
-           "fp4q_adamw_table", "fp4q_adamw_step_table",
+           "fp4q_adamw_table", "fp4q_adamw_step_table", "fp4q_residual_norm",
+           "fp4q_residual_norm_grad_workspace_bytes", "fp4q_residual_norm_grad",
+           "fp4q_grad_norm_workspace_bytes", "fp4q_grad_norm", "fp4q_grad_scale",
            "fp4q_set_next_launch", "fp4q_status_string",
            "fp4q_last_error", "fp4q_abi_version"]
 
@@ -49,6 +52,11 @@ class AdamwTensor(_ct.Structure):
                 ("exp_avg_sq", _ct.c_void_p), ("exp_avg_scales", _ct.c_void_p),
                 ("exp_avg_sq_scales", _ct.c_void_p), ("copy", _ct.c_void_p),
                 ("numel", _ct.c_int64), ("weight_decay", _ct.c_double)]
+
+
+class Tensor(_ct.Structure):
+    """One tensor of a gradient norm (fp4q_tensor_t)."""
+    _fields_ = [("data", _ct.c_void_p), ("numel", _ct.c_int64), ("dtype", _ct.c_int64)]
 
 
 _lib = None
@@ -107,6 +115,16 @@ def lib():
             "fp4q_adamw_step": (I32, [P, I32, I32, I32, D, D, D, D, I64, U64, P, P]),
             "fp4q_adamw_table": (I32, [P, I32, I32, P, P, P]),
             "fp4q_adamw_step_table": (I32, [P, I32, I64, I32, I32, D, D, D, D, I64, U64, P, P]),
+            "fp4q_residual_norm": (I32, [I64, I64, P, I32, I64, P, I32, I64, I32, P, P, P, I32, I64, I64,
+                                         D, D, I32, P, P, I32, D, P, I64, P, I32, I64, P, P, P, P, P,
+                                         P, P]),
+            "fp4q_residual_norm_grad_workspace_bytes": (SZ, [I64, I64, I64]),
+            "fp4q_residual_norm_grad": (I32, [I64, I64, P, I32, I64, P, I64, P, I32, I64, P, I32, I64, I32,
+                                              P, P, P, I32, I64, I64, D, D, I32, P, I32, P, P, P, P, P,
+                                              I64, P, I64, P, P, P, P, P, P, SZ, P]),
+            "fp4q_grad_norm_workspace_bytes": (SZ, [P, I32]),
+            "fp4q_grad_norm": (I32, [P, I32, I32, D, D, P, P, P, SZ, P]),
+            "fp4q_grad_scale": (I32, [P, I32, P, P]),
             "fp4q_set_next_launch": (I32, [P, P, _ct.c_uint32]),
             "fp4q_status_string": (_ct.c_char_p, [I32]),
             "fp4q_last_error": (_ct.c_char_p, []),
@@ -834,6 +852,305 @@ def layer_norm_grad(dy, x, weight, mean, rstd, kind=LAYER_NORM, dx=None, want_we
     return dx, dweight, dbias
 
 
+def _on_device(first, stream, *others):
+    """Raises unless the tensors lie on one device, the current one or the
+    stream's: a kernel on another device's stream would read them over there."""
+    d = first.get_device()
+    if d != ((_torch_module or _torch())._C._cuda_getDevice() if stream is None else stream.device_index):
+        raise ValueError("the tensors must lie on the current device (or the stream's)")
+    for t in others:
+        if t is not None and t.get_device() != d:
+            raise ValueError("the tensors must lie on one device")
+
+
+def _gate(gate, gate_rows, rows, cols):
+    """Dtype code, rows per row of the gate and row stride of a gate [cols] or
+    [groups, cols]."""
+    if gate is None:
+        return F32, rows, cols
+    size = gate.shape
+    if len(size) == 1:
+        _vec(gate, "gate", None, cols)
+        groups, ld = 1, cols
+    else:
+        ld = _rows(gate, "gate")
+        groups = size[0]
+        if size[1] != cols or groups == 0:
+            raise ValueError(f"gate must have {cols} columns and a row, got {tuple(size)}")
+    if gate_rows is None:
+        if groups == 1:
+            gate_rows = rows
+        elif rows % groups == 0:
+            gate_rows = rows // groups
+        else:
+            raise ValueError("gate_rows is needed where the gate's rows do not divide the rows")
+    if gate_rows < 1 or -(-rows // gate_rows) != groups:
+        raise ValueError(f"gate has {groups} rows for {rows} rows of which {gate_rows} share one")
+    return _dt(gate), gate_rows, ld
+
+
+def _norm_vectors(cols, **vectors):
+    """Dtype code of the vectors of both norms."""
+    dt = None
+    for name, t in vectors.items():
+        if t is None:
+            continue
+        _vec(t, name, None, cols)
+        if dt is None:
+            dt = t.dtype
+            code = _dt(t)
+        elif t.dtype is not dt:
+            raise TypeError("the norms' weights and biases must have the same dtype")
+    return F32 if dt is None else code
+
+
+def residual_norm(x, branch, weight=None, bias=None, eps=1e-5, kind=LAYER_NORM, post_kind=NO_NORM,
+                  post_weight=None, post_bias=None, gate=None, gate_rows=None, x_scale=1.0,
+                  branch_scale=1.0, x_out=None, y=None, out_dtype=None, quantize=False, stats=True,
+                  stream=None):
+    """The norm behind a block (post_kind), its gate, the residual sum and the
+    norm in front of the next block (fp4q_residual_norm):
+        x_out = x_scale x + branch_scale gate post(branch),  y = norm(x_out).
+    gate: [cols], or one row per gate_rows rows of x (by default rows / gate's
+    rows).  Returns (x_out, y, stats): x_out of x's dtype (x itself may be given
+    for it), y of out_dtype (x's by default), or with quantize=True the pair
+    (codes, scales) of quantize(y, 32); stats = (post_mean, post_rstd, mean,
+    rstd), fp32 per row, for residual_norm_grad (None where the norm has none,
+    or without stats)."""
+    torch = _torch()
+    f32 = torch.float32
+    ldx = _rows(x, "x")
+    R, C = x.shape
+    ldb = _rows(branch, "branch", shape=(R, C))
+    xdt = _dt(x)
+    wdt = _norm_vectors(C, weight=weight, bias=bias, post_weight=post_weight, post_bias=post_bias)
+    gdt, gate_rows, ldg = _gate(gate, gate_rows, R, C)
+    _on_device(x, stream, branch, weight, bias, post_weight, post_bias, gate, x_out, y)
+    empty = _allocator(x, stream)
+    if x_out is None:
+        x_out, ldxo = empty((R, C), (C, 1), x.dtype), C
+    else:
+        ldxo = _rows(x_out, "x_out", x.dtype, (R, C))
+    codes = scales = None
+    ydt, ldy = xdt, C
+    if quantize:
+        if y is not None or out_dtype is not None:
+            raise ValueError("y and out_dtype are for a result that is not quantized")
+        if C % 32:
+            raise ValueError(f"codes need a multiple of 32 columns, got {C}")
+        codes = empty((R, C // 2), (C // 2, 1), torch.uint8)
+        scales = empty((R, C // 32), (C // 32, 1), torch.uint8)
+    elif y is None:
+        y = empty((R, C), (C, 1), x.dtype if out_dtype is None else out_dtype)
+        if out_dtype is not None:
+            ydt = _dt(y)
+    else:
+        ldy, ydt = _rows(y, "y", shape=(R, C)), _dt(y)
+    pm = pr = m = r = None
+    if stats:
+        if post_kind == LAYER_NORM:
+            pm = empty((R,), (1,), f32)
+        if post_kind != NO_NORM:
+            pr = empty((R,), (1,), f32)
+        if kind == LAYER_NORM:
+            m = empty((R,), (1,), f32)
+        r = empty((R,), (1,), f32)
+    status = lib().fp4q_residual_norm(
+        R, C, x.data_ptr(), xdt, ldx, branch.data_ptr(), _dt(branch), ldb, post_kind, _ptr(post_weight),
+        _ptr(post_bias), _ptr(gate), gdt, gate_rows, ldg, x_scale, branch_scale, kind, _ptr(weight),
+        _ptr(bias), wdt, eps, x_out.data_ptr(), ldxo, _ptr(y), ydt, ldy, _ptr(codes), _ptr(scales),
+        _ptr(pm), _ptr(pr), _ptr(m), _ptr(r), _stream(stream))
+    if status:
+        _check(status)
+    return x_out, (codes, scales) if quantize else y, (pm, pr, m, r)
+
+
+def residual_norm_grad_workspace_bytes(rows, cols, gate_rows=0):
+    return int(lib().fp4q_residual_norm_grad_workspace_bytes(rows, cols, gate_rows))
+
+
+def residual_norm_grad(dy, dx_out, x_out, branch, stats, weight=None, kind=LAYER_NORM, post_kind=NO_NORM,
+                       post_weight=None, post_bias=None, gate=None, gate_rows=None, x_scale=1.0,
+                       branch_scale=1.0, dx=None, dbranch=None, want_weight=True, want_bias=True,
+                       want_post_weight=None, want_post_bias=None, want_gate=None, dweight=None,
+                       dbias=None, dpost_weight=None, dpost_bias=None, dgate=None, workspace=None,
+                       stream=None):
+    """Backward pass of residual_norm (fp4q_residual_norm_grad): dy is y's
+    gradient, dx_out the one that arrives at x_out along the residual stream (or
+    None), stats what residual_norm returned.  Returns (dx, dbranch, dweight,
+    dbias, dpost_weight, dpost_bias, dgate): dx of x_out's dtype, dbranch of
+    branch's, the others fp32 (dgate of the gate's shape), None where not wanted.
+    The gradients of post_weight, post_bias and gate are wanted where these are
+    given.  branch may be None without post_kind where the gate's gradient is not
+    wanted (dbranch then has x_out's dtype)."""
+    f32 = _torch().float32
+    ldxo = _rows(x_out, "x_out")
+    R, C = x_out.shape
+    xdt = _dt(x_out)
+    lddy = _rows(dy, "dy", shape=(R, C))
+    lddxo = C if dx_out is None else _rows(dx_out, "dx_out", x_out.dtype, (R, C))
+    ldb = C if branch is None else _rows(branch, "branch", shape=(R, C))
+    bdtype = branch.dtype if branch is not None else x_out.dtype if dbranch is None else dbranch.dtype
+    wdt = _norm_vectors(C, weight=weight, post_weight=post_weight, post_bias=post_bias)
+    gdt, rows_each, ldg = _gate(gate, gate_rows, R, C)
+    pm, pr, m, r = stats
+    for t, name in ((pm, "post_mean"), (pr, "post_rstd"), (m, "mean"), (r, "rstd")):
+        if t is not None:
+            _vec(t, name, f32, R)
+    _on_device(x_out, stream, dy, dx_out, branch, weight, post_weight, post_bias, gate, pm, pr, m, r, dx,
+               dbranch, dweight, dbias, dpost_weight, dpost_bias, dgate, workspace)
+    empty = _allocator(x_out, stream)
+    if dx is None:
+        dx, lddx = empty((R, C), (C, 1), x_out.dtype), C
+    else:
+        lddx = _rows(dx, "dx", x_out.dtype, (R, C))
+    if dbranch is None:
+        dbranch, lddb = empty((R, C), (C, 1), bdtype), C
+    else:
+        lddb = _rows(dbranch, "dbranch", bdtype, (R, C))
+    out = []
+    for t, name, want in ((dweight, "dweight", want_weight), (dbias, "dbias", want_bias),
+                          (dpost_weight, "dpost_weight",
+                           post_weight is not None if want_post_weight is None else want_post_weight),
+                          (dpost_bias, "dpost_bias",
+                           post_bias is not None if want_post_bias is None else want_post_bias)):
+        if t is not None:
+            _vec(t, name, f32, C)
+        elif want:
+            t = empty((C,), (1,), f32)
+        out.append(t)
+    if dgate is not None:
+        if gate is None:
+            raise ValueError("dgate without a gate")
+        _need_cuda(dgate)
+        _need(dgate, "dgate", f32, gate.shape)
+    elif gate is not None if want_gate is None else want_gate:
+        if gate is None:
+            raise ValueError("want_gate without a gate")
+        size = gate.shape
+        dgate = empty(tuple(size), (C, 1) if len(size) == 2 else (1,), f32)
+    if workspace is None:
+        nbytes = lib().fp4q_residual_norm_grad_workspace_bytes(R, C, rows_each)
+        workspace = empty((nbytes,), (1,), _torch().uint8)
+    else:
+        _need_cuda(workspace)
+        _need(workspace, "workspace", workspace.dtype)
+        nbytes = workspace.numel() * workspace.element_size()
+    dw, dc, dpw, dpc = out
+    status = lib().fp4q_residual_norm_grad(
+        R, C, dy.data_ptr(), _dt(dy), lddy, _ptr(dx_out), lddxo, x_out.data_ptr(), xdt, ldxo, _ptr(branch),
+        _dt(dbranch), ldb, post_kind, _ptr(post_weight), _ptr(post_bias), _ptr(gate), gdt, rows_each, ldg,
+        x_scale, branch_scale, kind, _ptr(weight), wdt, _ptr(pm), _ptr(pr), _ptr(m), _ptr(r), dx.data_ptr(),
+        lddx, dbranch.data_ptr(), lddb, _ptr(dpw), _ptr(dpc), _ptr(dgate), _ptr(dw), _ptr(dc),
+        workspace.data_ptr(), nbytes, _stream(stream))
+    if status:
+        _check(status)
+    return dx, dbranch, dw, dc, dpw, dpc, dgate
+
+
+class GradPlan:
+    """The tensors of a gradient norm, checked once (see grad_plan).  Holds their
+    memory, through tensors of its own."""
+
+    def __init__(self, grads):
+        torch = _torch()
+        self.n = len(grads)
+        self.array = (Tensor * max(self.n, 1))()
+        self.tensors = [t.detach() for t in grads]
+        self.like = self.tensors[0]
+        for i, t in enumerate(grads):
+            _need_cuda(t)
+            if t.dtype not in (torch.float32, torch.bfloat16):
+                raise TypeError(f"gradient {i} must be bf16 or fp32, got {t.dtype}")
+            if not t.is_contiguous():
+                raise ValueError(f"gradient {i} must be contiguous")
+            if t.get_device() != grads[0].get_device():
+                raise ValueError("the gradients must lie on one device")
+            self.array[i] = Tensor(t.data_ptr(), t.numel(), _dt(t))
+        self.nbytes = lib().fp4q_grad_norm_workspace_bytes(self.array, self.n)
+
+
+def grad_plan(grads):
+    """Checks the gradients of a norm (contiguous, fp32 and bf16 mixed) and keeps
+    their addresses for grad_norm and clip_grads.  Like an AdamwPlan it is of
+    addresses, holds the memory behind them and is made anew when a gradient gets
+    other memory."""
+    grads = list(grads)
+    if not grads:
+        raise ValueError("a plan needs a gradient")
+    return GradPlan(grads)
+
+
+def _grads_of(plan):
+    if isinstance(plan, AdamwPlan):
+        if plan.grads is None:
+            plan.grads = grad_plan([row[1] for row in plan.tensors])
+        return plan.grads
+    return plan
+
+
+def grad_norm(plan, max_norm=None, eps=1e-6, order=NORM_L2, norm=None, scale=None, workspace=None,
+              stream=None):
+    """The norm of a plan's gradients taken as one vector (fp4q_grad_norm), and
+    with max_norm the factor min(1, max_norm / (norm + eps)) that clips it.  plan:
+    a grad_plan, or an adamw_plan for its gradients.  Returns (norm, scale),
+    device fp32 scalars (scale None without max_norm); scale is adamw_step's
+    grad_scale.  A graph that captured the call reads the plan's memory at every
+    replay: the plan is kept as long as the graph."""
+    f32 = _torch().float32
+    plan = _grads_of(plan)
+    _on_device(plan.like, stream, norm, scale, workspace)
+    empty = _allocator(plan.like, stream)
+    for t, name in ((norm, "norm"), (scale, "scale")):
+        if t is not None:
+            _need_cuda(t)
+            _need(t, name, f32)
+            if t.numel() != 1:
+                raise ValueError(f"{name} must have one element, got {t.numel()}")
+    if norm is None:
+        norm = empty((), (), f32)
+    if max_norm is None:
+        if scale is not None:
+            raise ValueError("scale needs max_norm")
+    elif scale is None:
+        scale = empty((), (), f32)
+    if workspace is None:
+        nbytes = plan.nbytes
+        workspace = empty((nbytes,), (1,), _torch().uint8)
+    else:
+        _need_cuda(workspace)
+        _need(workspace, "workspace", workspace.dtype)
+        nbytes = workspace.numel() * workspace.element_size()
+    status = lib().fp4q_grad_norm(plan.array, plan.n, order, 0.0 if max_norm is None else max_norm, eps,
+                                  norm.data_ptr(), _ptr(scale), workspace.data_ptr(), nbytes,
+                                  _stream(stream))
+    if status:
+        _check(status)
+    return norm, scale
+
+
+def scale_grads(plan, scale, stream=None):
+    """Multiplies a plan's gradients by a device fp32 scalar in place
+    (fp4q_grad_scale)."""
+    plan = _grads_of(plan)
+    _need_cuda(scale)
+    _need(scale, "scale", _torch().float32)
+    if scale.numel() != 1:
+        raise ValueError(f"scale must have one element, got {scale.numel()}")
+    _on_device(plan.like, stream, scale)
+    status = lib().fp4q_grad_scale(plan.array, plan.n, scale.data_ptr(), _stream(stream))
+    if status:
+        _check(status)
+
+
+def clip_grads(plan, max_norm, eps=1e-6, order=NORM_L2, stream=None):
+    """Clips a plan's gradients in place to the norm max_norm (grad_norm, then
+    scale_grads).  Returns the norm they had, a device fp32 scalar."""
+    norm, scale = grad_norm(plan, max_norm, eps, order, stream=stream)
+    scale_grads(plan, scale, stream)
+    return norm
+
+
 class AdamwPlan:
     """The tensors of an AdamW step, checked once (see adamw_plan).  Holds
     their memory (through tensors of its own, which a later `param.data = ...`
@@ -845,6 +1162,7 @@ class AdamwPlan:
         self.array, self.n, self.bits, self.grad_dtype = array, n, bits, grad_dtype
         self.tensors = tensors
         self.table, self.chunks, self.streams = None, 0, set()
+        self.grads = None  # the plan of the gradients' norm, made when it is asked for
         if n > self.ARGUMENTS:
             torch = _torch()
             size, chunks = _ct.c_size_t(0), _ct.c_int64(0)

@@ -8,6 +8,7 @@
 
 #include "../../include/libfp4q.h"
 #include "fp4q_internal.h"
+#include "residual_norm.h"
 
 namespace fp4q {
 thread_local NextLaunch g_next_launch = {nullptr, nullptr, 0u, false};
@@ -101,6 +102,48 @@ fp4q_status_t adamw_tensors(const char* who, const fp4q_adamw_tensor_t* tensors,
         if (!aligned16(t.param) || !aligned16(t.grad) || !aligned16(t.exp_avg) ||
             !aligned16(t.exp_avg_sq) || !aligned16(t.copy))
             return fail(FP4Q_ERR_ALIGNMENT, "%s: tensor %d: pointers must be 16-byte aligned", who, i);
+    }
+    return FP4Q_OK;
+}
+
+// Arguments that the residual norms share.
+fp4q_status_t residual_args(const char* who, fp4q_norm_t post_kind, const void* post_weight,
+                            const void* post_bias, const void* gate, fp4q_dtype_t gate_dtype,
+                            int64_t gate_rows, int64_t ld_gate, double x_scale, double branch_scale,
+                            fp4q_norm_t kind, int64_t rows, int64_t cols) {
+    if (kind != FP4Q_LAYER_NORM && kind != FP4Q_RMS_NORM)
+        return fail(FP4Q_ERR_INVALID, "%s: bad kind %d", who, (int)kind);
+    if (post_kind != FP4Q_LAYER_NORM && post_kind != FP4Q_RMS_NORM && post_kind != FP4Q_NO_NORM)
+        return fail(FP4Q_ERR_INVALID, "%s: bad post_kind %d", who, (int)post_kind);
+    if (post_kind == FP4Q_NO_NORM && (post_weight || post_bias))
+        return fail(FP4Q_ERR_INVALID, "%s: post_weight and post_bias need a post_kind", who);
+    if (!(x_scale > -1e30) || !(x_scale < 1e30) || !(branch_scale > -1e30) || !(branch_scale < 1e30))
+        return fail(FP4Q_ERR_INVALID, "%s: bad x_scale or branch_scale", who);
+    if (!gate) return FP4Q_OK;
+    if (!valid_dtype(gate_dtype)) return fail(FP4Q_ERR_INVALID, "%s: bad dtype", who);
+    if (gate_rows < 1) return fail(FP4Q_ERR_INVALID, "%s: gate_rows below 1", who);
+    if (gate_rows < rows && ld_gate < cols)
+        return fail(FP4Q_ERR_INVALID, "%s: row stride below cols", who);
+    if ((uintptr_t)gate % esize(gate_dtype))
+        return fail(FP4Q_ERR_ALIGNMENT, "%s: pointers must be element-aligned", who);
+    return FP4Q_OK;
+}
+
+fp4q_status_t grad_tensors(const char* who, const fp4q_tensor_t* tensors, int32_t n) {
+    if (n < 0 || (n > 0 && !tensors)) return fail(FP4Q_ERR_INVALID, "%s: no tensors", who);
+    int64_t sum = 0;
+    for (int32_t i = 0; i < n; ++i) {
+        const fp4q_tensor_t& t = tensors[i];
+        if (t.numel < 0 || t.numel >= ((int64_t)1 << 40))
+            return fail(FP4Q_ERR_INVALID, "%s: tensor %d: numel", who, i);
+        if (t.dtype != FP4Q_F32 && t.dtype != FP4Q_BF16)
+            return fail(FP4Q_ERR_INVALID, "%s: tensor %d: bad dtype", who, i);
+        if (t.numel == 0) continue;
+        if (!t.data) return fail(FP4Q_ERR_INVALID, "%s: tensor %d: null pointer", who, i);
+        if ((uintptr_t)t.data % esize((int)t.dtype))
+            return fail(FP4Q_ERR_ALIGNMENT, "%s: tensor %d: pointers must be element-aligned", who, i);
+        if ((sum += t.numel) >= ((int64_t)1 << 44))
+            return fail(FP4Q_ERR_UNSUPPORTED, "%s: too many elements", who);
     }
     return FP4Q_OK;
 }
@@ -824,6 +867,165 @@ fp4q_status_t fp4q_layer_norm_grad(fp4q_norm_t kind, const void* dy, fp4q_dtype_
                                              ld_dx, dweight, dbias, workspace,
                                              (hipStream_t)stream),
                       "layer_norm_grad launch");
+}
+
+fp4q_status_t fp4q_residual_norm(int64_t rows, int64_t cols, const void* x, fp4q_dtype_t x_dtype,
+                                 int64_t ld_x, const void* branch, fp4q_dtype_t b_dtype,
+                                 int64_t ld_b, fp4q_norm_t post_kind, const void* post_weight,
+                                 const void* post_bias, const void* gate, fp4q_dtype_t gate_dtype,
+                                 int64_t gate_rows, int64_t ld_gate, double x_scale,
+                                 double branch_scale, fp4q_norm_t kind, const void* weight,
+                                 const void* bias, fp4q_dtype_t w_dtype, double eps, void* x_out,
+                                 int64_t ld_xo, void* y, fp4q_dtype_t y_dtype, int64_t ld_y,
+                                 uint8_t* codes, uint8_t* scales, float* post_mean,
+                                 float* post_rstd, float* mean, float* rstd, void* stream) {
+    if (!x || !branch || !x_out) return fail(FP4Q_ERR_INVALID, "residual_norm: null pointer");
+    if (y ? codes || scales : !codes || !scales)
+        return fail(FP4Q_ERR_INVALID, "residual_norm: either y or codes and scales");
+    if (!valid_dtype(x_dtype) || !valid_dtype(b_dtype) || !valid_dtype(w_dtype) ||
+        (y && !valid_dtype(y_dtype)))
+        return fail(FP4Q_ERR_INVALID, "residual_norm: bad dtype");
+    int64_t ld = ld_x < ld_b ? ld_x : ld_b;
+    ld = ld < ld_xo ? ld : ld_xo;
+    fp4q_status_t e = norm_sizes("residual_norm", rows, cols, y && ld_y < ld ? ld_y : ld);
+    if (e == FP4Q_OK)
+        e = residual_args("residual_norm", post_kind, post_weight, post_bias, gate, gate_dtype,
+                          gate_rows, ld_gate, x_scale, branch_scale, kind, rows, cols);
+    if (e != FP4Q_OK) return e;
+    if (!(eps >= 0.0) || !(eps < 1e30)) return fail(FP4Q_ERR_INVALID, "residual_norm: bad eps");
+    if (codes && cols % 32) return fail(FP4Q_ERR_INVALID, "residual_norm: codes need cols %% 32 == 0");
+    if (((uintptr_t)x % esize(x_dtype)) || ((uintptr_t)x_out % esize(x_dtype)) ||
+        ((uintptr_t)branch % esize(b_dtype)) || (y && ((uintptr_t)y % esize(y_dtype))) ||
+        ((uintptr_t)post_weight % esize(w_dtype)) || ((uintptr_t)post_bias % esize(w_dtype)) ||
+        ((uintptr_t)weight % esize(w_dtype)) || ((uintptr_t)bias % esize(w_dtype)) ||
+        ((uintptr_t)post_mean % 4) || ((uintptr_t)post_rstd % 4) || ((uintptr_t)mean % 4) ||
+        ((uintptr_t)rstd % 4) || !aligned16(codes))
+        return fail(FP4Q_ERR_ALIGNMENT,
+                    "residual_norm: pointers must be element-aligned, codes 16-byte aligned");
+    fp4q::ResidualNorm a = {};
+    a.rows = rows, a.cols = cols, a.gate_rows = gate && gate_rows < rows ? gate_rows : rows;
+    a.x = x, a.b = branch, a.gate = gate;
+    a.post_weight = post_weight, a.post_bias = post_bias, a.weight = weight, a.bias = bias;
+    a.ldx = ld_x, a.ldb = ld_b, a.ldg = ld_gate;
+    a.x_bf16 = x_dtype, a.b_bf16 = b_dtype, a.gate_bf16 = gate_dtype, a.w_bf16 = w_dtype;
+    a.y_bf16 = y_dtype;
+    a.post = post_kind, a.rms = kind == FP4Q_RMS_NORM;
+    a.x_scale = (float)x_scale, a.branch_scale = (float)branch_scale, a.eps = (float)eps;
+    a.xo = x_out, a.y = y, a.ldxo = ld_xo, a.ldy = ld_y;
+    a.codes = codes, a.scales = scales;
+    a.post_mean = post_mean, a.post_rstd = post_rstd, a.mean = mean, a.rstd = rstd;
+    return hip_status(fp4q::launch_residual_norm(a, (hipStream_t)stream), "residual_norm launch");
+}
+
+size_t fp4q_residual_norm_grad_workspace_bytes(int64_t rows, int64_t cols, int64_t gate_rows) {
+    if (rows <= 0 || cols <= 0 || gate_rows < 0) return 0;
+    return fp4q::residual_norm_grad_workspace_bytes(
+        rows, cols, gate_rows && gate_rows < rows ? gate_rows : rows);
+}
+
+fp4q_status_t fp4q_residual_norm_grad(
+    int64_t rows, int64_t cols, const void* dy, fp4q_dtype_t dy_dtype, int64_t ld_dy,
+    const void* dx_out, int64_t ld_dxo, const void* x_out, fp4q_dtype_t x_dtype, int64_t ld_xo,
+    const void* branch, fp4q_dtype_t b_dtype, int64_t ld_b, fp4q_norm_t post_kind,
+    const void* post_weight, const void* post_bias, const void* gate, fp4q_dtype_t gate_dtype,
+    int64_t gate_rows, int64_t ld_gate, double x_scale, double branch_scale, fp4q_norm_t kind,
+    const void* weight, fp4q_dtype_t w_dtype, const float* post_mean, const float* post_rstd,
+    const float* mean, const float* rstd, void* dx, int64_t ld_dx, void* dbranch, int64_t ld_db,
+    float* dpost_weight, float* dpost_bias, float* dgate, float* dweight, float* dbias,
+    void* workspace, size_t workspace_bytes, void* stream) {
+    if (!dy || !x_out || !dx || !dbranch || !rstd)
+        return fail(FP4Q_ERR_INVALID, "residual_norm_grad: null pointer");
+    if (!valid_dtype(x_dtype) || !valid_dtype(b_dtype) || !valid_dtype(w_dtype) ||
+        !valid_dtype(dy_dtype))
+        return fail(FP4Q_ERR_INVALID, "residual_norm_grad: bad dtype");
+    int64_t ld = ld_dy < ld_xo ? ld_dy : ld_xo;
+    ld = ld < ld_dx ? ld : ld_dx;
+    ld = ld < ld_db ? ld : ld_db;
+    if (dx_out && ld_dxo < ld) ld = ld_dxo;
+    if (branch && ld_b < ld) ld = ld_b;
+    fp4q_status_t e = norm_sizes("residual_norm_grad", rows, cols, ld);
+    if (e == FP4Q_OK)
+        e = residual_args("residual_norm_grad", post_kind, post_weight, post_bias, gate, gate_dtype,
+                          gate_rows, ld_gate, x_scale, branch_scale, kind, rows, cols);
+    if (e != FP4Q_OK) return e;
+    const bool post = post_kind != FP4Q_NO_NORM;
+    if ((kind == FP4Q_LAYER_NORM && !mean) || (post && !post_rstd) ||
+        (post_kind == FP4Q_LAYER_NORM && !post_mean))
+        return fail(FP4Q_ERR_INVALID, "residual_norm_grad: the norms' statistics are missing");
+    if (!branch && (post || dgate))
+        return fail(FP4Q_ERR_INVALID, "residual_norm_grad: null branch");
+    if ((!post && (dpost_weight || dpost_bias)) || (!gate && dgate))
+        return fail(FP4Q_ERR_INVALID, "residual_norm_grad: a gradient of what is not there");
+    if (((uintptr_t)dy % esize(dy_dtype)) || ((uintptr_t)dx_out % esize(x_dtype)) ||
+        ((uintptr_t)x_out % esize(x_dtype)) || ((uintptr_t)dx % esize(x_dtype)) ||
+        ((uintptr_t)branch % esize(b_dtype)) || ((uintptr_t)dbranch % esize(b_dtype)) ||
+        ((uintptr_t)post_weight % esize(w_dtype)) || ((uintptr_t)post_bias % esize(w_dtype)) ||
+        ((uintptr_t)weight % esize(w_dtype)) || ((uintptr_t)post_mean % 4) ||
+        ((uintptr_t)post_rstd % 4) || ((uintptr_t)mean % 4) || ((uintptr_t)rstd % 4) ||
+        ((uintptr_t)dpost_weight % 4) || ((uintptr_t)dpost_bias % 4) || ((uintptr_t)dgate % 4) ||
+        ((uintptr_t)dweight % 4) || ((uintptr_t)dbias % 4))
+        return fail(FP4Q_ERR_ALIGNMENT, "residual_norm_grad: pointers must be element-aligned");
+    fp4q::ResidualNormGrad a = {};
+    a.rows = rows, a.cols = cols, a.gate_rows = gate && gate_rows < rows ? gate_rows : rows;
+    const size_t need = fp4q::residual_norm_grad_workspace_bytes(rows, cols, a.gate_rows);
+    if (!workspace) return fail(FP4Q_ERR_INVALID, "residual_norm_grad: null workspace");
+    if (!aligned16(workspace))
+        return fail(FP4Q_ERR_ALIGNMENT, "residual_norm_grad: workspace must be 16-byte aligned");
+    if (workspace_bytes < need)
+        return fail(FP4Q_ERR_WORKSPACE, "residual_norm_grad: workspace %zu < %zu bytes",
+                    workspace_bytes, need);
+    a.dy = dy, a.dxo = dx_out, a.xo = x_out, a.b = branch, a.gate = gate;
+    a.post_weight = post_weight, a.post_bias = post_bias, a.weight = weight;
+    a.lddy = ld_dy, a.lddxo = ld_dxo, a.ldxo = ld_xo, a.ldb = ld_b, a.ldg = ld_gate;
+    a.dy_bf16 = dy_dtype, a.x_bf16 = x_dtype, a.b_bf16 = b_dtype, a.gate_bf16 = gate_dtype;
+    a.w_bf16 = w_dtype;
+    a.post = post_kind, a.rms = kind == FP4Q_RMS_NORM;
+    a.x_scale = (float)x_scale, a.branch_scale = (float)branch_scale;
+    a.post_mean = post_mean, a.post_rstd = post_rstd, a.mean = mean, a.rstd = rstd;
+    a.dx = dx, a.db = dbranch, a.lddx = ld_dx, a.lddb = ld_db;
+    a.dpost_weight = dpost_weight, a.dpost_bias = dpost_bias, a.dgate = dgate;
+    a.dweight = dweight, a.dbias = dbias;
+    return hip_status(fp4q::launch_residual_norm_grad(a, workspace, (hipStream_t)stream),
+                      "residual_norm_grad launch");
+}
+
+size_t fp4q_grad_norm_workspace_bytes(const fp4q_tensor_t* tensors, int32_t n) {
+    if (grad_tensors("grad_norm_workspace_bytes", tensors, n) != FP4Q_OK) return 0;
+    return fp4q::grad_norm_workspace_bytes(tensors, n);
+}
+
+fp4q_status_t fp4q_grad_norm(const fp4q_tensor_t* tensors, int32_t n, fp4q_norm_order_t order,
+                             double max_norm, double eps, float* norm, float* scale,
+                             void* workspace, size_t workspace_bytes, void* stream) {
+    if (order != FP4Q_NORM_L2 && order != FP4Q_NORM_MAX)
+        return fail(FP4Q_ERR_INVALID, "grad_norm: bad order %d", (int)order);
+    if (!(max_norm >= 0.0) || !(max_norm < 1e300) || !(eps >= 0.0) || !(eps < 1e300))
+        return fail(FP4Q_ERR_INVALID, "grad_norm: bad max_norm or eps");
+    const fp4q_status_t e = grad_tensors("grad_norm", tensors, n);
+    if (e != FP4Q_OK) return e;
+    if (!norm && !scale) return fail(FP4Q_ERR_INVALID, "grad_norm: null pointer");
+    if (((uintptr_t)norm % 4) || ((uintptr_t)scale % 4))
+        return fail(FP4Q_ERR_ALIGNMENT, "grad_norm: pointers must be element-aligned");
+    const size_t need = fp4q::grad_norm_workspace_bytes(tensors, n);
+    if (!workspace) return fail(FP4Q_ERR_INVALID, "grad_norm: null workspace");
+    if (!aligned16(workspace))
+        return fail(FP4Q_ERR_ALIGNMENT, "grad_norm: workspace must be 16-byte aligned");
+    if (workspace_bytes < need)
+        return fail(FP4Q_ERR_WORKSPACE, "grad_norm: workspace %zu < %zu bytes", workspace_bytes, need);
+    return hip_status(fp4q::launch_grad_norm(tensors, n, order == FP4Q_NORM_MAX, max_norm, eps, norm,
+                                             scale, workspace, (hipStream_t)stream),
+                      "grad_norm launch");
+}
+
+fp4q_status_t fp4q_grad_scale(const fp4q_tensor_t* tensors, int32_t n, const float* scale,
+                              void* stream) {
+    const fp4q_status_t e = grad_tensors("grad_scale", tensors, n);
+    if (e != FP4Q_OK) return e;
+    if (!scale) return fail(FP4Q_ERR_INVALID, "grad_scale: null pointer");
+    if ((uintptr_t)scale % 4)
+        return fail(FP4Q_ERR_ALIGNMENT, "grad_scale: pointers must be element-aligned");
+    return hip_status(fp4q::launch_grad_scale(tensors, n, scale, (hipStream_t)stream),
+                      "grad_scale launch");
 }
 
 fp4q_status_t fp4q_adamw_step(const fp4q_adamw_tensor_t* tensors, int32_t n, int32_t state_bits,

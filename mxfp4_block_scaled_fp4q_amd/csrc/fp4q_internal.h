@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 struct fp4q_adamw_tensor;  // include/libfp4q.h
+struct fp4q_tensor;
 
 namespace fp4q {
 
@@ -174,6 +175,12 @@ hipError_t launch_norm_grad(const void* dy, int dydtype, int64_t lddy, const voi
                             int64_t rows, int64_t cols, int64_t ldx, const void* w, int wdtype,
                             const float* mean, const float* rstd, bool rms, void* dx, int64_t lddx,
                             float* dw, float* db, void* ws, hipStream_t s);
+// Norm of many tensors taken as one vector, with the factor that clips it to
+// max_norm, and the product of the tensors with such a factor.
+size_t grad_norm_workspace_bytes(const fp4q_tensor* t, int n);
+hipError_t launch_grad_norm(const fp4q_tensor* t, int n, bool largest, double max_norm, double eps,
+                            float* norm, float* scale, void* ws, hipStream_t s);
+hipError_t launch_grad_scale(const fp4q_tensor* t, int n, const float* scale, hipStream_t s);
 hipError_t launch_adamw(const fp4q_adamw_tensor* t, int n, int bits, int gdtype, double lr,
                         double beta1, double beta2, double eps, int64_t step, uint64_t seed,
                         const float* grad_scale, hipStream_t s);

@@ -24,162 +24,9 @@
 
 #include "fp4q_device.h"
 #include "fp4q_internal.h"
+#include "row_norm.h"
 
 namespace fp4q {
-
-template <int BF16T>
-__device__ __forceinline__ float load1(const void* p, int64_t i) {
-    if (BF16T) return as_f32((uint32_t)((const uint16_t*)p)[i] << 16);
-    return ((const float*)p)[i];
-}
-template <int BF16T>
-__device__ __forceinline__ void store1(void* p, int64_t i, float v) {
-    if (BF16T)
-        ((uint16_t*)p)[i] = (uint16_t)f32_to_bf16_bits(v);
-    else
-        ((float*)p)[i] = v;
-}
-// A weight or bias element; `none` where the caller passed no vector.
-__device__ __forceinline__ float vec1(const void* p, int bf16, int64_t i, float none) {
-    if (!p) return none;
-    return bf16 ? load1<1>(p, i) : load1<0>(p, i);
-}
-
-// 8 consecutive elements as they lie in memory.
-template <int BF16T>
-struct Chunk {
-    u32x4 v[BF16T ? 1 : 2];
-    __device__ __forceinline__ void load(const void* p, int64_t i) {
-        if (BF16T) {
-            v[0] = *(const u32x4_a2*)((const uint16_t*)p + i);
-        } else {
-            v[0] = *(const u32x4_a4*)((const float*)p + i);
-            v[BF16T ? 0 : 1] = *(const u32x4_a4*)((const float*)p + i + 4);
-        }
-    }
-    __device__ __forceinline__ float at(int e) const {
-        if (BF16T) {
-            const uint32_t w = v[0][e >> 1];
-            return (e & 1) ? bf16_hi(w) : bf16_lo(w);
-        }
-        return as_f32(v[BF16T ? 0 : e >> 2][e & 3]);
-    }
-};
-template <int BF16T>
-__device__ __forceinline__ void store_chunk(void* p, int64_t i, const float (&f)[8]) {
-    if (BF16T) {
-        u32x4 v;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const bf16x2_t q = {(__bf16)f[2 * e], (__bf16)f[2 * e + 1]};  // v_cvt_pk_bf16_f32
-            v[e] = __builtin_bit_cast(uint32_t, q);
-        }
-        *(u32x4_a2*)((uint16_t*)p + i) = v;
-    } else {
-        float* q = (float*)p + i;
-        *(u32x4_a4*)q = (u32x4){as_u32(f[0]), as_u32(f[1]), as_u32(f[2]), as_u32(f[3])};
-        *(u32x4_a4*)(q + 4) = (u32x4){as_u32(f[4]), as_u32(f[5]), as_u32(f[6]), as_u32(f[7])};
-    }
-}
-// All of them, or elements skip .. 7.
-template <int BF16T>
-__device__ __forceinline__ void store_own(void* p, int64_t i, const float (&f)[8], int skip) {
-    if (skip == 0) {
-        store_chunk<BF16T>(p, i, f);
-    } else {
-#pragma unroll
-        for (int e = 1; e < 8; ++e)
-            if (e >= skip) store1<BF16T>(p, i + e, f[e]);
-    }
-}
-__device__ __forceinline__ void load_vec8(const void* p, int bf16, int64_t i, float none,
-                                          float (&f)[8]) {
-    if (!p) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = none;
-    } else if (bf16) {
-        Chunk<1> c;
-        c.load(p, i);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = c.at(e);
-    } else {
-        Chunk<0> c;
-        c.load(p, i);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = c.at(e);
-    }
-}
-
-// Sums over 16 lanes (DPP steps, as in group_max_u32) and over the wave (then
-// the four rows of 16 by gfx950's lane swaps), in every lane.
-template <int CTRL>
-__device__ __forceinline__ float dpp_add(float v) {
-    return v + as_f32((uint32_t)__builtin_amdgcn_update_dpp(0, (int)as_u32(v), CTRL, 0xF, 0xF, true));
-}
-__device__ __forceinline__ float sum16(float v) {
-    return dpp_add<0x140>(dpp_add<0x141>(dpp_add<0x4E>(dpp_add<0xB1>(v))));
-}
-__device__ __forceinline__ float rows_sum(float v) {  // over the four rows, lane by lane
-    const auto a = __builtin_amdgcn_permlane16_swap(as_u32(v), as_u32(v), false, false);
-    v = as_f32(a[0]) + as_f32(a[1]);
-    const auto b = __builtin_amdgcn_permlane32_swap(as_u32(v), as_u32(v), false, false);
-    return as_f32(b[0]) + as_f32(b[1]);
-}
-__device__ __forceinline__ float wave_sum(float v) { return rows_sum(sum16(v)); }
-
-// Sums of N values over the waves that share a row (W of them, at most 16), in
-// every lane.  `red` holds two sets of N * 16 floats that take turns, so one
-// barrier is enough: a set is written again only after the next sum's barrier.
-template <int MULTI, int N>
-__device__ __forceinline__ void row_sums(float (&v)[N], float* red, int W, int& turn) {
-#pragma unroll
-    for (int n = 0; n < N; ++n) v[n] = wave_sum(v[n]);
-    if (!MULTI) return;
-    float* r = red + turn * (N * 16);
-    turn ^= 1;
-    if ((threadIdx.x & 63) == 0) {
-#pragma unroll
-        for (int n = 0; n < N; ++n) r[n * 16 + (threadIdx.x >> 6)] = v[n];
-    }
-    __syncthreads();
-    const int l = threadIdx.x & 15;
-#pragma unroll
-    for (int n = 0; n < N; ++n) v[n] = sum16(l < W ? r[n * 16 + l] : 0.0f);
-}
-
-// A row is held by one wave (MULTI = 0; 256 threads work on four rows) or by
-// all W waves of its workgroup, NV chunks per lane.  The last chunk begins at
-// `tail` in this lane and its first `skip` elements are another lane's; a lane
-// past the row's end holds that row's last chunk again, with skip = 8.
-//
-// Every lane loads and stores all its chunks, and past the last row loads that
-// row again: a load or store under a condition would leave the compiler not
-// knowing how many are in flight, and it would wait for the rows ahead too.
-// Elements that two lanes hold are stored by both, with the same bits.
-template <int NV>
-struct Place {
-    int W, t, step, tail, skip;
-    template <int MULTI>
-    __device__ __forceinline__ static Place make(int cols) {
-        Place p;
-        p.W = MULTI ? (int)(blockDim.x >> 6) : 1;
-        p.t = (MULTI ? (int)threadIdx.x : (int)(threadIdx.x & 63)) * 8;
-        p.step = p.W * 512;
-        const int c0 = (NV - 1) * p.step + p.t;
-        p.tail = min(c0, cols - 8);
-        p.skip = c0 < cols ? c0 - p.tail : 8;
-        return p;
-    }
-    __device__ __forceinline__ int start(int k) const { return k < NV - 1 ? k * step + t : tail; }
-    __device__ __forceinline__ bool owns(int k, int e) const { return k < NV - 1 || e >= skip; }
-};
-
-// First row of this wave's (or workgroup's) walk, a scalar.
-template <int MULTI>
-__device__ __forceinline__ int64_t first_row() {
-    if (MULTI) return blockIdx.x;
-    return (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-}
 
 template <int XB, int YB, int MULTI, int NV>
 __global__ __launch_bounds__(MULTI ? 1024 : 256) void norm_kernel(
@@ -447,14 +294,6 @@ __global__ __launch_bounds__(1024) void norm_grad_join_kernel(const float* __res
 
 // Rows below 8 columns, or too long for the registers: 256 threads walk over
 // the row once per sum, element by element.
-__device__ __forceinline__ float block_sum(float v, float* red) {
-    v = wave_sum(v);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-    __syncthreads();
-    return (red[0] + red[1]) + (red[2] + red[3]);
-}
-
 template <int XB, int YB>
 __global__ __launch_bounds__(256) void norm_any_kernel(
     const void* __restrict__ x, int64_t rows, int64_t cols, int64_t ldx, const void* __restrict__ w,
@@ -529,21 +368,6 @@ __global__ __launch_bounds__(256) void norm_grad_cols_kernel(
     part[((int64_t)blockIdx.y * 2 + 1) * cols + c] = sb;
 }
 
-// How rows of `cols` elements are held: by one wave or by all waves of their
-// workgroup, in nv chunks per lane (nv = 0: not in registers).  One wave needs
-// no barrier, but has only enough loads in flight where there are rows for all
-// of them.
-struct NormShape {
-    bool multi;
-    int nv, threads;
-};
-static NormShape norm_shape(int64_t rows, int64_t cols) {
-    if (cols < 8 || cols > 16384) return {false, 0, 256};
-    if (cols <= 512) return {false, 1, 256};
-    if (cols <= 1024 && rows > 1024) return {false, 2, 256};
-    const int nv = cols <= 8192 ? 1 : 2;
-    return {true, nv, 64 * (int)((cols + nv * 512 - 1) / (nv * 512))};
-}
 constexpr int64_t kAnyGrid = 1 << 16;
 
 // Workgroups of a walk over the rows: what 256 compute units hold of them at

@@ -131,3 +131,55 @@ def adamw(p, g, m, v, lr, beta1, beta2, eps, step, wd, grad_scale=1.0):
     den = np.sqrt(v / (1 - beta2 ** step)) + eps
     up = lr * (m / (1 - beta1 ** step)) / den
     return p * (1 - lr * wd) - up, m, v, parts, den
+
+
+# ---- residual norms: kind 0 layer, 1 rms, 2 none ----
+
+def group_rows(t, rows, gate_rows):
+    """Rows of a gate [groups, C], one for each of `rows` rows; ones for None."""
+    return 1.0 if t is None else t[np.arange(rows) // gate_rows]
+
+
+def residual_norm(x, b, post, pw, pc, gate, gate_rows, xs, bs, rms, w, c, eps):
+    """(x_out, y, (post_mean, post_rstd, mean, rstd)) with x_out unrounded."""
+    if post == 2:
+        n, pm, pr = b, None, None
+    else:
+        n, pm, pr = norm(b, pw, pc, eps, post == 1)
+    xo = xs * x + bs * group_rows(gate, len(x), gate_rows) * n
+    y, m, r = norm(xo, w, c, eps, rms)
+    return xo, y, (pm, pr, m, r)
+
+
+def residual_norm_grad(dy, dxo, xo, b, stats, post, pw, pc, gate, gate_rows, xs, bs, rms, w):
+    """dict of the gradients, for given statistics (pm, pr, m, r)."""
+    pm, pr, m, r = stats
+    R = len(xo)
+    d, dw, dc = norm_grad(dy, xo, w, m, r, rms)
+    D = d if dxo is None else dxo + d
+    g = group_rows(gate, R, gate_rows)
+    e = bs * g * D
+    out = dict(dx=xs * D, dweight=dw, dbias=dc)
+    n = b
+    if post == 2:
+        out["dbranch"] = e
+    else:
+        out["dbranch"], out["dpost_weight"], out["dpost_bias"] = norm_grad(e, b, pw, pm, pr, post == 1)
+        n = (b - (0.0 if post == 1 else pm[:, None])) * pr[:, None]
+        n = n * (1.0 if pw is None else pw) + (0.0 if pc is None else pc)
+    if gate is not None:
+        out["dgate"] = np.stack([(bs * D * n)[i:i + gate_rows].sum(0) for i in range(0, R, gate_rows)])
+    return out
+
+
+# ---- the norm of many gradients ----
+
+def grad_norm(grads, largest):
+    """Norm of the tensors taken as one vector."""
+    flat = np.concatenate([np.asarray(g, np.float64).ravel() for g in grads] + [np.zeros(1)])
+    return np.abs(flat).max() if largest else np.sqrt((flat * flat).sum())
+
+
+def clip_scale(norm, max_norm, eps):
+    with np.errstate(invalid="ignore", divide="ignore"):
+        return np.where(norm + eps == 0, 1.0, np.minimum(1.0, np.float64(max_norm) / (norm + eps)))
