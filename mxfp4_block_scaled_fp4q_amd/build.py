@@ -16,7 +16,7 @@ SOURCES = ["fp4q_api.hip", "quantize.hip", "dequantize.hip", "grad.hip", "gemm_f
            "hcp.hip", "hotsel.hip",
            "quant2d.hip", "rht.hip",
            "occ.hip", "gated.hip", "gated_small.hip", "norm.hip", "adamw.hip",
-           "residual_norm.hip", "grad_norm.hip"]
+           "residual_norm.hip", "residual_norm_grad.hip", "grad_norm.hip"]
 ARCH = "gfx950"
 FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-Wall",
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]

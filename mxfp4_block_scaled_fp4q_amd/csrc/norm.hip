@@ -386,10 +386,6 @@ constexpr int64_t kAnyGrid = 1 << 16;
 // 8192, so the rule asks for the rows alone (its step past 1024 rows, 256 to 129
 // workgroups at 5120 columns, costs nothing).
 constexpr int kNormWaves = 24, kGradWaves = 16;
-static int norm_groups(const NormShape& sh, int64_t rows, int waves, int min_rows) {
-    const int64_t per = (int64_t)min_rows * (sh.multi ? 1 : 4);
-    return (int)std::min<int64_t>(256 * (waves * 64 / sh.threads), (rows + per - 1) / per);
-}
 static int norm_slabs(int64_t rows, int64_t cols) {
     const NormShape sh = norm_shape(rows, cols);
     if (sh.nv == 0) return (int)std::min<int64_t>(128, (rows + 63) / 64);

@@ -25,6 +25,17 @@ __device__ __forceinline__ float vec1(const void* p, int bf16, int64_t i, float 
     return bf16 ? load1<1>(p, i) : load1<0>(p, i);
 }
 
+// The same where the type is known at run time only.
+__device__ __forceinline__ float load_as(const void* p, int bf16, int64_t i) {
+    return bf16 ? load1<1>(p, i) : load1<0>(p, i);
+}
+__device__ __forceinline__ void store_as(void* p, int bf16, int64_t i, float v) {
+    if (bf16)
+        store1<1>(p, i, v);
+    else
+        store1<0>(p, i, v);
+}
+
 // 8 consecutive elements as they lie in memory.
 template <int BF16T>
 struct Chunk {
@@ -185,4 +196,12 @@ inline NormShape norm_shape(int64_t rows, int64_t cols) {
     const int nv = cols <= 8192 ? 1 : 2;
     return {true, nv, 64 * (int)((cols + nv * 512 - 1) / (nv * 512))};
 }
+// Workgroups of a walk over the rows: what 256 compute units hold of them at
+// `waves` waves each, and at least `min_rows` rows to a workgroup (or to each
+// of its four waves).
+inline int norm_groups(const NormShape& sh, int64_t rows, int waves, int min_rows) {
+    const int64_t per = (int64_t)min_rows * (sh.multi ? 1 : 4);
+    return (int)std::min<int64_t>(256 * (waves * 64 / sh.threads), (rows + per - 1) / per);
+}
+
 }  // namespace fp4q
