@@ -11,7 +11,7 @@ namespace fp4q {
 
 // Slabs of rows that each leave one row of partial column sums.  A slab holds
 // whole groups of rows that share a gate, or, where a group is longer than a
-// slab, one of the k even parts of one group.
+// slab or the only one, one of the k even parts of one group.
 struct Slabs {
     int64_t count, rows, group;  // group: rows of a group
     int64_t k;                   // slabs of a group, 0 with whole groups
@@ -35,7 +35,7 @@ static Slabs make_slabs(int64_t rows, int64_t gate_rows, int64_t want) {
     s.group = std::min(gate_rows, rows);
     const int64_t all = (rows + s.group - 1) / s.group;
     const int64_t each = (rows + want - 1) / want;
-    if (s.group > each) {
+    if (s.group > each || all == 1) {
         s.k = (s.group + each - 1) / each;
         s.groups = 0;
         s.count = all * s.k;
@@ -53,12 +53,14 @@ struct RowMeans {
 };
 struct RowStats {
     float m, r, pm, pr;
+    // Every row reads four numbers, those that are not there from rstd: a load
+    // under a condition would have the compiler wait for more than it needs.
     __device__ __forceinline__ static RowStats of(const ResidualNormGrad& a, int64_t r) {
-        RowStats s = {0.0f, a.rstd[r], 0.0f, 1.0f};
-        if (!a.rms) s.m = a.mean[r];
-        if (a.post != kPostNone) s.pr = a.post_rstd[r];
-        if (a.post == 0) s.pm = a.post_mean[r];
-        return s;
+        const float* m = a.rms ? a.rstd : a.mean;
+        const float* pm = a.post == 0 ? a.post_mean : a.rstd;
+        const float* pr = a.post != kPostNone ? a.post_rstd : a.rstd;
+        const RowStats s = {m[r], a.rstd[r], pm[r], pr[r]};
+        return {a.rms ? 0.0f : s.m, s.r, a.post == 0 ? s.pm : 0.0f, a.post != kPostNone ? s.pr : 1.0f};
     }
 };
 struct RowPoint {
@@ -116,55 +118,120 @@ __global__ __launch_bounds__(256) void residual_grad_rows_kernel(const ResidualN
     }
 }
 
-// Column sums of a slab, four rows of `cols` floats of the partial sums: dw,
-// dc, and S1, S2 of the slab's group, or with whole groups dwp, dbp (the
-// groups' dg is then written at once).
-__global__ __launch_bounds__(256) void residual_grad_cols_kernel(const ResidualNormGrad a,
-                                                                 const RowMeans* __restrict__ means,
-                                                                 const Slabs sl,
-                                                                 float* __restrict__ part) {
-    const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (c >= a.cols) return;
-    const float wp = vec1(a.post_weight, a.w_bf16, c, 1.0f), bp = vec1(a.post_bias, a.w_bf16, c, 0.0f);
-    for (int64_t i = blockIdx.y; i < sl.count; i += gridDim.y) {
-        int64_t r0, r1;
-        sl.bounds(i, r0, r1);
-        float dw = 0.0f, dc = 0.0f, s1 = 0.0f, s2 = 0.0f, dwp = 0.0f, dbp = 0.0f;
-        for (int64_t r = r0; r < r1; ++r) {
-            const RowPoint p(a, r);
-            const float dy = p.dy(c), d = p.D(c, means[r]);
-            dw += dy * p.xh(c);
-            dc += dy;
-            s1 += d * p.nh(c);
-            s2 += d;
-            if (!sl.k && ((r + 1) % sl.group == 0 || r + 1 == r1)) {
-                const int64_t g = r / sl.group;
-                const float f = a.branch_scale * (a.gate ? load_as(a.gate, a.gate_bf16, g * a.ldg + c) : 1.0f);
-                if (a.dgate) a.dgate[g * a.cols + c] = a.branch_scale * (wp * s1 + bp * s2);
-                dwp += f * s1;
-                dbp += f * s2;
-                s1 = s2 = 0.0f;
-            }
-        }
-        float* o = part + i * 4 * a.cols + c;
-        o[0] = dw;
-        o[a.cols] = dc;
-        o[2 * a.cols] = sl.k ? s1 : dwp;
-        o[3 * a.cols] = sl.k ? s2 : dbp;
+// Outputs and column sums where the rows' means are known: 8 columns to a lane,
+// 2048 to a workgroup, over the rows of a slab.  The sums are four rows of
+// `cols` floats: dw, dc, and S1, S2 of the slab's group, or with whole groups
+// dwp, dbp (the groups' dg is then written at once).  Each element is read and
+// written by one lane, so that dx and db may lie on dxo and b.
+template <class F>
+__device__ __forceinline__ void each8(int left, F f) {
+    if (left >= 8) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f(e);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (e < left) f(e);
+    }
+}
+template <int B16>
+__device__ __forceinline__ void load8(const void* p, int64_t i, int left, float (&f)[8]) {
+    if (left >= 8) {
+        Chunk<B16> c;
+        c.load(p, i);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = c.at(e);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = e < left ? load1<B16>(p, i + e) : 0.0f;
+    }
+}
+template <int B16>
+__device__ __forceinline__ void store8(void* p, int64_t i, int left, const float (&f)[8]) {
+    if (left >= 8)
+        store_chunk<B16>(p, i, f);
+    else
+        each8(left, [&](int e) { store1<B16>(p, i + e, f[e]); });
+}
+__device__ __forceinline__ void load8_as(const void* p, int bf16, int64_t i, int left, float none,
+                                         float (&f)[8]) {
+    if (!p) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = none;
+    } else if (bf16) {
+        load8<1>(p, i, left, f);
+    } else {
+        load8<0>(p, i, left, f);
     }
 }
 
-__global__ __launch_bounds__(256) void residual_grad_any_kernel(const ResidualNormGrad a,
-                                                                const RowMeans* __restrict__ means) {
-    for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
-        const RowPoint p(a, r);
-        const RowMeans k = means[r];
-        for (int64_t c = threadIdx.x; c < a.cols; c += 256) {
-            const float d = p.D(c, k), u = p.u(c, d);
-            const float v = a.post == kPostNone ? u : p.s.pr * (u - k.u - p.nh(c) * k.unh);
-            store_as(a.dx, a.x_bf16, r * a.lddx + c, a.x_scale * d);
-            store_as(a.db, a.b_bf16, r * a.lddb + c, v);
+template <int XB, int BB, int DB>
+__global__ __launch_bounds__(256) void residual_grad_tile_kernel(const ResidualNormGrad a,
+                                                                 const RowMeans* __restrict__ means,
+                                                                 const Slabs sl, float* part) {
+    const int64_t c = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+    if (c >= a.cols) return;
+    const int left = (int)min<int64_t>(a.cols - c, 8);
+    float w[8], wp[8], bp[8];
+    load8_as(a.weight, a.w_bf16, c, left, 1.0f, w);
+    load8_as(a.post_weight, a.w_bf16, c, left, 1.0f, wp);
+    load8_as(a.post_bias, a.w_bf16, c, left, 0.0f, bp);
+    const bool post = a.post != kPostNone;
+    for (int64_t i = blockIdx.y; i < sl.count; i += gridDim.y) {
+        int64_t r0, r1;
+        sl.bounds(i, r0, r1);
+        float dw[8] = {}, dc[8] = {}, s1[8] = {}, s2[8] = {}, dwp[8] = {}, dbp[8] = {};
+        for (int64_t g = r0 / sl.group, r = r0; r < r1; ++g) {
+            const int64_t end = min((g + 1) * sl.group, r1);
+            float gate[8];
+            load8_as(a.gate, a.gate_bf16, g * a.ldg + c, left, 1.0f, gate);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) gate[e] *= a.branch_scale;
+#pragma unroll 2
+            for (; r < end; ++r) {
+                const RowStats st = RowStats::of(a, r);
+                const RowMeans k = means[r];
+                float x[8], d[8], s[8], h[8] = {}, f[8];
+                load8<XB>(a.xo, r * a.ldxo + c, left, x);
+                load8<DB>(a.dy, r * a.lddy + c, left, d);
+                if (a.b) load8<BB>(a.b, r * a.ldb + c, left, h);
+                load8_as(a.dxo, XB, r * a.lddxo + c, left, 0.0f, s);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float xh = (x[e] - st.m) * st.r;
+                    dw[e] += d[e] * xh;
+                    dc[e] += d[e];
+                    d[e] = s[e] + st.r * (d[e] * w[e] - k.t - xh * k.txh);
+                    h[e] = (h[e] - st.pm) * st.pr;
+                    s1[e] += d[e] * h[e];
+                    s2[e] += d[e];
+                    f[e] = a.x_scale * d[e];
+                }
+                store8<XB>(a.dx, r * a.lddx + c, left, f);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float u = d[e] * (gate[e] * wp[e]);
+                    f[e] = post ? st.pr * (u - k.u - h[e] * k.unh) : u;
+                }
+                store8<BB>(a.db, r * a.lddb + c, left, f);
+            }
+            if (sl.k) continue;
+            float f[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                f[e] = a.branch_scale * (wp[e] * s1[e] + bp[e] * s2[e]);
+                dwp[e] += gate[e] * s1[e];
+                dbp[e] += gate[e] * s2[e];
+                s1[e] = s2[e] = 0.0f;
+            }
+            if (a.dgate) store8<0>(a.dgate, g * a.cols + c, left, f);
         }
+        if (!part) continue;
+        const int64_t o = i * 4 * a.cols + c;
+        store8<0>(part, o, left, dw);
+        store8<0>(part, o + a.cols, left, dc);
+        store8<0>(part, o + 2 * a.cols, left, sl.k ? s1 : dwp);
+        store8<0>(part, o + 3 * a.cols, left, sl.k ? s2 : dbp);
     }
 }
 
@@ -226,34 +293,327 @@ __global__ __launch_bounds__(1024) void residual_grad_join_kernel(const Residual
     }
 }
 
+// ---- rows in registers ----
+
+// Where the walk over a slab's rows stands.  With parts of one group (and in
+// general where one gate holds for the slab) the rows follow each other by
+// `step`; with whole groups a walker takes every step-th group, row by row.
+template <int GATE>
+struct Walk {
+    int64_t r, gend;
+    bool in;
+    __device__ __forceinline__ void begin(const Slabs& sl, int64_t r0, int64_t r1, int first) {
+        r = r0 + (GATE ? first * sl.group : first);
+        gend = GATE ? min(r + sl.group, r1) : r1;
+        in = r < r1;
+    }
+    __device__ __forceinline__ bool last_of_group() const { return r + 1 == gend; }
+    __device__ __forceinline__ void next(const Slabs& sl, int64_t r1, int step) {
+        if (!GATE) {
+            r += step;
+        } else if (++r == gend) {
+            r += (step - 1) * sl.group;
+            gend = min(r + sl.group, r1);
+        }
+        in = r < r1;
+    }
+};
+
+// GATE 0: the slab's rows share one row of gates, or have none; its partial
+// sums are dw, dc, S1, S2.  GATE 1, 2: whole groups with a row of gates each,
+// fp32 or bf16; dg is written group by group, and the partial sums are dw, dc,
+// dwp, dbp.
+template <int XB, int BB, int DB, int GATE, int T, int NV>
+__global__ __launch_bounds__(T ? T : 256) void residual_grad_kernel(
+    const ResidualNormGrad a, const Slabs sl, float* __restrict__ part) {
+    constexpr int MULTI = T != 0;
+    __shared__ __attribute__((aligned(16))) float red[MULTI ? 4 * 16 : 4 * 512];
+    const int cols = (int)a.cols;
+    const Place<NV> pl = Place<NV>::template make<MULTI>(cols);
+    const int step = MULTI ? 1 : 4;
+    int64_t r0, r1;
+    sl.bounds(blockIdx.x, r0, r1);
+    Walk<GATE> at;
+    at.begin(sl, r0, r1, MULTI ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x >> 6));
+    int turn = 0;
+    const bool post = a.post != kPostNone, post_layer = a.post == 0;
+    struct Row {
+        Chunk<XB> x[NV], s[NV];
+        Chunk<DB> d[NV];
+        Chunk<BB> b[NV];
+        Chunk<GATE == 2> g[GATE ? NV : 1];
+        RowStats st;
+    };
+    Row in;
+    // operands that are not there are read where others are, and not used
+    const void* dxo = a.dxo ? a.dxo : a.xo;
+    const int64_t lddxo = a.dxo ? a.lddxo : a.ldxo;
+    const bool stream = a.dxo != nullptr;
+    const bool branch = a.b != nullptr;
+    const void* b = branch ? a.b : a.db;
+    const int64_t ldb = branch ? a.ldb : a.lddb;
+    const int64_t group0 = GATE ? r0 / sl.group : 0;
+    auto fetch = [&](const Walk<GATE>& w) __attribute__((always_inline)) {
+        const int64_t row = w.in ? w.r : r1 - 1;
+        in.st = RowStats::of(a, row);
+        const int64_t g = GATE ? (group0 + (uint32_t)(row - r0) / (uint32_t)sl.group) * a.ldg : 0;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            in.x[k].load(a.xo, row * a.ldxo + pl.start(k));
+            in.d[k].load(a.dy, row * a.lddy + pl.start(k));
+            in.s[k].load(dxo, row * lddxo + pl.start(k));
+            in.b[k].load(b, row * ldb + pl.start(k));
+            if (GATE) in.g[k].load(a.gate, g + pl.start(k));
+        }
+    };
+    fetch(at);
+    float w[NV][8], u[NV][8];
+    float dw[NV][8] = {}, dc[NV][8] = {}, s1[NV][8] = {}, s2[NV][8] = {};
+    float dpw[GATE ? NV : 1][8] = {}, dpc[GATE ? NV : 1][8] = {};
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        load_vec8(a.weight, a.w_bf16, pl.start(k), 1.0f, w[k]);
+        load_vec8(a.post_weight, a.w_bf16, pl.start(k), 1.0f, u[k]);
+        float g[8];
+        const bool one = !GATE && a.gate;
+        load_vec8(one ? a.gate : nullptr, a.gate_bf16,
+                  (one && sl.k ? sl.group_of(blockIdx.x) * a.ldg : 0) + pl.start(k), 1.0f, g);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) u[k][e] *= a.branch_scale * g[e];
+    }
+    const float n = (float)cols;
+    while (at.in) {
+        const RowStats st = in.st;
+        const int64_t r = at.r;
+        const bool flush = GATE && at.last_of_group();
+        float xh[NV][8], d[NV][8], sx[NV][8], h[NV][8], g[GATE ? NV : 1][8];
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                xh[k][e] = (in.x[k].at(e) - st.m) * st.r;
+                d[k][e] = in.d[k].at(e);
+                sx[k][e] = stream ? in.s[k].at(e) : 0.0f;
+                h[k][e] = branch ? (in.b[k].at(e) - st.pm) * st.pr : 0.0f;
+                if (GATE) g[k][e] = in.g[k].at(e);
+            }
+        // dx and db may lie on dxo and b, whose last elements two waves hold: all
+        // of a row has arrived before the barrier that its stores come after
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            in.s[k].arrived();
+            in.b[k].arrived();
+        }
+        at.next(sl, r1, step);
+        fetch(at);
+        float s[2] = {0.0f, 0.0f};  // of t xh, and of t
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            float p0 = 0.0f, p1 = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                dw[k][e] += d[k][e] * xh[k][e];
+                dc[k][e] += d[k][e];
+                d[k][e] *= w[k][e];
+                const float t = pl.owns(k, e) ? d[k][e] : 0.0f;
+                p0 += t * xh[k][e];
+                p1 += t;
+            }
+            s[0] += p0;
+            s[1] += p1;
+        }
+        row_sums<MULTI>(s, red, pl.W, turn);
+        const float mx = s[0] / n, mt = a.rms ? 0.0f : s[1] / n;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            float f[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                d[k][e] = sx[k][e] + st.r * (d[k][e] - mt - xh[k][e] * mx);
+                s1[k][e] += d[k][e] * h[k][e];
+                s2[k][e] += d[k][e];
+                f[e] = a.x_scale * d[k][e];
+            }
+            store_chunk<XB>(a.dx, r * a.lddx + pl.start(k), f);
+        }
+        if (flush) {
+            const int64_t at_g = (group0 + (uint32_t)(r - r0) / (uint32_t)sl.group) * a.cols;
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                float f[8], pc[8];
+                load_vec8(a.post_bias, a.w_bf16, pl.start(k), 0.0f, pc);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    f[e] = u[k][e] * s1[k][e] + a.branch_scale * pc[e] * s2[k][e];  // u = bs wp here
+                    dpw[k][e] += a.branch_scale * g[k][e] * s1[k][e];
+                    dpc[k][e] += a.branch_scale * g[k][e] * s2[k][e];
+                    s1[k][e] = s2[k][e] = 0.0f;
+                }
+                if (a.dgate) store_chunk<0>(a.dgate, at_g + pl.start(k), f);
+            }
+        }
+        float mh = 0.0f, mu = 0.0f;
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                d[k][e] *= u[k][e];
+                if (GATE) d[k][e] *= g[k][e];
+            }
+        if (post) {
+            s[0] = s[1] = 0.0f;  // of u nh, and of u
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                float p0 = 0.0f, p1 = 0.0f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float t = pl.owns(k, e) ? d[k][e] : 0.0f;
+                    p0 += t * h[k][e];
+                    p1 += t;
+                }
+                s[0] += p0;
+                s[1] += p1;
+            }
+            row_sums<MULTI>(s, red, pl.W, turn);
+            mh = s[0] / n;
+            mu = post_layer ? s[1] / n : 0.0f;
+        }
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            float f[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = post ? st.pr * (d[k][e] - mu - h[k][e] * mh) : d[k][e];
+            store_chunk<BB>(a.db, r * a.lddb + pl.start(k), f);
+        }
+    }
+    if (!part) return;
+#pragma unroll
+    for (int o = 0; o < 4; ++o) {
+        float* out = part + ((int64_t)blockIdx.x * 4 + o) * cols;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            float(&v)[8] = o == 0 ? dw[k] : o == 1 ? dc[k] : o == 2 ? (GATE ? dpw[k] : s1[k]) : (GATE ? dpc[k] : s2[k]);
+            const int skip = k < NV - 1 ? 0 : pl.skip, c = pl.start(k);
+            if (MULTI) {
+                store_own<0>(out, c, v, skip);
+                continue;
+            }
+            // the four waves hold the same 512 columns of different rows
+            __syncthreads();
+            float* mine = red + (threadIdx.x >> 6) * 512;
+            if (skip == 0) {
+                *(u32x4*)(mine + pl.t) =
+                    (u32x4){as_u32(v[0]), as_u32(v[1]), as_u32(v[2]), as_u32(v[3])};
+                *(u32x4*)(mine + pl.t + 4) =
+                    (u32x4){as_u32(v[4]), as_u32(v[5]), as_u32(v[6]), as_u32(v[7])};
+            } else {
+#pragma unroll
+                for (int e = 1; e < 8; ++e)
+                    if (e >= skip) mine[c - k * 512 + e] = v[e];
+            }
+            __syncthreads();
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int i = h * 256 + threadIdx.x;
+                if (k * 512 + i < cols)
+                    out[k * 512 + i] = (red[i] + red[512 + i]) + (red[1024 + i] + red[1536 + i]);
+            }
+        }
+    }
+}
+
 constexpr int64_t kAnyGrid = 1 << 16;
+
 constexpr int64_t kGridY = 1 << 15;
 
 static bool any_sums(const ResidualNormGrad& a) {
     return a.dweight || a.dbias || a.dpost_weight || a.dpost_bias || a.dgate;
 }
 
+// How rows are held: by waves of their own (T = 0) or by a workgroup of at most
+// T threads, nv chunks per lane; nv = 0: the rows' means first, then tiles.
+struct GradShape {
+    int T, nv, threads;
+    bool whole;  // slabs of whole groups of a gate's rows
+};
+static GradShape grad_shape(int64_t cols, bool whole) {
+    const int waves = (int)((cols + 511) / 512);
+    if (cols < 8 || cols > 8192 || (whole && cols > 6144)) return {0, 0, 256, whole};
+    if (cols <= 512) return {0, 1, 256, whole};
+    if (cols <= 6144) return {waves <= 8 ? 512 : 768, 1, 64 * waves, whole};
+    return {512, 2, 64 * ((waves + 1) / 2), whole};
+}
+// As many slabs as 256 compute units hold workgroups of (12 waves to a unit, 8
+// where a row of gates comes with every row), of 8 rows and more to a walker.
 static Slabs grad_slabs(int64_t rows, int64_t cols, int64_t gate_rows) {
-    return make_slabs(rows, gate_rows, std::min<int64_t>(256, (rows + 15) / 16));
+    const auto slabs = [&](bool whole) {
+        const GradShape sh = grad_shape(cols, whole);
+        const int64_t per = sh.nv == 0 ? 16 : sh.T ? 8 : 16;
+        const int64_t most = sh.nv == 0 ? 256 : 256 * std::max(1, (whole ? 8 : 12) * 64 / sh.threads);
+        return make_slabs(rows, gate_rows, std::min<int64_t>(most, (rows + per - 1) / per));
+    };
+    const Slabs sl = slabs(false);
+    return gate_rows < rows && !sl.k ? slabs(true) : sl;
 }
 
 size_t residual_norm_grad_workspace_bytes(int64_t rows, int64_t cols, int64_t gate_rows) {
     const Slabs sl = grad_slabs(rows, cols, gate_rows);
-    return (size_t)rows * sizeof(RowMeans) + (size_t)sl.count * 4 * (size_t)cols * sizeof(float);
+    const bool whole = gate_rows < rows && !sl.k;
+    const size_t means = grad_shape(cols, whole).nv == 0 ? (size_t)rows * sizeof(RowMeans) : 0;
+    return means + (size_t)sl.count * 4 * (size_t)cols * sizeof(float);
+}
+
+template <int XB, int BB, int DB, int GATE>
+static void go_rows(const GradShape sh, const ResidualNormGrad& a, const Slabs& sl, float* part,
+                    hipStream_t s) {
+#define FP4Q_GO(T_, NV_)                                                                        \
+    if (sh.T == T_ && sh.nv == NV_)                                                             \
+    FP4Q_LAUNCH((residual_grad_kernel<XB, BB, DB, GATE, T_, NV_>), dim3((unsigned)sl.count),    \
+                dim3((unsigned)sh.threads), 0, s, a, sl, part)
+    FP4Q_GO(0, 1);
+    FP4Q_GO(512, 1);
+    FP4Q_GO(768, 1);
+    if constexpr (GATE == 0) FP4Q_GO(512, 2);
+#undef FP4Q_GO
+}
+template <int XB, int BB, int DB>
+static void go_gate(const GradShape sh, const ResidualNormGrad& a, const Slabs& sl, RowMeans* means,
+                    float* part, hipStream_t s) {
+    if (sh.nv == 0) {
+        const int64_t tiles = (a.cols + 2047) / 2048;
+        FP4Q_LAUNCH((residual_grad_tile_kernel<XB, BB, DB>),
+                    dim3((unsigned)tiles, (unsigned)std::min(sl.count, kGridY)), dim3(256), 0, s, a,
+                    means, sl, part);
+    } else if (!sh.whole) {
+        go_rows<XB, BB, DB, 0>(sh, a, sl, part, s);
+    } else if (!a.gate_bf16) {
+        go_rows<XB, BB, DB, 1>(sh, a, sl, part, s);
+    } else {
+        go_rows<XB, BB, DB, 2>(sh, a, sl, part, s);
+    }
+}
+template <int XB, int BB>
+static void go_dy(const GradShape sh, const ResidualNormGrad& a, const Slabs& sl, RowMeans* means,
+                  float* part, hipStream_t s) {
+    a.dy_bf16 ? go_gate<XB, BB, 1>(sh, a, sl, means, part, s)
+              : go_gate<XB, BB, 0>(sh, a, sl, means, part, s);
 }
 
 hipError_t launch_residual_norm_grad(const ResidualNormGrad& a, void* ws, hipStream_t s) {
     const Slabs sl = grad_slabs(a.rows, a.cols, a.gate_rows);
+    const GradShape sh = grad_shape(a.cols, a.gate_rows < a.rows && !sl.k);
+    const bool sums = any_sums(a);
     RowMeans* means = (RowMeans*)ws;
-    float* part = (float*)(means + a.rows);
-    const unsigned rows = (unsigned)std::min(a.rows, kAnyGrid);
-    FP4Q_LAUNCH(residual_grad_rows_kernel, dim3(rows), dim3(256), 0, s, a, means);
-    if (any_sums(a))  // before dx and db, which may lie on dxo and b
-        FP4Q_LAUNCH(residual_grad_cols_kernel,
-                    dim3((unsigned)((a.cols + 255) / 256), (unsigned)std::min(sl.count, kGridY)),
-                    dim3(256), 0, s, a, means, sl, part);
-    FP4Q_LAUNCH(residual_grad_any_kernel, dim3(rows), dim3(256), 0, s, a, means);
-    if (any_sums(a)) {
+    float* part = sh.nv == 0 ? (float*)(means + a.rows) : (float*)ws;
+    if (sh.nv == 0)
+        FP4Q_LAUNCH(residual_grad_rows_kernel, dim3((unsigned)std::min(a.rows, kAnyGrid)), dim3(256), 0,
+                    s, a, means);
+    float* p = sums ? part : nullptr;
+    if (a.x_bf16)
+        a.b_bf16 ? go_dy<1, 1>(sh, a, sl, means, p, s) : go_dy<1, 0>(sh, a, sl, means, p, s);
+    else
+        a.b_bf16 ? go_dy<0, 1>(sh, a, sl, means, p, s) : go_dy<0, 0>(sh, a, sl, means, p, s);
+    if (sums) {
         const int64_t gates = a.dgate && sl.k ? std::min(sl.count / sl.k, kGridY) : 0;
         const int64_t groups = (a.cols + 15) / 16;
         for (int64_t g = 0; g < groups; g += kJoinGroups)

@@ -48,6 +48,11 @@ struct Chunk {
             v[BF16T ? 0 : 1] = *(const u32x4_a4*)((const float*)p + i + 4);
         }
     }
+    // Waits here for the load.
+    __device__ __forceinline__ void arrived() const {
+        asm volatile("" ::"v"(v[0][0]));
+        if (!BF16T) asm volatile("" ::"v"(v[BF16T ? 0 : 1][0]));
+    }
     __device__ __forceinline__ float at(int e) const {
         if (BF16T) {
             const uint32_t w = v[0][e >> 1];
