@@ -16,6 +16,15 @@
 
 namespace fp4q {
 
+// Pointers that come from memory are generic to the compiler, and generic
+// accesses wait on the LDS counter too: global<T>(p) is p in global memory.
+template <class T>
+using Global = T __attribute__((address_space(1))) *;
+template <class T>
+__device__ __forceinline__ Global<T> global(const void* p) {
+    return (Global<T>)p;
+}
+
 constexpr int kTensors = 192;            // descriptors per launch: 4 KB of kernel arguments
 constexpr int64_t kChunk = 16384;        // elements per workgroup
 constexpr int64_t kMaxGroups = 1 << 22;  // workgroups per launch: 2^30 threads
@@ -54,52 +63,131 @@ __device__ __forceinline__ Piece piece_of(const Tensors& t, uint32_t group) {
     q.i1 = min(q.i0 + kChunk, n & ~kBf16Bit);
     return q;
 }
-__device__ __forceinline__ float element(const Piece& q, int64_t i) {
-    return q.bf16 ? as_f32((uint32_t)((const uint16_t*)q.p)[i] << 16) : ((const float*)q.p)[i];
+// 16 bytes of a gradient at any element, and its values.
+template <int B16>
+struct Vec {
+    static constexpr int N = B16 ? 8 : 4;
+    u32x4 w;
+    __device__ __forceinline__ void load(const void* p, int64_t i) {
+        w = B16 ? *global<const u32x4_a2>((const uint16_t*)p + i) : *global<const u32x4_a4>((const float*)p + i);
+    }
+    __device__ __forceinline__ void store(void* p, int64_t i) const {
+        if (B16)
+            *global<u32x4_a2>((uint16_t*)p + i) = w;
+        else
+            *global<u32x4_a4>((float*)p + i) = w;
+    }
+    __device__ __forceinline__ float at(int e) const {
+        if (B16) return (e & 1) ? bf16_hi(w[e >> 1]) : bf16_lo(w[e >> 1]);
+        return as_f32(w[e & 3]);
+    }
+};
+template <int B16>
+__device__ __forceinline__ float element(const void* p, int64_t i) {
+    return B16 ? as_f32((uint32_t)global<const uint16_t>(p)[i] << 16) : global<const float>(p)[i];
 }
 
-__global__ __launch_bounds__(256) void grad_norm_kernel(const Tensors t, int largest,
-                                                        double* __restrict__ part) {
-    __shared__ double red[256];
-    const Piece q = piece_of(t, blockIdx.x);
-    double s = 0.0;
-    uint32_t top = 0;
-    for (int64_t i = q.i0 + threadIdx.x; i < q.i1; i += 256) {
-        const float g = element(q, i);
-        top = max(top, as_u32(g) & 0x7FFFFFFFu);
-        s += (double)g * (double)g;
+// Sums of squares, or the bits of the largest magnitude, which order
+// magnitudes as whole numbers do, infinity above the finite ones and NaN above
+// it.  Four sums take turns, so that few additions follow each other.
+template <int MAX>
+struct Total {
+    double s[4];
+    uint32_t top;
+    __device__ __forceinline__ Total() : s{0.0, 0.0, 0.0, 0.0}, top(0) {}
+    __device__ __forceinline__ void add(float g, int k) {
+        if (MAX)
+            top = max(top, as_u32(g) & 0x7FFFFFFFu);
+        else
+            s[k & 3] = __builtin_fma((double)g, (double)g, s[k & 3]);
     }
-    red[threadIdx.x] = largest ? (double)top : s;
+};
+
+// Of all lanes of a workgroup, in thread 0.
+template <int MAX>
+__device__ __forceinline__ double total_of(double v, double* red) {
+#pragma unroll
+    for (int k = 32; k; k >>= 1) {
+        const double o = __shfl_xor(v, k);
+        v = MAX ? fmax(v, o) : v + o;
+    }
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
     __syncthreads();
-    for (int k = 128; k; k >>= 1) {
-        if ((int)threadIdx.x < k)
-            red[threadIdx.x] = largest ? fmax(red[threadIdx.x], red[threadIdx.x + k])
-                                       : red[threadIdx.x] + red[threadIdx.x + k];
-        __syncthreads();
-    }
-    if (threadIdx.x == 0) part[blockIdx.x] = red[0];
+    if (threadIdx.x) return 0.0;
+    v = red[0];
+    for (int k = 1; k < (int)(blockDim.x >> 6); ++k) v = MAX ? fmax(v, red[k]) : v + red[k];
+    return v;
 }
 
-__global__ __launch_bounds__(1024) void grad_norm_join_kernel(const double* __restrict__ part,
-                                                              int64_t n, int largest,
+constexpr int kThreads = 256, kAhead = 8;  // loads of a lane in flight
+
+// f(vector, its first element) over the whole vectors of a piece, kAhead of a
+// lane's at a time, f1(element's place) over the rest.
+template <int B16, class F, class F1>
+__device__ __forceinline__ void over(const Piece& q, F f, F1 f1) {
+    constexpr int N = Vec<B16>::N, SPAN = kThreads * N;
+    const int n = (int)(q.i1 - q.i0);
+    int i = threadIdx.x * N;
+    for (; i - (int)threadIdx.x * N + kAhead * SPAN <= n; i += kAhead * SPAN) {
+        Vec<B16> v[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) v[k].load(q.p, q.i0 + i + k * SPAN);
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) f(v[k], q.i0 + i + k * SPAN);
+    }
+    if (i + N <= n) {
+        Vec<B16> v[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+            if (i + k * SPAN + N <= n) v[k].load(q.p, q.i0 + i + k * SPAN);
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+            if (i + k * SPAN + N <= n) f(v[k], q.i0 + i + k * SPAN);
+    }
+    const int rest = (n & ~(N - 1)) + threadIdx.x;
+    if (rest < n) f1(q.i0 + rest);
+}
+
+template <int MAX, int B16>
+__device__ __forceinline__ double piece_total(const Piece& q) {
+    Total<MAX> t;
+    over<B16>(
+        q,
+        [&](const Vec<B16>& v, int64_t) __attribute__((always_inline)) {
+#pragma unroll
+            for (int e = 0; e < Vec<B16>::N; ++e) t.add(v.at(e), e);
+        },
+        [&](int64_t i) __attribute__((always_inline)) { t.add(element<B16>(q.p, i), 0); });
+    return MAX ? (double)t.top : (t.s[0] + t.s[1]) + (t.s[2] + t.s[3]);
+}
+
+template <int MAX>
+__global__ __launch_bounds__(kThreads) void grad_norm_kernel(const Tensors t, double* __restrict__ part) {
+    __shared__ double red[kThreads / 64];
+    const Piece q = piece_of(t, blockIdx.x);
+    const double v = total_of<MAX>(q.bf16 ? piece_total<MAX, 1>(q) : piece_total<MAX, 0>(q), red);
+    if (threadIdx.x == 0) part[blockIdx.x] = v;
+}
+
+template <int MAX>
+__global__ __launch_bounds__(1024) void grad_norm_join_kernel(const double* __restrict__ part, int64_t n,
                                                               double max_norm, double eps,
                                                               float* __restrict__ norm,
                                                               float* __restrict__ scale) {
-    __shared__ double red[1024];
-    double s = 0.0;
-    for (int64_t i = threadIdx.x; i < n; i += 1024) s = largest ? fmax(s, part[i]) : s + part[i];
-    red[threadIdx.x] = s;
-    __syncthreads();
-    for (int k = 512; k; k >>= 1) {
-        if ((int)threadIdx.x < k)
-            red[threadIdx.x] = largest ? fmax(red[threadIdx.x], red[threadIdx.x + k])
-                                       : red[threadIdx.x] + red[threadIdx.x + k];
-        __syncthreads();
+    __shared__ double red[16];
+    double s[4] = {0.0, 0.0, 0.0, 0.0};
+#pragma unroll 2
+    for (int64_t i = threadIdx.x; i < n; i += 4096) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const double v = i + k * 1024 < n ? part[i + k * 1024] : 0.0;
+            s[k] = MAX ? fmax(s[k], v) : s[k] + v;
+        }
     }
+    const double all = total_of<MAX>(MAX ? fmax(fmax(s[0], s[1]), fmax(s[2], s[3]))
+                                         : (s[0] + s[1]) + (s[2] + s[3]), red);
     if (threadIdx.x) return;
-    // the largest magnitude's bits, which order magnitudes as whole numbers do,
-    // infinity above the finite ones and NaN above it
-    const double v = largest ? (double)as_f32((uint32_t)red[0]) : sqrt(red[0]);
+    const double v = MAX ? (double)as_f32((uint32_t)all) : sqrt(all);
     if (norm) *norm = (float)v;
     if (scale) {
         const double d = v + eps, c = max_norm / d;
@@ -107,17 +195,36 @@ __global__ __launch_bounds__(1024) void grad_norm_join_kernel(const double* __re
     }
 }
 
-__global__ __launch_bounds__(256) void grad_scale_kernel(const Tensors t,
-                                                         const float* __restrict__ scale) {
-    const Piece q = piece_of(t, blockIdx.x);
+template <int B16>
+__device__ __forceinline__ void scale_piece(const Piece& q, float f) {
+    over<B16>(
+        q,
+        [&](Vec<B16> v, int64_t i) __attribute__((always_inline)) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (B16) {
+                    const bf16x2_t p = {(__bf16)(v.at(2 * k) * f), (__bf16)(v.at(2 * k + 1) * f)};
+                    v.w[k] = __builtin_bit_cast(uint32_t, p);
+                } else {
+                    v.w[k] = as_u32(v.at(k) * f);
+                }
+            }
+            v.store(q.p, i);
+        },
+        [&](int64_t i) __attribute__((always_inline)) {
+            const float g = element<B16>(q.p, i) * f;
+            if (B16)
+                global<uint16_t>(q.p)[i] = (uint16_t)f32_to_bf16_bits(g);
+            else
+                global<float>(q.p)[i] = g;
+        });
+}
+__global__ __launch_bounds__(kThreads) void grad_scale_kernel(const Tensors t,
+                                                              const float* __restrict__ scale) {
     const float f = *scale;
-    for (int64_t i = q.i0 + threadIdx.x; i < q.i1; i += 256) {
-        const float g = element(q, i) * f;
-        if (q.bf16)
-            ((uint16_t*)q.p)[i] = (uint16_t)f32_to_bf16_bits(g);
-        else
-            ((float*)q.p)[i] = g;
-    }
+    if (f == 1.0f) return;
+    const Piece q = piece_of(t, blockIdx.x);
+    q.bf16 ? scale_piece<1>(q, f) : scale_piece<0>(q, f);
 }
 
 static int64_t groups_of(const fp4q_tensor_t& t) { return (t.numel + kChunk - 1) / kChunk; }
@@ -166,18 +273,25 @@ hipError_t launch_grad_norm(const fp4q_tensor_t* t, int n, bool largest, double 
     double* part = (double*)ws;
     int64_t groups = 0;
     const hipError_t e = for_tensors(t, n, [&](const Tensors& a, int64_t now, int64_t before) {
-        FP4Q_LAUNCH(grad_norm_kernel, dim3((unsigned)now), dim3(256), 0, s, a, (int)largest, part + before);
+        if (largest)
+            FP4Q_LAUNCH(grad_norm_kernel<1>, dim3((unsigned)now), dim3(kThreads), 0, s, a, part + before);
+        else
+            FP4Q_LAUNCH(grad_norm_kernel<0>, dim3((unsigned)now), dim3(kThreads), 0, s, a, part + before);
         groups = before + now;
     });
     if (e != hipSuccess) return e;
-    FP4Q_LAUNCH(grad_norm_join_kernel, dim3(1), dim3(1024), 0, s, part, groups, (int)largest, max_norm,
-                eps, norm, scale);
+    if (largest)
+        FP4Q_LAUNCH(grad_norm_join_kernel<1>, dim3(1), dim3(1024), 0, s, part, groups, max_norm, eps, norm,
+                    scale);
+    else
+        FP4Q_LAUNCH(grad_norm_join_kernel<0>, dim3(1), dim3(1024), 0, s, part, groups, max_norm, eps, norm,
+                    scale);
     return hipGetLastError();
 }
 
 hipError_t launch_grad_scale(const fp4q_tensor_t* t, int n, const float* scale, hipStream_t s) {
     return for_tensors(t, n, [&](const Tensors& a, int64_t now, int64_t) {
-        FP4Q_LAUNCH(grad_scale_kernel, dim3((unsigned)now), dim3(256), 0, s, a, scale);
+        FP4Q_LAUNCH(grad_scale_kernel, dim3((unsigned)now), dim3(kThreads), 0, s, a, scale);
     });
 }
 
