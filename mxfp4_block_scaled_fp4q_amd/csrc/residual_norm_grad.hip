@@ -1,6 +1,7 @@
 // The backward pass of the residual norms (the formulas stand at the head of
 // residual_norm.hip).
 #include <algorithm>
+#include <type_traits>
 
 #include "residual_norm.h"
 #include "row_norm.h"
@@ -11,39 +12,43 @@ namespace fp4q {
 
 // Slabs of rows that each leave one row of partial column sums.  A slab holds
 // whole groups of rows that share a gate, or, where a group is longer than a
-// slab or the only one, one of the k even parts of one group.
+// slab or the only one, one of the k parts of one group (the last may be short,
+// or empty in a short group).
 struct Slabs {
     int64_t count, rows, group;  // group: rows of a group
     int64_t k;                   // slabs of a group, 0 with whole groups
-    int64_t groups;              // groups of a slab, with whole groups
-    __host__ __device__ void bounds(int64_t i, int64_t& r0, int64_t& r1) const {
+    int64_t each;                // rows of a slab
+    FastDiv div;                 // by k
+    __device__ __forceinline__ void bounds(uint32_t i, int64_t& r0, int64_t& r1) const {
         if (k) {
-            const int64_t g = i / k, j = i % k, base = g * group;
-            const int64_t n = rows - base < group ? rows - base : group;
-            r0 = base + n * j / k;
-            r1 = base + n * (j + 1) / k;
+            const uint32_t g = fastdiv(i, div);
+            r0 = g * group + (i - g * (uint32_t)k) * each;
+            r1 = min(min(r0 + each, (g + 1) * group), rows);
         } else {
-            r0 = i * groups * group;
-            r1 = rows - r0 < groups * group ? rows : r0 + groups * group;
+            r0 = i * each;
+            r1 = min(r0 + each, rows);
         }
     }
-    __host__ __device__ int64_t group_of(int64_t i) const { return i / k; }  // with parts
+    __device__ __forceinline__ int64_t group_of(uint32_t i) const { return fastdiv(i, div); }  // of parts
 };
-static Slabs make_slabs(int64_t rows, int64_t gate_rows, int64_t want) {
+// At most `most` slabs of at least `least` rows, or as many as there are groups.
+static Slabs make_slabs(int64_t rows, int64_t gate_rows, int64_t most, int64_t least) {
     Slabs s;
     s.rows = rows;
     s.group = std::min(gate_rows, rows);
     const int64_t all = (rows + s.group - 1) / s.group;
-    const int64_t each = (rows + want - 1) / want;
+    const int64_t each = std::max(least, (rows + most - 1) / most);
     if (s.group > each || all == 1) {
-        s.k = (s.group + each - 1) / each;
-        s.groups = 0;
+        const int64_t k = std::max<int64_t>(1, std::min((s.group + each - 1) / each, most / all));
+        s.each = (s.group + k - 1) / k;
+        s.k = (s.group + s.each - 1) / s.each;
         s.count = all * s.k;
     } else {
         s.k = 0;
-        s.groups = each / s.group;
-        s.count = (all + s.groups - 1) / s.groups;
+        s.each = each / s.group * s.group;
+        s.count = (rows + s.each - 1) / s.each;
     }
+    s.div = make_fastdiv((uint32_t)std::max<int64_t>(s.k, 1));
     return s;
 }
 
@@ -118,25 +123,89 @@ __global__ __launch_bounds__(256) void residual_grad_rows_kernel(const ResidualN
     }
 }
 
+// The same with the row in registers, two chunks of 8 elements to a lane (8 to
+// 16384 columns).
+template <int XB, int BB, int DB>
+__global__ __launch_bounds__(1024) void residual_grad_means_kernel(const ResidualNormGrad a,
+                                                                   RowMeans* __restrict__ means) {
+    __shared__ float red[4 * 16];
+    const int cols = (int)a.cols;
+    const Place<2> pl = Place<2>::template make<1>(cols);
+    int turn = 0;
+    const float rn = 1.0f / (float)cols;
+    const void* dxo = a.dxo ? a.dxo : a.xo;
+    const int64_t lddxo = a.dxo ? a.lddxo : a.ldxo;
+    const bool post = a.post != kPostNone;
+    for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
+        const RowStats st = RowStats::of(a, r);
+        Chunk<XB> x[2], sx[2];
+        Chunk<DB> dy[2];
+        Chunk<BB> b[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            x[k].load(a.xo, r * a.ldxo + pl.start(k));
+            dy[k].load(a.dy, r * a.lddy + pl.start(k));
+        }
+        if (post) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                sx[k].load(dxo, r * lddxo + pl.start(k));
+                b[k].load(a.b, r * a.ldb + pl.start(k));
+            }
+        }
+        float xh[2][8], t[2][8], s[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            load_vec8(a.weight, a.w_bf16, pl.start(k), 1.0f, t[k]);
+            float p0 = 0.0f, p1 = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                xh[k][e] = (x[k].at(e) - st.m) * st.r;
+                t[k][e] *= dy[k].at(e);
+                const float o = pl.owns(k, e) ? t[k][e] : 0.0f;
+                p0 += o * xh[k][e];
+                p1 += o;
+            }
+            s[0] += p0;
+            s[1] += p1;
+        }
+        row_sums<1>(s, red, pl.W, turn);
+        RowMeans m = {s[0] * rn, a.rms ? 0.0f : s[1] * rn, 0.0f, 0.0f};
+        if (post) {
+            const int64_t g0 = r / a.gate_rows * a.ldg;
+            s[0] = s[1] = 0.0f;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                float wp[8], g[8], p0 = 0.0f, p1 = 0.0f;
+                load_vec8(a.post_weight, a.w_bf16, pl.start(k), 1.0f, wp);
+                load_vec8(a.gate, a.gate_bf16, g0 + pl.start(k), 1.0f, g);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float d = (a.dxo ? sx[k].at(e) : 0.0f) + st.r * (t[k][e] - m.t - xh[k][e] * m.txh);
+                    const float o = pl.owns(k, e) ? d * (a.branch_scale * wp[e] * g[e]) : 0.0f;
+                    p0 += o * ((b[k].at(e) - st.pm) * st.pr);
+                    p1 += o;
+                }
+                s[0] += p0;
+                s[1] += p1;
+            }
+            row_sums<1>(s, red, pl.W, turn);
+            m.unh = s[0] * rn;
+            if (a.post == 0) m.u = s[1] * rn;
+        }
+        if (threadIdx.x == 0) means[r] = m;
+    }
+}
+
 // Outputs and column sums where the rows' means are known: 8 columns to a lane,
 // 2048 to a workgroup, over the rows of a slab.  The sums are four rows of
 // `cols` floats: dw, dc, and S1, S2 of the slab's group, or with whole groups
 // dwp, dbp (the groups' dg is then written at once).  Each element is read and
 // written by one lane, so that dx and db may lie on dxo and b.
-template <class F>
-__device__ __forceinline__ void each8(int left, F f) {
-    if (left >= 8) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f(e);
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (e < left) f(e);
-    }
-}
-template <int B16>
+// FULL: all 8 elements are there, otherwise the first `left`.
+template <int B16, int FULL>
 __device__ __forceinline__ void load8(const void* p, int64_t i, int left, float (&f)[8]) {
-    if (left >= 8) {
+    if (FULL) {
         Chunk<B16> c;
         c.load(p, i);
 #pragma unroll
@@ -146,37 +215,42 @@ __device__ __forceinline__ void load8(const void* p, int64_t i, int left, float 
         for (int e = 0; e < 8; ++e) f[e] = e < left ? load1<B16>(p, i + e) : 0.0f;
     }
 }
-template <int B16>
+template <int B16, int FULL>
 __device__ __forceinline__ void store8(void* p, int64_t i, int left, const float (&f)[8]) {
-    if (left >= 8)
+    if (FULL) {
         store_chunk<B16>(p, i, f);
-    else
-        each8(left, [&](int e) { store1<B16>(p, i + e, f[e]); });
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (e < left) store1<B16>(p, i + e, f[e]);
+    }
 }
+template <int FULL>
 __device__ __forceinline__ void load8_as(const void* p, int bf16, int64_t i, int left, float none,
                                          float (&f)[8]) {
     if (!p) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[e] = none;
     } else if (bf16) {
-        load8<1>(p, i, left, f);
+        load8<1, FULL>(p, i, left, f);
     } else {
-        load8<0>(p, i, left, f);
+        load8<0, FULL>(p, i, left, f);
     }
 }
 
-template <int XB, int BB, int DB>
-__global__ __launch_bounds__(256) void residual_grad_tile_kernel(const ResidualNormGrad a,
-                                                                 const RowMeans* __restrict__ means,
-                                                                 const Slabs sl, float* part) {
-    const int64_t c = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
-    if (c >= a.cols) return;
-    const int left = (int)min<int64_t>(a.cols - c, 8);
+template <int XB, int BB, int DB, int FULL>
+__device__ __forceinline__ void tile(const ResidualNormGrad& a, const RowMeans* __restrict__ means,
+                                     const Slabs& sl, float* part, int64_t c, int left) {
     float w[8], wp[8], bp[8];
-    load8_as(a.weight, a.w_bf16, c, left, 1.0f, w);
-    load8_as(a.post_weight, a.w_bf16, c, left, 1.0f, wp);
-    load8_as(a.post_bias, a.w_bf16, c, left, 0.0f, bp);
+    load8_as<FULL>(a.weight, a.w_bf16, c, left, 1.0f, w);
+    load8_as<FULL>(a.post_weight, a.w_bf16, c, left, 1.0f, wp);
+    load8_as<FULL>(a.post_bias, a.w_bf16, c, left, 0.0f, bp);
     const bool post = a.post != kPostNone;
+    // operands that are not there are read where others are, and not used
+    const void* dxo = a.dxo ? a.dxo : a.xo;
+    const int64_t lddxo = a.dxo ? a.lddxo : a.ldxo;
+    const void* b = a.b ? a.b : a.db;
+    const int64_t ldb = a.b ? a.ldb : a.lddb;
     for (int64_t i = blockIdx.y; i < sl.count; i += gridDim.y) {
         int64_t r0, r1;
         sl.bounds(i, r0, r1);
@@ -184,36 +258,36 @@ __global__ __launch_bounds__(256) void residual_grad_tile_kernel(const ResidualN
         for (int64_t g = r0 / sl.group, r = r0; r < r1; ++g) {
             const int64_t end = min((g + 1) * sl.group, r1);
             float gate[8];
-            load8_as(a.gate, a.gate_bf16, g * a.ldg + c, left, 1.0f, gate);
+            load8_as<FULL>(a.gate, a.gate_bf16, g * a.ldg + c, left, 1.0f, gate);
 #pragma unroll
             for (int e = 0; e < 8; ++e) gate[e] *= a.branch_scale;
 #pragma unroll 2
             for (; r < end; ++r) {
                 const RowStats st = RowStats::of(a, r);
                 const RowMeans k = means[r];
-                float x[8], d[8], s[8], h[8] = {}, f[8];
-                load8<XB>(a.xo, r * a.ldxo + c, left, x);
-                load8<DB>(a.dy, r * a.lddy + c, left, d);
-                if (a.b) load8<BB>(a.b, r * a.ldb + c, left, h);
-                load8_as(a.dxo, XB, r * a.lddxo + c, left, 0.0f, s);
+                float x[8], d[8], s[8], h[8], f[8];
+                load8<XB, FULL>(a.xo, r * a.ldxo + c, left, x);
+                load8<DB, FULL>(a.dy, r * a.lddy + c, left, d);
+                load8<BB, FULL>(b, r * ldb + c, left, h);
+                load8<XB, FULL>(dxo, r * lddxo + c, left, s);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const float xh = (x[e] - st.m) * st.r;
                     dw[e] += d[e] * xh;
                     dc[e] += d[e];
-                    d[e] = s[e] + st.r * (d[e] * w[e] - k.t - xh * k.txh);
-                    h[e] = (h[e] - st.pm) * st.pr;
+                    d[e] = (a.dxo ? s[e] : 0.0f) + st.r * (d[e] * w[e] - k.t - xh * k.txh);
+                    h[e] = a.b ? (h[e] - st.pm) * st.pr : 0.0f;
                     s1[e] += d[e] * h[e];
                     s2[e] += d[e];
                     f[e] = a.x_scale * d[e];
                 }
-                store8<XB>(a.dx, r * a.lddx + c, left, f);
+                store8<XB, FULL>(a.dx, r * a.lddx + c, left, f);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const float u = d[e] * (gate[e] * wp[e]);
                     f[e] = post ? st.pr * (u - k.u - h[e] * k.unh) : u;
                 }
-                store8<BB>(a.db, r * a.lddb + c, left, f);
+                store8<BB, FULL>(a.db, r * a.lddb + c, left, f);
             }
             if (sl.k) continue;
             float f[8];
@@ -224,80 +298,143 @@ __global__ __launch_bounds__(256) void residual_grad_tile_kernel(const ResidualN
                 dbp[e] += gate[e] * s2[e];
                 s1[e] = s2[e] = 0.0f;
             }
-            if (a.dgate) store8<0>(a.dgate, g * a.cols + c, left, f);
+            if (a.dgate) store8<0, FULL>(a.dgate, g * a.cols + c, left, f);
         }
         if (!part) continue;
         const int64_t o = i * 4 * a.cols + c;
-        store8<0>(part, o, left, dw);
-        store8<0>(part, o + a.cols, left, dc);
-        store8<0>(part, o + 2 * a.cols, left, sl.k ? s1 : dwp);
-        store8<0>(part, o + 3 * a.cols, left, sl.k ? s2 : dbp);
+        store8<0, FULL>(part, o, left, dw);
+        store8<0, FULL>(part, o + a.cols, left, dc);
+        store8<0, FULL>(part, o + 2 * a.cols, left, sl.k ? s1 : dwp);
+        store8<0, FULL>(part, o + 3 * a.cols, left, sl.k ? s2 : dbp);
     }
 }
+template <int XB, int BB, int DB>
+__global__ __launch_bounds__(256) void residual_grad_tile_kernel(const ResidualNormGrad a,
+                                                                 const RowMeans* __restrict__ means,
+                                                                 const Slabs sl, float* part) {
+    const int64_t c = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+    if (c + 8 <= a.cols)
+        tile<XB, BB, DB, 1>(a, means, sl, part, c, 8);
+    else if (c < a.cols)
+        tile<XB, BB, DB, 0>(a, means, sl, part, c, (int)(a.cols - c));
+}
 
-// Adds up the rows of partial sums: 16 columns per workgroup, 64 groups of 16
-// lanes over the slabs, so that few loads follow each other.  blockIdx.y: dw,
-// dc, dwp, dbp, then the gate's groups, grid_y apart.
+// Adds up the rows of partial sums: 64 columns per workgroup, 4 to a lane, 64
+// groups of 16 lanes over the slabs, so that few loads follow each other.
+// blockIdx.y: dw, dc, dwp, dbp, then the gate's groups, gridDim.y - 4 apart.
 constexpr int64_t kJoinGroups = 1 << 21;
-__device__ __forceinline__ float join16(float s, float (*red)[16]) {
+constexpr int kFewParts = 16;
+__device__ __forceinline__ void join64(float (&v)[4], float (*red)[64]) {
     const int l = threadIdx.x & 15, wave = threadIdx.x >> 6;
-    s = rows_sum(s);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = rows_sum(v[e]);
     __syncthreads();
-    if ((threadIdx.x & 63) < 16) red[wave][l] = s;
+    if ((threadIdx.x & 63) < 16) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) red[wave][4 * l + e] = v[e];
+    }
     __syncthreads();
-    const int r = (threadIdx.x & 63) >> 4;
-    return rows_sum((red[r][l] + red[4 + r][l]) + (red[8 + r][l] + red[12 + r][l]));
+    // thread t < 64: column t
+    float s = 0.0f;
+    if (threadIdx.x < 64) {
+#pragma unroll
+        for (int i = 0; i < 16; i += 4)
+            s += (red[i][threadIdx.x] + red[i + 1][threadIdx.x]) +
+                 (red[i + 2][threadIdx.x] + red[i + 3][threadIdx.x]);
+    }
+    v[0] = s;
 }
 __global__ __launch_bounds__(1024) void residual_grad_join_kernel(const ResidualNormGrad a,
                                                                   const float* __restrict__ part,
                                                                   const Slabs sl, int64_t group0) {
-    __shared__ float red[16][16];
-    const int64_t c = (group0 + blockIdx.x) * 16 + (threadIdx.x & 15);
-    const bool in = c < a.cols;
+    __shared__ float red[16][64];
+    const int64_t c64 = (group0 + blockIdx.x) * 64, c = c64 + (threadIdx.x & 15) * 4;
+    const int left = (int)max<int64_t>(0, min<int64_t>(a.cols - c, 4));
     const int first = threadIdx.x >> 4;
-    const float* p = part + c;
+    auto row = [&](int64_t i, int y, float (&v)[4]) __attribute__((always_inline)) {
+        const float* p = part + (i * 4 + y) * a.cols + c;
+        if (left == 4) {
+            const u32x4 w = *(const u32x4_a4*)p;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = as_f32(w[e]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = e < left ? p[e] : 0.0f;
+        }
+    };
+    const bool writes = threadIdx.x < 64 && c64 + threadIdx.x < a.cols;
     if (blockIdx.y < 4) {
         const int y = blockIdx.y;
         float* out = y == 0 ? a.dweight : y == 1 ? a.dbias : y == 2 ? a.dpost_weight : a.dpost_bias;
         if (!out) return;
         const bool scaled = y >= 2 && sl.k;
-        float s = 0.0f;
-        if (in) {
-            for (int64_t i = first; i < sl.count; i += 64) {
-                float v = p[(i * 4 + y) * a.cols];
+        float s[4] = {};
+#pragma unroll 4
+        for (int64_t i = first; i < sl.count; i += 64) {
+            float v[4];
+            row(i, y, v);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
                 if (scaled) {
-                    v *= a.branch_scale;
-                    if (a.gate) v *= load_as(a.gate, a.gate_bf16, sl.group_of(i) * a.ldg + c);
+                    v[e] *= a.branch_scale;
+                    if (a.gate && e < left) v[e] *= load_as(a.gate, a.gate_bf16, sl.group_of(i) * a.ldg + c + e);
                 }
-                s += v;
+                s[e] += v[e];
             }
         }
-        s = join16(s, red);
-        if (threadIdx.x < 16 && in) out[c] = s;
+        join64(s, red);
+        if (writes) out[c64 + threadIdx.x] = s[0];
         return;
     }
-    const float wp = in ? vec1(a.post_weight, a.w_bf16, c, 1.0f) : 0.0f;
-    const float bp = in ? vec1(a.post_bias, a.w_bf16, c, 0.0f) : 0.0f;
     const int64_t groups = sl.count / sl.k;
+    if (sl.k <= kFewParts) {  // 16 lanes to a group of gates
+        for (int64_t g = (blockIdx.y - 4) * 64 + first; g < groups; g += (gridDim.y - 4) * 64) {
+            float s1[4] = {}, s2[4] = {};
+            for (int64_t i = 0; i < sl.k; ++i) {
+                float v1[4], v2[4];
+                row(g * sl.k + i, 2, v1);
+                row(g * sl.k + i, 3, v2);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    s1[e] += v1[e];
+                    s2[e] += v2[e];
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (e < left)
+                    a.dgate[g * a.cols + c + e] =
+                        a.branch_scale * (vec1(a.post_weight, a.w_bf16, c + e, 1.0f) * s1[e] +
+                                          vec1(a.post_bias, a.w_bf16, c + e, 0.0f) * s2[e]);
+        }
+        return;
+    }
+    const float wp = writes ? vec1(a.post_weight, a.w_bf16, c64 + threadIdx.x, 1.0f) : 0.0f;
+    const float bp = writes ? vec1(a.post_bias, a.w_bf16, c64 + threadIdx.x, 0.0f) : 0.0f;
     for (int64_t g = blockIdx.y - 4; g < groups; g += gridDim.y - 4) {
-        float s1 = 0.0f, s2 = 0.0f;
-        if (in) {
-            for (int64_t i = first; i < sl.k; i += 64) {
-                s1 += p[((g * sl.k + i) * 4 + 2) * a.cols];
-                s2 += p[((g * sl.k + i) * 4 + 3) * a.cols];
+        float s1[4] = {}, s2[4] = {};
+#pragma unroll 4
+        for (int64_t i = first; i < sl.k; i += 64) {
+            float v1[4], v2[4];
+            row(g * sl.k + i, 2, v1);
+            row(g * sl.k + i, 3, v2);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                s1[e] += v1[e];
+                s2[e] += v2[e];
             }
         }
-        s1 = join16(s1, red);
-        s2 = join16(s2, red);
-        if (threadIdx.x < 16 && in) a.dgate[g * a.cols + c] = a.branch_scale * (wp * s1 + bp * s2);
+        join64(s1, red);
+        join64(s2, red);
+        if (writes) a.dgate[g * a.cols + c64 + threadIdx.x] = a.branch_scale * (wp * s1[0] + bp * s2[0]);
     }
 }
 
 // ---- rows in registers ----
 
-// Where the walk over a slab's rows stands.  With parts of one group (and in
-// general where one gate holds for the slab) the rows follow each other by
-// `step`; with whole groups a walker takes every step-th group, row by row.
+// A row is held by a team of W waves, NV chunks of 8 elements per lane, and a
+// workgroup has P teams (waves of their own where W = 1 and T = 0), which take
+// the slab's rows, or with whole groups its groups, in turn.
 template <int GATE>
 struct Walk {
     int64_t r, gend;
@@ -311,13 +448,31 @@ struct Walk {
     __device__ __forceinline__ void next(const Slabs& sl, int64_t r1, int step) {
         if (!GATE) {
             r += step;
-        } else if (++r == gend) {
+        } else if (++r >= gend) {
             r += (step - 1) * sl.group;
             gend = min(r + sl.group, r1);
         }
         in = r < r1;
     }
 };
+// Sums of N values over the waves of a team, in every lane (row_sums of
+// row_norm.h for a workgroup of several teams).
+template <int MULTI, int N>
+__device__ __forceinline__ void team_sums(float (&v)[N], float* red, int W, int wave0, int& turn) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) v[n] = wave_sum(v[n]);
+    if (!MULTI) return;
+    float* r = red + turn * (N * 16);
+    turn ^= 1;
+    if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+        for (int n = 0; n < N; ++n) r[n * 16 + (threadIdx.x >> 6)] = v[n];
+    }
+    __syncthreads();
+    const int l = threadIdx.x & 15;
+#pragma unroll
+    for (int n = 0; n < N; ++n) v[n] = sum16(l < W ? r[n * 16 + wave0 + l] : 0.0f);
+}
 
 // GATE 0: the slab's rows share one row of gates, or have none; its partial
 // sums are dw, dc, S1, S2.  GATE 1, 2: whole groups with a row of gates each,
@@ -325,16 +480,23 @@ struct Walk {
 // dwp, dbp.
 template <int XB, int BB, int DB, int GATE, int T, int NV>
 __global__ __launch_bounds__(T ? T : 256) void residual_grad_kernel(
-    const ResidualNormGrad a, const Slabs sl, float* __restrict__ part) {
+    const ResidualNormGrad a, const Slabs sl, const int W, float* __restrict__ part) {
     constexpr int MULTI = T != 0;
-    __shared__ __attribute__((aligned(16))) float red[MULTI ? 4 * 16 : 4 * 512];
+    __shared__ __attribute__((aligned(16))) float red[(T ? T : 256) * (NV == 1 ? 32 : 8)];
     const int cols = (int)a.cols;
-    const Place<NV> pl = Place<NV>::template make<MULTI>(cols);
-    const int step = MULTI ? 1 : 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int P = MULTI ? (int)(blockDim.x >> 6) / W : 4, team = MULTI ? wave / W : wave;
+    const int wave0 = MULTI ? team * W : wave;
+    const Place<NV> pl = Place<NV>::of_team(cols, MULTI ? W : 1, threadIdx.x - wave0 * 64);
     int64_t r0, r1;
     sl.bounds(blockIdx.x, r0, r1);
     Walk<GATE> at;
-    at.begin(sl, r0, r1, MULTI ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x >> 6));
+    at.begin(sl, r0, r1, team);
+    // The teams meet at the row sums' barriers: all go as often as the first, the
+    // last of them perhaps without a row.
+    Walk<GATE> lead, trail;
+    lead.begin(sl, r0, r1, 0);
+    trail.begin(sl, r0, r1, P - 1);
     int turn = 0;
     const bool post = a.post != kPostNone, post_layer = a.post == 0;
     struct Row {
@@ -377,15 +539,19 @@ __global__ __launch_bounds__(T ? T : 256) void residual_grad_kernel(
         float g[8];
         const bool one = !GATE && a.gate;
         load_vec8(one ? a.gate : nullptr, a.gate_bf16,
-                  (one && sl.k ? sl.group_of(blockIdx.x) * a.ldg : 0) + pl.start(k), 1.0f, g);
+                  (one ? sl.group_of(blockIdx.x) * a.ldg : 0) + pl.start(k), 1.0f, g);
 #pragma unroll
         for (int e = 0; e < 8; ++e) u[k][e] *= a.branch_scale * g[e];
     }
-    const float n = (float)cols;
-    while (at.in) {
+    const float rn = 1.0f / (float)cols;
+    // One row of each team; `all`: every team has one.  (A store under a condition
+    // leaves the compiler not knowing how many are in flight, and it would wait
+    // for them with the next row's loads.)
+    auto one = [&](auto all) __attribute__((always_inline)) {
         const RowStats st = in.st;
         const int64_t r = at.r;
-        const bool flush = GATE && at.last_of_group();
+        const bool on = decltype(all)::value || at.in;
+        const bool flush = GATE && on && at.last_of_group();
         float xh[NV][8], d[NV][8], sx[NV][8], h[NV][8], g[GATE ? NV : 1][8];
 #pragma unroll
         for (int k = 0; k < NV; ++k)
@@ -404,7 +570,11 @@ __global__ __launch_bounds__(T ? T : 256) void residual_grad_kernel(
             in.s[k].arrived();
             in.b[k].arrived();
         }
-        at.next(sl, r1, step);
+        at.next(sl, r1, P);
+        if (MULTI) {
+            lead.next(sl, r1, P);
+            trail.next(sl, r1, P);
+        }
         fetch(at);
         float s[2] = {0.0f, 0.0f};  // of t xh, and of t
 #pragma unroll
@@ -412,29 +582,37 @@ __global__ __launch_bounds__(T ? T : 256) void residual_grad_kernel(
             float p0 = 0.0f, p1 = 0.0f;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                dw[k][e] += d[k][e] * xh[k][e];
-                dc[k][e] += d[k][e];
-                d[k][e] *= w[k][e];
-                const float t = pl.owns(k, e) ? d[k][e] : 0.0f;
-                p0 += t * xh[k][e];
-                p1 += t;
+                const float t = d[k][e];
+                if (on) {
+                    dw[k][e] += t * xh[k][e];
+                    dc[k][e] += t;
+                }
+                d[k][e] = t * w[k][e];
+                const float o = pl.owns(k, e) ? d[k][e] : 0.0f;
+                p0 += o * xh[k][e];
+                p1 += o;
             }
             s[0] += p0;
             s[1] += p1;
         }
-        row_sums<MULTI>(s, red, pl.W, turn);
-        const float mx = s[0] / n, mt = a.rms ? 0.0f : s[1] / n;
+        team_sums<MULTI>(s, red, W, wave0, turn);
+        const float mx = s[0] * rn, mt = a.rms ? 0.0f : s[1] * rn;
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            float f[8];
+        for (int k = 0; k < NV; ++k)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                d[k][e] = sx[k][e] + st.r * (d[k][e] - mt - xh[k][e] * mx);
-                s1[k][e] += d[k][e] * h[k][e];
-                s2[k][e] += d[k][e];
-                f[e] = a.x_scale * d[k][e];
+            for (int e = 0; e < 8; ++e) d[k][e] = sx[k][e] + st.r * (d[k][e] - mt - xh[k][e] * mx);
+        if (on) {
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                float f[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    s1[k][e] += d[k][e] * h[k][e];
+                    s2[k][e] += d[k][e];
+                    f[e] = a.x_scale * d[k][e];
+                }
+                store_chunk<XB>(a.dx, r * a.lddx + pl.start(k), f);
             }
-            store_chunk<XB>(a.dx, r * a.lddx + pl.start(k), f);
         }
         if (flush) {
             const int64_t at_g = (group0 + (uint32_t)(r - r0) / (uint32_t)sl.group) * a.cols;
@@ -474,50 +652,63 @@ __global__ __launch_bounds__(T ? T : 256) void residual_grad_kernel(
                 s[0] += p0;
                 s[1] += p1;
             }
-            row_sums<MULTI>(s, red, pl.W, turn);
-            mh = s[0] / n;
-            mu = post_layer ? s[1] / n : 0.0f;
+            team_sums<MULTI>(s, red, W, wave0, turn);
+            mh = s[0] * rn;
+            mu = post_layer ? s[1] * rn : 0.0f;
         }
+        if (on) {
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            float f[8];
+            for (int k = 0; k < NV; ++k) {
+                float f[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = post ? st.pr * (d[k][e] - mu - h[k][e] * mh) : d[k][e];
-            store_chunk<BB>(a.db, r * a.lddb + pl.start(k), f);
+                for (int e = 0; e < 8; ++e)
+                    f[e] = post ? st.pr * (d[k][e] - mu - h[k][e] * mh) : d[k][e];
+                store_chunk<BB>(a.db, r * a.lddb + pl.start(k), f);
+            }
         }
-    }
+    };
+    while (MULTI ? trail.in : at.in) one(std::true_type{});
+    if (MULTI)
+        while (lead.in) one(std::false_type{});
     if (!part) return;
+    float* out = part + (int64_t)blockIdx.x * 4 * cols;
+    auto sums_of = [&](int o, int k) __attribute__((always_inline)) -> float(&)[8] {
+        return o == 0 ? dw[k] : o == 1 ? dc[k] : o == 2 ? (GATE ? dpw[k] : s1[k]) : (GATE ? dpc[k] : s2[k]);
+    };
+    if (P == 1) {
+#pragma unroll
+        for (int o = 0; o < 4; ++o)
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+                store_own<0>(out + o * cols, pl.start(k), sums_of(o, k), k < NV - 1 ? 0 : pl.skip);
+        return;
+    }
+    if (NV != 1) return;  // such rows have one team
+    // the teams' sums of the same columns, added up through LDS
+    const int span = pl.W * 512;  // columns that a team's lanes hold
+    __syncthreads();
 #pragma unroll
     for (int o = 0; o < 4; ++o) {
-        float* out = part + ((int64_t)blockIdx.x * 4 + o) * cols;
+        float(&v)[8] = sums_of(o, 0);
+        float* mine = red + (o * P + team) * span;
+        if (pl.skip == 0) {
+            *(u32x4*)(mine + pl.t) = (u32x4){as_u32(v[0]), as_u32(v[1]), as_u32(v[2]), as_u32(v[3])};
+            *(u32x4*)(mine + pl.t + 4) =
+                (u32x4){as_u32(v[4]), as_u32(v[5]), as_u32(v[6]), as_u32(v[7])};
+        } else {
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            float(&v)[8] = o == 0 ? dw[k] : o == 1 ? dc[k] : o == 2 ? (GATE ? dpw[k] : s1[k]) : (GATE ? dpc[k] : s2[k]);
-            const int skip = k < NV - 1 ? 0 : pl.skip, c = pl.start(k);
-            if (MULTI) {
-                store_own<0>(out, c, v, skip);
-                continue;
-            }
-            // the four waves hold the same 512 columns of different rows
-            __syncthreads();
-            float* mine = red + (threadIdx.x >> 6) * 512;
-            if (skip == 0) {
-                *(u32x4*)(mine + pl.t) =
-                    (u32x4){as_u32(v[0]), as_u32(v[1]), as_u32(v[2]), as_u32(v[3])};
-                *(u32x4*)(mine + pl.t + 4) =
-                    (u32x4){as_u32(v[4]), as_u32(v[5]), as_u32(v[6]), as_u32(v[7])};
-            } else {
+            for (int e = 1; e < 8; ++e)
+                if (e >= pl.skip) mine[pl.tail + e] = v[e];
+        }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < cols; i += blockDim.x) {
 #pragma unroll
-                for (int e = 1; e < 8; ++e)
-                    if (e >= skip) mine[c - k * 512 + e] = v[e];
-            }
-            __syncthreads();
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int i = h * 256 + threadIdx.x;
-                if (k * 512 + i < cols)
-                    out[k * 512 + i] = (red[i] + red[512 + i]) + (red[1024 + i] + red[1536 + i]);
-            }
+        for (int o = 0; o < 4; ++o) {
+            const float* q = red + o * P * span + i;
+            float sum = q[0];
+            for (int t = 1; t < P; ++t) sum += q[t * span];
+            out[o * cols + i] = sum;
         }
     }
 }
@@ -530,27 +721,30 @@ static bool any_sums(const ResidualNormGrad& a) {
     return a.dweight || a.dbias || a.dpost_weight || a.dpost_bias || a.dgate;
 }
 
-// How rows are held: by waves of their own (T = 0) or by a workgroup of at most
-// T threads, nv chunks per lane; nv = 0: the rows' means first, then tiles.
+// How rows are held: by waves of their own (T = 0) or by teams of W waves in a
+// workgroup of at most T threads, nv chunks per lane; nv = 0: the rows' means
+// first, then tiles.  whole: slabs of whole groups of a gate's rows.
 struct GradShape {
-    int T, nv, threads;
-    bool whole;  // slabs of whole groups of a gate's rows
+    int T, nv, W, threads;
 };
 static GradShape grad_shape(int64_t cols, bool whole) {
     const int waves = (int)((cols + 511) / 512);
-    if (cols < 8 || cols > 8192 || (whole && cols > 6144)) return {0, 0, 256, whole};
-    if (cols <= 512) return {0, 1, 256, whole};
-    if (cols <= 6144) return {waves <= 8 ? 512 : 768, 1, 64 * waves, whole};
-    return {512, 2, 64 * ((waves + 1) / 2), whole};
+    if (cols < 8 || cols > 8192 || (whole && cols > 6144)) return {0, 0, 0, 256};
+    if (cols <= 512) return {0, 1, 1, 256};
+    if (cols > 6144) return {512, 2, (waves + 1) / 2, 64 * ((waves + 1) / 2)};
+    const int T = whole && waves <= 8 ? 512 : 768;
+    return {T, 1, waves, 64 * waves * (T / 64 / waves)};
 }
 // As many slabs as 256 compute units hold workgroups of (12 waves to a unit, 8
-// where a row of gates comes with every row), of 8 rows and more to a walker.
+// where a row of gates comes with every row), of FP4Q_MIN rows and more.
+#ifndef FP4Q_MIN
+#define FP4Q_MIN 8
+#endif
 static Slabs grad_slabs(int64_t rows, int64_t cols, int64_t gate_rows) {
     const auto slabs = [&](bool whole) {
         const GradShape sh = grad_shape(cols, whole);
-        const int64_t per = sh.nv == 0 ? 16 : sh.T ? 8 : 16;
         const int64_t most = sh.nv == 0 ? 256 : 256 * std::max(1, (whole ? 8 : 12) * 64 / sh.threads);
-        return make_slabs(rows, gate_rows, std::min<int64_t>(most, (rows + per - 1) / per));
+        return make_slabs(rows, gate_rows, most, sh.nv && sh.T ? FP4Q_MIN : 16);
     };
     const Slabs sl = slabs(false);
     return gate_rows < rows && !sl.k ? slabs(true) : sl;
@@ -569,22 +763,31 @@ static void go_rows(const GradShape sh, const ResidualNormGrad& a, const Slabs& 
 #define FP4Q_GO(T_, NV_)                                                                        \
     if (sh.T == T_ && sh.nv == NV_)                                                             \
     FP4Q_LAUNCH((residual_grad_kernel<XB, BB, DB, GATE, T_, NV_>), dim3((unsigned)sl.count),    \
-                dim3((unsigned)sh.threads), 0, s, a, sl, part)
+                dim3((unsigned)sh.threads), 0, s, a, sl, sh.W, part)
     FP4Q_GO(0, 1);
-    FP4Q_GO(512, 1);
     FP4Q_GO(768, 1);
-    if constexpr (GATE == 0) FP4Q_GO(512, 2);
+    if constexpr (GATE == 0) {
+        FP4Q_GO(512, 2);
+    } else {
+        FP4Q_GO(512, 1);
+    }
 #undef FP4Q_GO
 }
 template <int XB, int BB, int DB>
 static void go_gate(const GradShape sh, const ResidualNormGrad& a, const Slabs& sl, RowMeans* means,
                     float* part, hipStream_t s) {
     if (sh.nv == 0) {
+        if (a.cols >= 8 && a.cols <= 16384)
+            FP4Q_LAUNCH((residual_grad_means_kernel<XB, BB, DB>), dim3((unsigned)std::min<int64_t>(a.rows, 1024)),
+                        dim3(64 * (unsigned)((a.cols + 1023) / 1024)), 0, s, a, means);
+        else
+            FP4Q_LAUNCH(residual_grad_rows_kernel, dim3((unsigned)std::min(a.rows, kAnyGrid)), dim3(256), 0,
+                        s, a, means);
         const int64_t tiles = (a.cols + 2047) / 2048;
         FP4Q_LAUNCH((residual_grad_tile_kernel<XB, BB, DB>),
                     dim3((unsigned)tiles, (unsigned)std::min(sl.count, kGridY)), dim3(256), 0, s, a,
                     means, sl, part);
-    } else if (!sh.whole) {
+    } else if (sl.k) {
         go_rows<XB, BB, DB, 0>(sh, a, sl, part, s);
     } else if (!a.gate_bf16) {
         go_rows<XB, BB, DB, 1>(sh, a, sl, part, s);
@@ -605,17 +808,16 @@ hipError_t launch_residual_norm_grad(const ResidualNormGrad& a, void* ws, hipStr
     const bool sums = any_sums(a);
     RowMeans* means = (RowMeans*)ws;
     float* part = sh.nv == 0 ? (float*)(means + a.rows) : (float*)ws;
-    if (sh.nv == 0)
-        FP4Q_LAUNCH(residual_grad_rows_kernel, dim3((unsigned)std::min(a.rows, kAnyGrid)), dim3(256), 0,
-                    s, a, means);
     float* p = sums ? part : nullptr;
     if (a.x_bf16)
         a.b_bf16 ? go_dy<1, 1>(sh, a, sl, means, p, s) : go_dy<1, 0>(sh, a, sl, means, p, s);
     else
         a.b_bf16 ? go_dy<0, 1>(sh, a, sl, means, p, s) : go_dy<0, 0>(sh, a, sl, means, p, s);
     if (sums) {
-        const int64_t gates = a.dgate && sl.k ? std::min(sl.count / sl.k, kGridY) : 0;
-        const int64_t groups = (a.cols + 15) / 16;
+        int64_t gates = a.dgate && sl.k ? sl.count / sl.k : 0;
+        if (sl.k <= kFewParts) gates = (gates + 63) / 64;
+        gates = std::min(gates, kGridY);
+        const int64_t groups = (a.cols + 63) / 64;
         for (int64_t g = 0; g < groups; g += kJoinGroups)
             FP4Q_LAUNCH(residual_grad_join_kernel,
                         dim3((unsigned)std::min(groups - g, kJoinGroups), (unsigned)(4 + gates)),

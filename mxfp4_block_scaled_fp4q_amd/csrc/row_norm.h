@@ -157,9 +157,14 @@ struct Place {
     int W, t, step, tail, skip;
     template <int MULTI>
     __device__ __forceinline__ static Place make(int cols) {
+        return of_team(cols, MULTI ? (int)(blockDim.x >> 6) : 1,
+                       MULTI ? (int)threadIdx.x : (int)(threadIdx.x & 63));
+    }
+    // The same for `waves` waves, this lane the `lane`-th of theirs.
+    __device__ __forceinline__ static Place of_team(int cols, int waves, int lane) {
         Place p;
-        p.W = MULTI ? (int)(blockDim.x >> 6) : 1;
-        p.t = (MULTI ? (int)threadIdx.x : (int)(threadIdx.x & 63)) * 8;
+        p.W = waves;
+        p.t = lane * 8;
         p.step = p.W * 512;
         const int c0 = (NV - 1) * p.step + p.t;
         p.tail = min(c0, cols - 8);
