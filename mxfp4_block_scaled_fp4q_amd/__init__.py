@@ -852,22 +852,42 @@ def layer_norm_grad(dy, x, weight, mean, rstd, kind=LAYER_NORM, dx=None, want_we
     return dx, dweight, dbias
 
 
-def _on_device(first, stream, *others):
-    """Raises unless the tensors lie on one device, the current one or the
-    stream's: a kernel on another device's stream would read them over there."""
-    d = first.get_device()
+def _device_of(t, stream):
+    """t's device, which has to be the current one, or the stream's: a kernel of
+    another device's stream would read t over there."""
+    d = t.get_device()
     if d != ((_torch_module or _torch())._C._cuda_getDevice() if stream is None else stream.device_index):
         raise ValueError("the tensors must lie on the current device (or the stream's)")
-    for t in others:
-        if t is not None and t.get_device() != d:
-            raise ValueError("the tensors must lie on one device")
+    return d
 
 
-def _gate(gate, gate_rows, rows, cols):
+def _same_device(t, name, d):
+    if t.get_device() != d:
+        _need_cuda(t)
+        raise ValueError(f"{name} must lie on one device with the others")
+
+
+def _rows_on(t, name, d, size, dtype=None):
+    """_rows of a tensor of that size on device d."""
+    if (t.shape == size and t.get_device() == d and t.is_contiguous()
+            and (dtype is None or t.dtype is dtype)):
+        return size[1]
+    _need_cuda(t)
+    _same_device(t, name, d)
+    return _rows(t, name, dtype, size)
+
+
+def _vec_on(t, name, d, size, dtype):
+    """_vec of a vector of that size on device d."""
+    if t.shape != size or t.get_device() != d or t.dtype is not dtype or not t.is_contiguous():
+        _need_cuda(t)
+        _same_device(t, name, d)
+        _vec(t, name, dtype, size[0])
+
+
+def _gate(gate, gate_rows, rows, cols, d):
     """Dtype code, rows per row of the gate and row stride of a gate [cols] or
     [groups, cols]."""
-    if gate is None:
-        return F32, rows, cols
     size = gate.shape
     if len(size) == 1:
         _vec(gate, "gate", None, cols)
@@ -877,6 +897,7 @@ def _gate(gate, gate_rows, rows, cols):
         groups = size[0]
         if size[1] != cols or groups == 0:
             raise ValueError(f"gate must have {cols} columns and a row, got {tuple(size)}")
+    _same_device(gate, "gate", d)
     if gate_rows is None:
         if groups == 1:
             gate_rows = rows
@@ -889,19 +910,21 @@ def _gate(gate, gate_rows, rows, cols):
     return _dt(gate), gate_rows, ld
 
 
-def _norm_vectors(cols, **vectors):
+def _norm_vectors(cols, d, weight, bias, post_weight, post_bias):
     """Dtype code of the vectors of both norms."""
-    dt = None
-    for name, t in vectors.items():
+    dtype, size = None, (cols,)
+    for t, name in ((weight, "weight"), (bias, "bias"), (post_weight, "post_weight"),
+                    (post_bias, "post_bias")):
         if t is None:
             continue
-        _vec(t, name, None, cols)
-        if dt is None:
-            dt = t.dtype
+        if dtype is None:
+            dtype = t.dtype
             code = _dt(t)
-        elif t.dtype is not dt:
+        elif t.dtype is not dtype:
             raise TypeError("the norms' weights and biases must have the same dtype")
-    return F32 if dt is None else code
+        if t.shape != size or t.get_device() != d or not t.is_contiguous():
+            _vec_on(t, name, d, size, dtype)
+    return F32 if dtype is None else code
 
 
 def residual_norm(x, branch, weight=None, bias=None, eps=1e-5, kind=LAYER_NORM, post_kind=NO_NORM,
@@ -917,21 +940,25 @@ def residual_norm(x, branch, weight=None, bias=None, eps=1e-5, kind=LAYER_NORM, 
     (codes, scales) of quantize(y, 32); stats = (post_mean, post_rstd, mean,
     rstd), fp32 per row, for residual_norm_grad (None where the norm has none,
     or without stats)."""
-    torch = _torch()
-    f32 = torch.float32
+    torch = _torch_module or _torch()
     ldx = _rows(x, "x")
-    R, C = x.shape
-    ldb = _rows(branch, "branch", shape=(R, C))
+    R, C = size = x.shape
+    d = _device_of(x, stream)
+    ldb = _rows_on(branch, "branch", d, size)
     xdt = _dt(x)
-    wdt = _norm_vectors(C, weight=weight, bias=bias, post_weight=post_weight, post_bias=post_bias)
-    gdt, gate_rows, ldg = _gate(gate, gate_rows, R, C)
-    _on_device(x, stream, branch, weight, bias, post_weight, post_bias, gate, x_out, y)
-    empty = _allocator(x, stream)
-    if x_out is None:
-        x_out, ldxo = empty((R, C), (C, 1), x.dtype), C
+    wdt = _norm_vectors(C, d, weight, bias, post_weight, post_bias)
+    if gate is None:
+        gate_at, gdt, gate_rows, ldg = None, F32, R, C
     else:
-        ldxo = _rows(x_out, "x_out", x.dtype, (R, C))
-    codes = scales = None
+        gdt, gate_rows, ldg = _gate(gate, gate_rows, R, C, d)
+        gate_at = gate.data_ptr()
+    empty = _allocator(x, stream)
+    dense = (C, 1)
+    if x_out is None:
+        x_out, ldxo = empty((R, C), dense, x.dtype), C
+    else:
+        ldxo = _rows_on(x_out, "x_out", d, size, x.dtype)
+    codes = scales = codes_at = scales_at = y_at = None
     ydt, ldy = xdt, C
     if quantize:
         if y is not None or out_dtype is not None:
@@ -940,26 +967,34 @@ def residual_norm(x, branch, weight=None, bias=None, eps=1e-5, kind=LAYER_NORM, 
             raise ValueError(f"codes need a multiple of 32 columns, got {C}")
         codes = empty((R, C // 2), (C // 2, 1), torch.uint8)
         scales = empty((R, C // 32), (C // 32, 1), torch.uint8)
-    elif y is None:
-        y = empty((R, C), (C, 1), x.dtype if out_dtype is None else out_dtype)
-        if out_dtype is not None:
-            ydt = _dt(y)
+        codes_at, scales_at = codes.data_ptr(), scales.data_ptr()
     else:
-        ldy, ydt = _rows(y, "y", shape=(R, C)), _dt(y)
-    pm = pr = m = r = None
+        if y is None:
+            y = empty((R, C), dense, x.dtype if out_dtype is None else out_dtype)
+            if out_dtype is not None:
+                ydt = _dt(y)
+        else:
+            ldy, ydt = _rows_on(y, "y", d, size), _dt(y)
+        y_at = y.data_ptr()
+    pm = pr = m = r = pm_at = pr_at = m_at = r_at = None
     if stats:
-        if post_kind == LAYER_NORM:
-            pm = empty((R,), (1,), f32)
+        f32, rows, one = torch.float32, (R,), (1,)
         if post_kind != NO_NORM:
-            pr = empty((R,), (1,), f32)
+            pr = empty(rows, one, f32)
+            pr_at = pr.data_ptr()
+            if post_kind == LAYER_NORM:
+                pm = empty(rows, one, f32)
+                pm_at = pm.data_ptr()
         if kind == LAYER_NORM:
-            m = empty((R,), (1,), f32)
-        r = empty((R,), (1,), f32)
-    status = lib().fp4q_residual_norm(
+            m = empty(rows, one, f32)
+            m_at = m.data_ptr()
+        r = empty(rows, one, f32)
+        r_at = r.data_ptr()
+    status = (_lib or lib()).fp4q_residual_norm(
         R, C, x.data_ptr(), xdt, ldx, branch.data_ptr(), _dt(branch), ldb, post_kind, _ptr(post_weight),
-        _ptr(post_bias), _ptr(gate), gdt, gate_rows, ldg, x_scale, branch_scale, kind, _ptr(weight),
-        _ptr(bias), wdt, eps, x_out.data_ptr(), ldxo, _ptr(y), ydt, ldy, _ptr(codes), _ptr(scales),
-        _ptr(pm), _ptr(pr), _ptr(m), _ptr(r), _stream(stream))
+        _ptr(post_bias), gate_at, gdt, gate_rows, ldg, x_scale, branch_scale, kind, _ptr(weight),
+        _ptr(bias), wdt, eps, x_out.data_ptr(), ldxo, y_at, ydt, ldy, codes_at, scales_at, pm_at, pr_at,
+        m_at, r_at, _stream(stream))
     if status:
         _check(status)
     return x_out, (codes, scales) if quantize else y, (pm, pr, m, r)
@@ -983,69 +1018,87 @@ def residual_norm_grad(dy, dx_out, x_out, branch, stats, weight=None, kind=LAYER
     The gradients of post_weight, post_bias and gate are wanted where these are
     given.  branch may be None without post_kind where the gate's gradient is not
     wanted (dbranch then has x_out's dtype)."""
-    f32 = _torch().float32
+    torch = _torch_module or _torch()
+    f32 = torch.float32
     ldxo = _rows(x_out, "x_out")
-    R, C = x_out.shape
-    xdt = _dt(x_out)
-    lddy = _rows(dy, "dy", shape=(R, C))
-    lddxo = C if dx_out is None else _rows(dx_out, "dx_out", x_out.dtype, (R, C))
-    ldb = C if branch is None else _rows(branch, "branch", shape=(R, C))
-    bdtype = branch.dtype if branch is not None else x_out.dtype if dbranch is None else dbranch.dtype
-    wdt = _norm_vectors(C, weight=weight, post_weight=post_weight, post_bias=post_bias)
-    gdt, rows_each, ldg = _gate(gate, gate_rows, R, C)
+    R, C = size = x_out.shape
+    d = _device_of(x_out, stream)
+    xdtype = x_out.dtype
+    lddy = _rows_on(dy, "dy", d, size)
+    dxo_at, lddxo, branch_at, ldb = None, C, None, C
+    if dx_out is not None:
+        lddxo = _rows_on(dx_out, "dx_out", d, size, xdtype)
+        dxo_at = dx_out.data_ptr()
+    if branch is not None:
+        ldb = _rows_on(branch, "branch", d, size)
+        branch_at, bdtype = branch.data_ptr(), branch.dtype
+    else:
+        bdtype = xdtype if dbranch is None else dbranch.dtype
+    wdt = _norm_vectors(C, d, weight, None, post_weight, post_bias)
+    if gate is None:
+        gate_at, gdt, gate_rows, ldg, rows_each = None, F32, R, C, 0
+    else:
+        gdt, gate_rows, ldg = _gate(gate, gate_rows, R, C, d)
+        gate_at, rows_each = gate.data_ptr(), gate_rows
     pm, pr, m, r = stats
+    rows = (R,)
     for t, name in ((pm, "post_mean"), (pr, "post_rstd"), (m, "mean"), (r, "rstd")):
         if t is not None:
-            _vec(t, name, f32, R)
-    _on_device(x_out, stream, dy, dx_out, branch, weight, post_weight, post_bias, gate, pm, pr, m, r, dx,
-               dbranch, dweight, dbias, dpost_weight, dpost_bias, dgate, workspace)
+            _vec_on(t, name, d, rows, f32)
     empty = _allocator(x_out, stream)
     if dx is None:
-        dx, lddx = empty((R, C), (C, 1), x_out.dtype), C
+        dx, lddx = empty((R, C), (C, 1), xdtype), C
     else:
-        lddx = _rows(dx, "dx", x_out.dtype, (R, C))
+        lddx = _rows_on(dx, "dx", d, size, xdtype)
     if dbranch is None:
         dbranch, lddb = empty((R, C), (C, 1), bdtype), C
     else:
-        lddb = _rows(dbranch, "dbranch", bdtype, (R, C))
-    out = []
-    for t, name, want in ((dweight, "dweight", want_weight), (dbias, "dbias", want_bias),
-                          (dpost_weight, "dpost_weight",
-                           post_weight is not None if want_post_weight is None else want_post_weight),
-                          (dpost_bias, "dpost_bias",
-                           post_bias is not None if want_post_bias is None else want_post_bias)):
-        if t is not None:
-            _vec(t, name, f32, C)
-        elif want:
-            t = empty((C,), (1,), f32)
-        out.append(t)
+        lddb = _rows_on(dbranch, "dbranch", d, size, bdtype)
+    cols, one = (C,), (1,)
+    if dweight is not None:
+        _vec_on(dweight, "dweight", d, cols, f32)
+    elif want_weight:
+        dweight = empty(cols, one, f32)
+    if dbias is not None:
+        _vec_on(dbias, "dbias", d, cols, f32)
+    elif want_bias:
+        dbias = empty(cols, one, f32)
+    if dpost_weight is not None:
+        _vec_on(dpost_weight, "dpost_weight", d, cols, f32)
+    elif post_weight is not None if want_post_weight is None else want_post_weight:
+        dpost_weight = empty(cols, one, f32)
+    if dpost_bias is not None:
+        _vec_on(dpost_bias, "dpost_bias", d, cols, f32)
+    elif post_bias is not None if want_post_bias is None else want_post_bias:
+        dpost_bias = empty(cols, one, f32)
     if dgate is not None:
         if gate is None:
             raise ValueError("dgate without a gate")
         _need_cuda(dgate)
         _need(dgate, "dgate", f32, gate.shape)
+        _same_device(dgate, "dgate", d)
     elif gate is not None if want_gate is None else want_gate:
         if gate is None:
             raise ValueError("want_gate without a gate")
-        size = gate.shape
-        dgate = empty(tuple(size), (C, 1) if len(size) == 2 else (1,), f32)
+        dgate = empty(tuple(gate.shape), (C, 1) if gate.dim() == 2 else one, f32)
+    L = _lib or lib()
     if workspace is None:
-        nbytes = lib().fp4q_residual_norm_grad_workspace_bytes(R, C, rows_each)
-        workspace = empty((nbytes,), (1,), _torch().uint8)
+        nbytes = L.fp4q_residual_norm_grad_workspace_bytes(R, C, rows_each)
+        workspace = empty((nbytes,), one, torch.uint8)
     else:
         _need_cuda(workspace)
         _need(workspace, "workspace", workspace.dtype)
+        _same_device(workspace, "workspace", d)
         nbytes = workspace.numel() * workspace.element_size()
-    dw, dc, dpw, dpc = out
-    status = lib().fp4q_residual_norm_grad(
-        R, C, dy.data_ptr(), _dt(dy), lddy, _ptr(dx_out), lddxo, x_out.data_ptr(), xdt, ldxo, _ptr(branch),
-        _dt(dbranch), ldb, post_kind, _ptr(post_weight), _ptr(post_bias), _ptr(gate), gdt, rows_each, ldg,
+    status = L.fp4q_residual_norm_grad(
+        R, C, dy.data_ptr(), _dt(dy), lddy, dxo_at, lddxo, x_out.data_ptr(), _dt(x_out), ldxo, branch_at,
+        _dt(dbranch), ldb, post_kind, _ptr(post_weight), _ptr(post_bias), gate_at, gdt, gate_rows, ldg,
         x_scale, branch_scale, kind, _ptr(weight), wdt, _ptr(pm), _ptr(pr), _ptr(m), _ptr(r), dx.data_ptr(),
-        lddx, dbranch.data_ptr(), lddb, _ptr(dpw), _ptr(dpc), _ptr(dgate), _ptr(dw), _ptr(dc),
-        workspace.data_ptr(), nbytes, _stream(stream))
+        lddx, dbranch.data_ptr(), lddb, _ptr(dpost_weight), _ptr(dpost_bias), _ptr(dgate), _ptr(dweight),
+        _ptr(dbias), workspace.data_ptr(), nbytes, _stream(stream))
     if status:
         _check(status)
-    return dx, dbranch, dw, dc, dpw, dpc, dgate
+    return dx, dbranch, dweight, dbias, dpost_weight, dpost_bias, dgate
 
 
 class GradPlan:
@@ -1099,7 +1152,7 @@ def grad_norm(plan, max_norm=None, eps=1e-6, order=NORM_L2, norm=None, scale=Non
     replay: the plan is kept as long as the graph."""
     f32 = _torch().float32
     plan = _grads_of(plan)
-    _on_device(plan.like, stream, norm, scale, workspace)
+    d = _device_of(plan.like, stream)
     empty = _allocator(plan.like, stream)
     for t, name in ((norm, "norm"), (scale, "scale")):
         if t is not None:
@@ -1107,6 +1160,7 @@ def grad_norm(plan, max_norm=None, eps=1e-6, order=NORM_L2, norm=None, scale=Non
             _need(t, name, f32)
             if t.numel() != 1:
                 raise ValueError(f"{name} must have one element, got {t.numel()}")
+            _same_device(t, name, d)
     if norm is None:
         norm = empty((), (), f32)
     if max_norm is None:
@@ -1120,8 +1174,9 @@ def grad_norm(plan, max_norm=None, eps=1e-6, order=NORM_L2, norm=None, scale=Non
     else:
         _need_cuda(workspace)
         _need(workspace, "workspace", workspace.dtype)
+        _same_device(workspace, "workspace", d)
         nbytes = workspace.numel() * workspace.element_size()
-    status = lib().fp4q_grad_norm(plan.array, plan.n, order, 0.0 if max_norm is None else max_norm, eps,
+    status = (_lib or lib()).fp4q_grad_norm(plan.array, plan.n, order, 0.0 if max_norm is None else max_norm, eps,
                                   norm.data_ptr(), _ptr(scale), workspace.data_ptr(), nbytes,
                                   _stream(stream))
     if status:
@@ -1137,8 +1192,8 @@ def scale_grads(plan, scale, stream=None):
     _need(scale, "scale", _torch().float32)
     if scale.numel() != 1:
         raise ValueError(f"scale must have one element, got {scale.numel()}")
-    _on_device(plan.like, stream, scale)
-    status = lib().fp4q_grad_scale(plan.array, plan.n, scale.data_ptr(), _stream(stream))
+    _same_device(scale, "scale", _device_of(plan.like, stream))
+    status = (_lib or lib()).fp4q_grad_scale(plan.array, plan.n, scale.data_ptr(), _stream(stream))
     if status:
         _check(status)
 

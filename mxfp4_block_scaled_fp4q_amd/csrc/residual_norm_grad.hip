@@ -319,114 +319,82 @@ __global__ __launch_bounds__(256) void residual_grad_tile_kernel(const ResidualN
         tile<XB, BB, DB, 0>(a, means, sl, part, c, (int)(a.cols - c));
 }
 
-// Adds up the rows of partial sums: 64 columns per workgroup, 4 to a lane, 64
-// groups of 16 lanes over the slabs, so that few loads follow each other.
-// blockIdx.y: dw, dc, dwp, dbp, then the gate's groups, gridDim.y - 4 apart.
-constexpr int64_t kJoinGroups = 1 << 21;
+// Adds up the rows of partial sums: 64 columns per workgroup, one to a lane, 16
+// waves over the slabs.  blockIdx.y: dw, dc, dwp, dbp, then the gate's groups:
+// one at a time, gridDim.y - 4 apart, or 16 at a time where a wave adds up the
+// few parts of one (kFewParts).
+constexpr int64_t kJoinGroups = 1 << 22;
 constexpr int kFewParts = 16;
-__device__ __forceinline__ void join64(float (&v)[4], float (*red)[64]) {
-    const int l = threadIdx.x & 15, wave = threadIdx.x >> 6;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = rows_sum(v[e]);
-    __syncthreads();
-    if ((threadIdx.x & 63) < 16) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) red[wave][4 * l + e] = v[e];
-    }
-    __syncthreads();
-    // thread t < 64: column t
+// factor(i): of slab i's row
+template <class F>
+__device__ __forceinline__ float slab_sum(const float* p, int64_t stride, int first, int step,
+                                          int64_t count, F factor) {
     float s = 0.0f;
-    if (threadIdx.x < 64) {
-#pragma unroll
-        for (int i = 0; i < 16; i += 4)
-            s += (red[i][threadIdx.x] + red[i + 1][threadIdx.x]) +
-                 (red[i + 2][threadIdx.x] + red[i + 3][threadIdx.x]);
-    }
-    v[0] = s;
+#pragma unroll 8
+    for (int64_t i = first; i < count; i += step) s += p[i * stride] * factor(i);
+    return s;
+}
+__device__ __forceinline__ float slab_sum(const float* p, int64_t stride, int first, int step,
+                                          int64_t count) {
+    float s = 0.0f;
+#pragma unroll 8
+    for (int64_t i = first; i < count; i += step) s += p[i * stride];
+    return s;
 }
 __global__ __launch_bounds__(1024) void residual_grad_join_kernel(const ResidualNormGrad a,
                                                                   const float* __restrict__ part,
                                                                   const Slabs sl, int64_t group0) {
-    __shared__ float red[16][64];
-    const int64_t c64 = (group0 + blockIdx.x) * 64, c = c64 + (threadIdx.x & 15) * 4;
-    const int left = (int)max<int64_t>(0, min<int64_t>(a.cols - c, 4));
-    const int first = threadIdx.x >> 4;
-    auto row = [&](int64_t i, int y, float (&v)[4]) __attribute__((always_inline)) {
-        const float* p = part + (i * 4 + y) * a.cols + c;
-        if (left == 4) {
-            const u32x4 w = *(const u32x4_a4*)p;
+    __shared__ float red[2][16][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t at = (group0 + blockIdx.x) * 64 + lane, c = min(at, a.cols - 1);
+    const int64_t stride = 4 * a.cols;
+    const float* p = part + c;
+    // of all waves, in the first
+    auto all16 = [&](float v, int n) __attribute__((always_inline)) {
+        red[n][wave][lane] = v;
+        __syncthreads();
+        float s = 0.0f;
+        if (wave == 0) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = as_f32(w[e]);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = e < left ? p[e] : 0.0f;
+            for (int i = 0; i < 16; ++i) s += red[n][i][lane];
         }
+        return s;
     };
-    const bool writes = threadIdx.x < 64 && c64 + threadIdx.x < a.cols;
     if (blockIdx.y < 4) {
         const int y = blockIdx.y;
         float* out = y == 0 ? a.dweight : y == 1 ? a.dbias : y == 2 ? a.dpost_weight : a.dpost_bias;
         if (!out) return;
-        const bool scaled = y >= 2 && sl.k;
-        float s[4] = {};
-#pragma unroll 4
-        for (int64_t i = first; i < sl.count; i += 64) {
-            float v[4];
-            row(i, y, v);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if (scaled) {
-                    v[e] *= a.branch_scale;
-                    if (a.gate && e < left) v[e] *= load_as(a.gate, a.gate_bf16, sl.group_of(i) * a.ldg + c + e);
-                }
-                s[e] += v[e];
-            }
-        }
-        join64(s, red);
-        if (writes) out[c64 + threadIdx.x] = s[0];
+        p += y * a.cols;
+        const bool gates = y >= 2 && sl.k && a.gate;
+        float s;
+        if (!gates)
+            s = slab_sum(p, stride, wave, 16, sl.count);
+        else if (a.gate_bf16)
+            s = slab_sum(p, stride, wave, 16, sl.count,
+                         [&](int64_t i) { return load1<1>(a.gate, sl.group_of(i) * a.ldg + c); });
+        else
+            s = slab_sum(p, stride, wave, 16, sl.count,
+                         [&](int64_t i) { return load1<0>(a.gate, sl.group_of(i) * a.ldg + c); });
+        s = all16(s, 0);
+        if (y >= 2 && sl.k) s *= a.branch_scale;
+        if (wave == 0 && at < a.cols) out[c] = s;
         return;
     }
+    const float wp = a.branch_scale * vec1(a.post_weight, a.w_bf16, c, 1.0f);
+    const float bp = a.branch_scale * vec1(a.post_bias, a.w_bf16, c, 0.0f);
     const int64_t groups = sl.count / sl.k;
-    if (sl.k <= kFewParts) {  // 16 lanes to a group of gates
-        for (int64_t g = (blockIdx.y - 4) * 64 + first; g < groups; g += (gridDim.y - 4) * 64) {
-            float s1[4] = {}, s2[4] = {};
-            for (int64_t i = 0; i < sl.k; ++i) {
-                float v1[4], v2[4];
-                row(g * sl.k + i, 2, v1);
-                row(g * sl.k + i, 3, v2);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    s1[e] += v1[e];
-                    s2[e] += v2[e];
-                }
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (e < left)
-                    a.dgate[g * a.cols + c + e] =
-                        a.branch_scale * (vec1(a.post_weight, a.w_bf16, c + e, 1.0f) * s1[e] +
-                                          vec1(a.post_bias, a.w_bf16, c + e, 0.0f) * s2[e]);
+    const bool few = sl.k <= kFewParts;
+    const int64_t step = (gridDim.y - 4) * (few ? 16 : 1);
+    for (int64_t g = (blockIdx.y - 4) * (few ? 16 : 1) + (few ? wave : 0); g < groups; g += step) {
+        const float* q = p + (g * sl.k * 4 + 2) * a.cols;
+        float s1 = slab_sum(q, stride, few ? 0 : wave, few ? 1 : 16, sl.k);
+        float s2 = slab_sum(q + a.cols, stride, few ? 0 : wave, few ? 1 : 16, sl.k);
+        if (!few) {
+            __syncthreads();
+            s1 = all16(s1, 0);
+            s2 = all16(s2, 1);
         }
-        return;
-    }
-    const float wp = writes ? vec1(a.post_weight, a.w_bf16, c64 + threadIdx.x, 1.0f) : 0.0f;
-    const float bp = writes ? vec1(a.post_bias, a.w_bf16, c64 + threadIdx.x, 0.0f) : 0.0f;
-    for (int64_t g = blockIdx.y - 4; g < groups; g += gridDim.y - 4) {
-        float s1[4] = {}, s2[4] = {};
-#pragma unroll 4
-        for (int64_t i = first; i < sl.k; i += 64) {
-            float v1[4], v2[4];
-            row(g * sl.k + i, 2, v1);
-            row(g * sl.k + i, 3, v2);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                s1[e] += v1[e];
-                s2[e] += v2[e];
-            }
-        }
-        join64(s1, red);
-        join64(s2, red);
-        if (writes) a.dgate[g * a.cols + c64 + threadIdx.x] = a.branch_scale * (wp * s1[0] + bp * s2[0]);
+        if ((few || wave == 0) && at < a.cols) a.dgate[g * a.cols + c] = wp * s1 + bp * s2;
     }
 }
 
@@ -474,15 +442,19 @@ __device__ __forceinline__ void team_sums(float (&v)[N], float* red, int W, int 
     for (int n = 0; n < N; ++n) v[n] = sum16(l < W ? r[n * 16 + wave0 + l] : 0.0f);
 }
 
+// Operands that are not there: a row of zeros, read with a row stride of 0.
+__device__ const float zeros[8192] = {};
+
 // GATE 0: the slab's rows share one row of gates, or have none; its partial
 // sums are dw, dc, S1, S2.  GATE 1, 2: whole groups with a row of gates each,
 // fp32 or bf16; dg is written group by group, and the partial sums are dw, dc,
-// dwp, dbp.
+// dwp, dbp (part is null where none are wanted).
 template <int XB, int BB, int DB, int GATE, int T, int NV>
 __global__ __launch_bounds__(T ? T : 256) void residual_grad_kernel(
     const ResidualNormGrad a, const Slabs sl, const int W, float* __restrict__ part) {
     constexpr int MULTI = T != 0;
-    __shared__ __attribute__((aligned(16))) float red[(T ? T : 256) * (NV == 1 ? 32 : 8)];
+    __shared__ __attribute__((aligned(16))) float red[4 * 16];
+    __shared__ u32x4 sums[NV == 1 ? 8 * (T ? T : 256) : 1];
     const int cols = (int)a.cols;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int P = MULTI ? (int)(blockDim.x >> 6) / W : 4, team = MULTI ? wave / W : wave;
@@ -490,11 +462,10 @@ __global__ __launch_bounds__(T ? T : 256) void residual_grad_kernel(
     const Place<NV> pl = Place<NV>::of_team(cols, MULTI ? W : 1, threadIdx.x - wave0 * 64);
     int64_t r0, r1;
     sl.bounds(blockIdx.x, r0, r1);
-    Walk<GATE> at;
-    at.begin(sl, r0, r1, team);
     // The teams meet at the row sums' barriers: all go as often as the first, the
     // last of them perhaps without a row.
-    Walk<GATE> lead, trail;
+    Walk<GATE> at, lead, trail;
+    at.begin(sl, r0, r1, team);
     lead.begin(sl, r0, r1, 0);
     trail.begin(sl, r0, r1, P - 1);
     int turn = 0;
@@ -507,28 +478,28 @@ __global__ __launch_bounds__(T ? T : 256) void residual_grad_kernel(
         RowStats st;
     };
     Row in;
-    // operands that are not there are read where others are, and not used
-    const void* dxo = a.dxo ? a.dxo : a.xo;
-    const int64_t lddxo = a.dxo ? a.lddxo : a.ldxo;
-    const bool stream = a.dxo != nullptr;
-    const bool branch = a.b != nullptr;
-    const void* b = branch ? a.b : a.db;
-    const int64_t ldb = branch ? a.ldb : a.lddb;
+    const void* dxo = a.dxo ? a.dxo : zeros;
+    const int64_t lddxo = a.dxo ? a.lddxo : 0;
+    const void* b = a.b ? a.b : zeros;
+    const int64_t ldb = a.b ? a.ldb : 0;
     const int64_t group0 = GATE ? r0 / sl.group : 0;
-    auto fetch = [&](const Walk<GATE>& w) __attribute__((always_inline)) {
-        const int64_t row = w.in ? w.r : r1 - 1;
+    auto gate_row = [&](int64_t row) __attribute__((always_inline)) {
+        return group0 + (uint32_t)(row - r0) / (uint32_t)sl.group;
+    };
+    auto fetch = [&]() __attribute__((always_inline)) {
+        const int64_t row = at.in ? at.r : r1 - 1;
         in.st = RowStats::of(a, row);
-        const int64_t g = GATE ? (group0 + (uint32_t)(row - r0) / (uint32_t)sl.group) * a.ldg : 0;
+        const int64_t g = GATE ? gate_row(row) * a.ldg : 0;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            in.x[k].load(a.xo, row * a.ldxo + pl.start(k));
-            in.d[k].load(a.dy, row * a.lddy + pl.start(k));
-            in.s[k].load(dxo, row * lddxo + pl.start(k));
-            in.b[k].load(b, row * ldb + pl.start(k));
-            if (GATE) in.g[k].load(a.gate, g + pl.start(k));
+            in.x[k].load_row(a.xo, row * a.ldxo, pl.start(k));
+            in.d[k].load_row(a.dy, row * a.lddy, pl.start(k));
+            in.s[k].load_row(dxo, row * lddxo, pl.start(k));
+            in.b[k].load_row(b, row * ldb, pl.start(k));
+            if (GATE) in.g[k].load_row(a.gate, g, pl.start(k));
         }
     };
-    fetch(at);
+    fetch();
     float w[NV][8], u[NV][8];
     float dw[NV][8] = {}, dc[NV][8] = {}, s1[NV][8] = {}, s2[NV][8] = {};
     float dpw[GATE ? NV : 1][8] = {}, dpc[GATE ? NV : 1][8] = {};
@@ -536,12 +507,15 @@ __global__ __launch_bounds__(T ? T : 256) void residual_grad_kernel(
     for (int k = 0; k < NV; ++k) {
         load_vec8(a.weight, a.w_bf16, pl.start(k), 1.0f, w[k]);
         load_vec8(a.post_weight, a.w_bf16, pl.start(k), 1.0f, u[k]);
-        float g[8];
-        const bool one = !GATE && a.gate;
-        load_vec8(one ? a.gate : nullptr, a.gate_bf16,
-                  (one ? sl.group_of(blockIdx.x) * a.ldg : 0) + pl.start(k), 1.0f, g);
+        if (GATE || !a.gate) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) u[k][e] *= a.branch_scale * g[e];
+            for (int e = 0; e < 8; ++e) u[k][e] *= a.branch_scale;
+        } else {
+            float g[8];
+            load_vec8(a.gate, a.gate_bf16, sl.group_of(blockIdx.x) * a.ldg + pl.start(k), 1.0f, g);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) u[k][e] *= a.branch_scale * g[e];
+        }
     }
     const float rn = 1.0f / (float)cols;
     // One row of each team; `all`: every team has one.  (A store under a condition
@@ -549,9 +523,9 @@ __global__ __launch_bounds__(T ? T : 256) void residual_grad_kernel(
     // for them with the next row's loads.)
     auto one = [&](auto all) __attribute__((always_inline)) {
         const RowStats st = in.st;
-        const int64_t r = at.r;
         const bool on = decltype(all)::value || at.in;
         const bool flush = GATE && on && at.last_of_group();
+        const int64_t r = at.r;
         float xh[NV][8], d[NV][8], sx[NV][8], h[NV][8], g[GATE ? NV : 1][8];
 #pragma unroll
         for (int k = 0; k < NV; ++k)
@@ -559,8 +533,8 @@ __global__ __launch_bounds__(T ? T : 256) void residual_grad_kernel(
             for (int e = 0; e < 8; ++e) {
                 xh[k][e] = (in.x[k].at(e) - st.m) * st.r;
                 d[k][e] = in.d[k].at(e);
-                sx[k][e] = stream ? in.s[k].at(e) : 0.0f;
-                h[k][e] = branch ? (in.b[k].at(e) - st.pm) * st.pr : 0.0f;
+                sx[k][e] = in.s[k].at(e);
+                h[k][e] = (in.b[k].at(e) - st.pm) * st.pr;
                 if (GATE) g[k][e] = in.g[k].at(e);
             }
         // dx and db may lie on dxo and b, whose last elements two waves hold: all
@@ -575,19 +549,18 @@ __global__ __launch_bounds__(T ? T : 256) void residual_grad_kernel(
             lead.next(sl, r1, P);
             trail.next(sl, r1, P);
         }
-        fetch(at);
+        fetch();
         float s[2] = {0.0f, 0.0f};  // of t xh, and of t
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             float p0 = 0.0f, p1 = 0.0f;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float t = d[k][e];
                 if (on) {
-                    dw[k][e] += t * xh[k][e];
-                    dc[k][e] += t;
+                    dw[k][e] += d[k][e] * xh[k][e];
+                    dc[k][e] += d[k][e];
                 }
-                d[k][e] = t * w[k][e];
+                d[k][e] *= w[k][e];
                 const float o = pl.owns(k, e) ? d[k][e] : 0.0f;
                 p0 += o * xh[k][e];
                 p1 += o;
@@ -611,11 +584,11 @@ __global__ __launch_bounds__(T ? T : 256) void residual_grad_kernel(
                     s2[k][e] += d[k][e];
                     f[e] = a.x_scale * d[k][e];
                 }
-                store_chunk<XB>(a.dx, r * a.lddx + pl.start(k), f);
+                store_row<XB>(a.dx, r * a.lddx, pl.start(k), f);
             }
         }
         if (flush) {
-            const int64_t at_g = (group0 + (uint32_t)(r - r0) / (uint32_t)sl.group) * a.cols;
+            const int64_t at_g = gate_row(r) * a.cols;
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
                 float f[8], pc[8];
@@ -663,7 +636,7 @@ __global__ __launch_bounds__(T ? T : 256) void residual_grad_kernel(
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     f[e] = post ? st.pr * (d[k][e] - mu - h[k][e] * mh) : d[k][e];
-                store_chunk<BB>(a.db, r * a.lddb + pl.start(k), f);
+                store_row<BB>(a.db, r * a.lddb, pl.start(k), f);
             }
         }
     };
@@ -675,41 +648,35 @@ __global__ __launch_bounds__(T ? T : 256) void residual_grad_kernel(
     auto sums_of = [&](int o, int k) __attribute__((always_inline)) -> float(&)[8] {
         return o == 0 ? dw[k] : o == 1 ? dc[k] : o == 2 ? (GATE ? dpw[k] : s1[k]) : (GATE ? dpc[k] : s2[k]);
     };
-    if (P == 1) {
+    // (where two lanes hold an element, their sums of it are the same bits)
+    if (NV != 1 || P == 1) {
 #pragma unroll
         for (int o = 0; o < 4; ++o)
 #pragma unroll
-            for (int k = 0; k < NV; ++k)
-                store_own<0>(out + o * cols, pl.start(k), sums_of(o, k), k < NV - 1 ? 0 : pl.skip);
+            for (int k = 0; k < NV; ++k) store_row<0>(out, o * cols, pl.start(k), sums_of(o, k));
         return;
     }
-    if (NV != 1) return;  // such rows have one team
-    // the teams' sums of the same columns, added up through LDS
-    const int span = pl.W * 512;  // columns that a team's lanes hold
-    __syncthreads();
+    // The teams' sums of the same columns are added up through LDS, four of a
+    // lane's columns at a time: part j of a lane's eight is added by team j % P.
+    const int threads = blockDim.x;
 #pragma unroll
-    for (int o = 0; o < 4; ++o) {
-        float(&v)[8] = sums_of(o, 0);
-        float* mine = red + (o * P + team) * span;
-        if (pl.skip == 0) {
-            *(u32x4*)(mine + pl.t) = (u32x4){as_u32(v[0]), as_u32(v[1]), as_u32(v[2]), as_u32(v[3])};
-            *(u32x4*)(mine + pl.t + 4) =
-                (u32x4){as_u32(v[4]), as_u32(v[5]), as_u32(v[6]), as_u32(v[7])};
-        } else {
-#pragma unroll
-            for (int e = 1; e < 8; ++e)
-                if (e >= pl.skip) mine[pl.tail + e] = v[e];
-        }
+    for (int j = 0; j < 8; ++j) {
+        const float* v = sums_of(j >> 1, 0) + 4 * (j & 1);
+        sums[(NV == 1 ? j : 0) * threads + threadIdx.x] =
+            (u32x4){as_u32(v[0]), as_u32(v[1]), as_u32(v[2]), as_u32(v[3])};
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < cols; i += blockDim.x) {
+    const int lane = threadIdx.x - wave0 * 64, waves = MULTI ? W * 64 : 64;
+    for (int j = team; j < 8; j += P) {
+        float v[4] = {};
+#pragma unroll 4
+        for (int q = 0; q < P; ++q) {
+            const u32x4 t = sums[j * threads + q * waves + lane];
 #pragma unroll
-        for (int o = 0; o < 4; ++o) {
-            const float* q = red + o * P * span + i;
-            float sum = q[0];
-            for (int t = 1; t < P; ++t) sum += q[t * span];
-            out[o * cols + i] = sum;
+            for (int e = 0; e < 4; ++e) v[e] += as_f32(t[e]);
         }
+        *(u32x4_a4*)(out + (j >> 1) * cols + pl.start(0) + 4 * (j & 1)) =
+            (u32x4){as_u32(v[0]), as_u32(v[1]), as_u32(v[2]), as_u32(v[3])};
     }
 }
 
@@ -736,15 +703,14 @@ static GradShape grad_shape(int64_t cols, bool whole) {
     return {T, 1, waves, 64 * waves * (T / 64 / waves)};
 }
 // As many slabs as 256 compute units hold workgroups of (12 waves to a unit, 8
-// where a row of gates comes with every row), of FP4Q_MIN rows and more.
-#ifndef FP4Q_MIN
-#define FP4Q_MIN 8
-#endif
+// where a row of gates comes with every row), of a few rows and more: 4 and 8
+// rows take 7.4 and 9.9 us at 256 x 1112 fp32 (32 and 64 workgroups), 20.4 and
+// 18.9 with the join at 1000 x 2048 bf16, where the partial sums count.
 static Slabs grad_slabs(int64_t rows, int64_t cols, int64_t gate_rows) {
     const auto slabs = [&](bool whole) {
         const GradShape sh = grad_shape(cols, whole);
         const int64_t most = sh.nv == 0 ? 256 : 256 * std::max(1, (whole ? 8 : 12) * 64 / sh.threads);
-        return make_slabs(rows, gate_rows, most, sh.nv && sh.T ? FP4Q_MIN : 16);
+        return make_slabs(rows, gate_rows, most, sh.nv && sh.T ? (rows <= 512 ? 4 : 8) : 16);
     };
     const Slabs sl = slabs(false);
     return gate_rows < rows && !sl.k ? slabs(true) : sl;
@@ -815,7 +781,7 @@ hipError_t launch_residual_norm_grad(const ResidualNormGrad& a, void* ws, hipStr
         a.b_bf16 ? go_dy<0, 1>(sh, a, sl, means, p, s) : go_dy<0, 0>(sh, a, sl, means, p, s);
     if (sums) {
         int64_t gates = a.dgate && sl.k ? sl.count / sl.k : 0;
-        if (sl.k <= kFewParts) gates = (gates + 63) / 64;
+        if (sl.k <= kFewParts) gates = (gates + 15) / 16;
         gates = std::min(gates, kGridY);
         const int64_t groups = (a.cols + 63) / 64;
         for (int64_t g = 0; g < groups; g += kJoinGroups)

@@ -48,6 +48,12 @@ struct Chunk {
             v[BF16T ? 0 : 1] = *(const u32x4_a4*)((const float*)p + i + 4);
         }
     }
+    // From element `first` of p, the same for the wave, and this lane's `c`: an
+    // address of a scalar and a 32-bit part.
+    __device__ __forceinline__ void load_row(const void* p, int64_t first, int c) {
+        const char* q = (const char*)p + first * (BF16T ? 2 : 4) + (uint32_t)c * (BF16T ? 2u : 4u);
+        load(q, 0);
+    }
     // Waits here for the load.
     __device__ __forceinline__ void arrived() const {
         asm volatile("" ::"v"(v[0][0]));
@@ -76,6 +82,11 @@ __device__ __forceinline__ void store_chunk(void* p, int64_t i, const float (&f)
         *(u32x4_a4*)q = (u32x4){as_u32(f[0]), as_u32(f[1]), as_u32(f[2]), as_u32(f[3])};
         *(u32x4_a4*)(q + 4) = (u32x4){as_u32(f[4]), as_u32(f[5]), as_u32(f[6]), as_u32(f[7])};
     }
+}
+// From element `first` of p, the same for the wave, and this lane's `c`.
+template <int BF16T>
+__device__ __forceinline__ void store_row(void* p, int64_t first, int c, const float (&f)[8]) {
+    store_chunk<BF16T>((char*)p + first * (BF16T ? 2 : 4) + (uint32_t)c * (BF16T ? 2u : 4u), 0, f);
 }
 // All of them, or elements skip .. 7.
 template <int BF16T>

@@ -149,6 +149,7 @@ def test_bindings_check_shapes_types_and_devices(there):
             (dict(gate=rows(2, 8), gate_rows=0), ValueError, "share one"),
             (dict(x_out=rows(4, 8, dtype=torch.bfloat16)), TypeError, "x_out"),
             (dict(y=rows(3, 8)), ValueError, "y must"), (dict(y=rows(), quantize=True), ValueError, "not quantized"),
+            (dict(quantize=True), ValueError, "multiple of 32"), (dict(branch=x.expand(2, 4, 8)[0].t()), ValueError, "branch"),
             (dict(branch=dev(torch.zeros(4, 16))[:, ::2]), ValueError, "stride")):
         with pytest.raises(e, match=text):
             fq.residual_norm(x, **{"branch": x, **kw})
@@ -204,10 +205,10 @@ def test_grad_plan_checks(there):
 
 
 def test_what_a_call_allocates_belongs_to_its_stream(there):
-    x, s = rows(), dev(torch.zeros(4))
+    x, s, wide = rows(), dev(torch.zeros(4)), rows(4, 32)
     p = fq.grad_plan([x])
     for call, made in ((lambda **kw: fq.residual_norm(x, x, post_kind=fq.LAYER_NORM, **kw), 6),
-                       (lambda **kw: fq.residual_norm(x, x, quantize=True, kind=fq.RMS_NORM, **kw), 4),
+                       (lambda **kw: fq.residual_norm(wide, wide, quantize=True, kind=fq.RMS_NORM, **kw), 4),
                        (lambda **kw: fq.residual_norm_grad(x, x, x, x, (None, None, s, s), gate=s.new_zeros(8), **kw), 6),
                        (lambda **kw: fq.grad_norm(p, 1.0, **kw), 3), (lambda **kw: fq.clip_grads(p, 1.0, **kw), 3)):
         MADE.clear()
