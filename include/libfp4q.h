@@ -700,6 +700,17 @@ fp4q_status_t fp4q_grad_norm(const fp4q_tensor_t* tensors, int32_t n, fp4q_norm_
                              void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * fp4q_grad_clip -- fp4q_grad_norm, and every element times its scale, in place,
+ * rounded to its type: gradients whose norm is at most max_norm - eps stay as
+ * they are, bit for bit.  norm: device fp32, the norm that they had, NULL to
+ * skip.  The tensors must not overlap; the other arguments and the results, NaN
+ * and Inf included, are fp4q_grad_norm's (of fp32 products: Inf times 0 is NaN).
+ */
+fp4q_status_t fp4q_grad_clip(const fp4q_tensor_t* tensors, int32_t n, fp4q_norm_order_t order,
+                             double max_norm, double eps, float* norm, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/*
  * fp4q_grad_scale -- every element of the tensors times *scale (device fp32), in
  * place, each rounded to its type.  Tensors as in fp4q_grad_norm; those of one
  * call must not overlap.  With *scale = 1 nothing is read or written.

@@ -35,7 +35,8 @@ EXPORTS = ["fp4q_channel_mask", "fp4q_quantize_masked", "fp4q_gemm_hcp_split",
            "fp4q_layer_norm_grad_workspace_bytes", "fp4q_layer_norm_grad", "fp4q_adamw_step",
            "fp4q_adamw_table", "fp4q_adamw_step_table", "fp4q_residual_norm",
            "fp4q_residual_norm_grad_workspace_bytes", "fp4q_residual_norm_grad",
-           "fp4q_grad_norm_workspace_bytes", "fp4q_grad_norm", "fp4q_grad_scale",
+           "fp4q_grad_norm_workspace_bytes", "fp4q_grad_norm", "fp4q_grad_clip",
+           "fp4q_grad_scale",
            "fp4q_set_next_launch", "fp4q_status_string",
            "fp4q_last_error", "fp4q_abi_version"]
 
@@ -124,6 +125,7 @@ def lib():
                                               I64, P, I64, P, P, P, P, P, P, SZ, P]),
             "fp4q_grad_norm_workspace_bytes": (SZ, [P, I32]),
             "fp4q_grad_norm": (I32, [P, I32, I32, D, D, P, P, P, SZ, P]),
+            "fp4q_grad_clip": (I32, [P, I32, I32, D, D, P, P, SZ, P]),
             "fp4q_grad_scale": (I32, [P, I32, P, P]),
             "fp4q_set_next_launch": (I32, [P, P, _ct.c_uint32]),
             "fp4q_status_string": (_ct.c_char_p, [I32]),
@@ -1142,6 +1144,29 @@ def _grads_of(plan):
     return plan
 
 
+def _scalar(t, name, d, empty):
+    """A given fp32 scalar on device d, or a new one."""
+    f32 = _torch_module.float32
+    if t is None:
+        return empty((), (), f32)
+    _need_cuda(t)
+    _need(t, name, f32)
+    if t.numel() != 1:
+        raise ValueError(f"{name} must have one element, got {t.numel()}")
+    _same_device(t, name, d)
+    return t
+
+
+def _norm_workspace(workspace, plan, d, empty):
+    """A given workspace or a new one, and its bytes."""
+    if workspace is None:
+        return empty((plan.nbytes,), (1,), _torch_module.uint8), plan.nbytes
+    _need_cuda(workspace)
+    _need(workspace, "workspace", workspace.dtype)
+    _same_device(workspace, "workspace", d)
+    return workspace, workspace.numel() * workspace.element_size()
+
+
 def grad_norm(plan, max_norm=None, eps=1e-6, order=NORM_L2, norm=None, scale=None, workspace=None,
               stream=None):
     """The norm of a plan's gradients taken as one vector (fp4q_grad_norm), and
@@ -1150,35 +1175,18 @@ def grad_norm(plan, max_norm=None, eps=1e-6, order=NORM_L2, norm=None, scale=Non
     device fp32 scalars (scale None without max_norm); scale is adamw_step's
     grad_scale.  A graph that captured the call reads the plan's memory at every
     replay: the plan is kept as long as the graph."""
-    f32 = _torch().float32
     plan = _grads_of(plan)
     d = _device_of(plan.like, stream)
     empty = _allocator(plan.like, stream)
-    for t, name in ((norm, "norm"), (scale, "scale")):
-        if t is not None:
-            _need_cuda(t)
-            _need(t, name, f32)
-            if t.numel() != 1:
-                raise ValueError(f"{name} must have one element, got {t.numel()}")
-            _same_device(t, name, d)
-    if norm is None:
-        norm = empty((), (), f32)
-    if max_norm is None:
-        if scale is not None:
-            raise ValueError("scale needs max_norm")
-    elif scale is None:
-        scale = empty((), (), f32)
-    if workspace is None:
-        nbytes = plan.nbytes
-        workspace = empty((nbytes,), (1,), _torch().uint8)
-    else:
-        _need_cuda(workspace)
-        _need(workspace, "workspace", workspace.dtype)
-        _same_device(workspace, "workspace", d)
-        nbytes = workspace.numel() * workspace.element_size()
-    status = (_lib or lib()).fp4q_grad_norm(plan.array, plan.n, order, 0.0 if max_norm is None else max_norm, eps,
-                                  norm.data_ptr(), _ptr(scale), workspace.data_ptr(), nbytes,
-                                  _stream(stream))
+    norm = _scalar(norm, "norm", d, empty)
+    if max_norm is not None:
+        scale = _scalar(scale, "scale", d, empty)
+    elif scale is not None:
+        raise ValueError("scale needs max_norm")
+    workspace, nbytes = _norm_workspace(workspace, plan, d, empty)
+    status = (_lib or lib()).fp4q_grad_norm(plan.array, plan.n, order, 0.0 if max_norm is None else max_norm,
+                                            eps, norm.data_ptr(), _ptr(scale), workspace.data_ptr(), nbytes,
+                                            _stream(stream))
     if status:
         _check(status)
     return norm, scale
@@ -1198,11 +1206,19 @@ def scale_grads(plan, scale, stream=None):
         _check(status)
 
 
-def clip_grads(plan, max_norm, eps=1e-6, order=NORM_L2, stream=None):
-    """Clips a plan's gradients in place to the norm max_norm (grad_norm, then
-    scale_grads).  Returns the norm they had, a device fp32 scalar."""
-    norm, scale = grad_norm(plan, max_norm, eps, order, stream=stream)
-    scale_grads(plan, scale, stream)
+def clip_grads(plan, max_norm, eps=1e-6, order=NORM_L2, norm=None, workspace=None, stream=None):
+    """Clips a plan's gradients in place to the norm max_norm (fp4q_grad_clip):
+    what scale_grads does with grad_norm's scale.  Returns the norm they had, a
+    device fp32 scalar."""
+    plan = _grads_of(plan)
+    d = _device_of(plan.like, stream)
+    empty = _allocator(plan.like, stream)
+    norm = _scalar(norm, "norm", d, empty)
+    workspace, nbytes = _norm_workspace(workspace, plan, d, empty)
+    status = (_lib or lib()).fp4q_grad_clip(plan.array, plan.n, order, max_norm, eps, norm.data_ptr(),
+                                            workspace.data_ptr(), nbytes, _stream(stream))
+    if status:
+        _check(status)
     return norm
 
 

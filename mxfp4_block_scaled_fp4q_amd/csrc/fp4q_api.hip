@@ -148,6 +148,27 @@ fp4q_status_t grad_tensors(const char* who, const fp4q_tensor_t* tensors, int32_
     return FP4Q_OK;
 }
 
+// Arguments that the gradient norm and the clipping share.
+fp4q_status_t grad_norm_args(const char* who, const fp4q_tensor_t* tensors, int32_t n,
+                             fp4q_norm_order_t order, double max_norm, double eps, const float* norm,
+                             const float* scale, const void* workspace, size_t workspace_bytes) {
+    if (order != FP4Q_NORM_L2 && order != FP4Q_NORM_MAX)
+        return fail(FP4Q_ERR_INVALID, "%s: bad order %d", who, (int)order);
+    if (!(max_norm >= 0.0) || !(max_norm < 1e300) || !(eps >= 0.0) || !(eps < 1e300))
+        return fail(FP4Q_ERR_INVALID, "%s: bad max_norm or eps", who);
+    const fp4q_status_t e = grad_tensors(who, tensors, n);
+    if (e != FP4Q_OK) return e;
+    if (((uintptr_t)norm % 4) || ((uintptr_t)scale % 4))
+        return fail(FP4Q_ERR_ALIGNMENT, "%s: pointers must be element-aligned", who);
+    const size_t need = fp4q::grad_norm_workspace_bytes(tensors, n);
+    if (!workspace) return fail(FP4Q_ERR_INVALID, "%s: null workspace", who);
+    if (!aligned16(workspace))
+        return fail(FP4Q_ERR_ALIGNMENT, "%s: workspace must be 16-byte aligned", who);
+    if (workspace_bytes < need)
+        return fail(FP4Q_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", who, workspace_bytes, need);
+    return FP4Q_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -997,24 +1018,24 @@ size_t fp4q_grad_norm_workspace_bytes(const fp4q_tensor_t* tensors, int32_t n) {
 fp4q_status_t fp4q_grad_norm(const fp4q_tensor_t* tensors, int32_t n, fp4q_norm_order_t order,
                              double max_norm, double eps, float* norm, float* scale,
                              void* workspace, size_t workspace_bytes, void* stream) {
-    if (order != FP4Q_NORM_L2 && order != FP4Q_NORM_MAX)
-        return fail(FP4Q_ERR_INVALID, "grad_norm: bad order %d", (int)order);
-    if (!(max_norm >= 0.0) || !(max_norm < 1e300) || !(eps >= 0.0) || !(eps < 1e300))
-        return fail(FP4Q_ERR_INVALID, "grad_norm: bad max_norm or eps");
-    const fp4q_status_t e = grad_tensors("grad_norm", tensors, n);
-    if (e != FP4Q_OK) return e;
     if (!norm && !scale) return fail(FP4Q_ERR_INVALID, "grad_norm: null pointer");
-    if (((uintptr_t)norm % 4) || ((uintptr_t)scale % 4))
-        return fail(FP4Q_ERR_ALIGNMENT, "grad_norm: pointers must be element-aligned");
-    const size_t need = fp4q::grad_norm_workspace_bytes(tensors, n);
-    if (!workspace) return fail(FP4Q_ERR_INVALID, "grad_norm: null workspace");
-    if (!aligned16(workspace))
-        return fail(FP4Q_ERR_ALIGNMENT, "grad_norm: workspace must be 16-byte aligned");
-    if (workspace_bytes < need)
-        return fail(FP4Q_ERR_WORKSPACE, "grad_norm: workspace %zu < %zu bytes", workspace_bytes, need);
+    const fp4q_status_t e = grad_norm_args("grad_norm", tensors, n, order, max_norm, eps, norm, scale,
+                                           workspace, workspace_bytes);
+    if (e != FP4Q_OK) return e;
     return hip_status(fp4q::launch_grad_norm(tensors, n, order == FP4Q_NORM_MAX, max_norm, eps, norm,
                                              scale, workspace, (hipStream_t)stream),
                       "grad_norm launch");
+}
+
+fp4q_status_t fp4q_grad_clip(const fp4q_tensor_t* tensors, int32_t n, fp4q_norm_order_t order,
+                             double max_norm, double eps, float* norm, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+    const fp4q_status_t e = grad_norm_args("grad_clip", tensors, n, order, max_norm, eps, norm, nullptr,
+                                           workspace, workspace_bytes);
+    if (e != FP4Q_OK) return e;
+    return hip_status(fp4q::launch_grad_clip(tensors, n, order == FP4Q_NORM_MAX, max_norm, eps, norm,
+                                             workspace, (hipStream_t)stream),
+                      "grad_clip launch");
 }
 
 fp4q_status_t fp4q_grad_scale(const fp4q_tensor_t* tensors, int32_t n, const float* scale,

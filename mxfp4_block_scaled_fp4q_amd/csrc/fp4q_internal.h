@@ -180,6 +180,8 @@ hipError_t launch_norm_grad(const void* dy, int dydtype, int64_t lddy, const voi
 size_t grad_norm_workspace_bytes(const fp4q_tensor* t, int n);
 hipError_t launch_grad_norm(const fp4q_tensor* t, int n, bool largest, double max_norm, double eps,
                             float* norm, float* scale, void* ws, hipStream_t s);
+hipError_t launch_grad_clip(const fp4q_tensor* t, int n, bool largest, double max_norm, double eps,
+                            float* norm, void* ws, hipStream_t s);
 hipError_t launch_grad_scale(const fp4q_tensor* t, int n, const float* scale, hipStream_t s);
 hipError_t launch_adamw(const fp4q_adamw_tensor* t, int n, int bits, int gdtype, double lr,
                         double beta1, double beta2, double eps, int64_t step, uint64_t seed,

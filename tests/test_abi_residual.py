@@ -94,8 +94,13 @@ def grads(*t):
 def test_grad_norm_refusals(L, t, kw, status):
     a = dict(n=2, order=0, max_norm=1.0, eps=1e-6, norm=FAKE, scale=FAKE, ws=FAKE, nb=1 << 30)
     a.update(kw)
-    assert L.fp4q_grad_norm(grads((NUL, 0, 0), t), *a.values(), NUL) == status
+    two = grads((NUL, 0, 0), t)
+    assert L.fp4q_grad_norm(two, *a.values(), NUL) == status
     assert "grad_norm" in L.fp4q_last_error().decode()
+    if "scale" not in kw:
+        a.pop("scale")
+        assert L.fp4q_grad_clip(two, *a.values(), NUL) == status
+        assert "grad_clip" in L.fp4q_last_error().decode()
 
 
 def test_grad_scale_refusals_and_empty_calls(L):
@@ -210,7 +215,7 @@ def test_what_a_call_allocates_belongs_to_its_stream(there):
     for call, made in ((lambda **kw: fq.residual_norm(x, x, post_kind=fq.LAYER_NORM, **kw), 6),
                        (lambda **kw: fq.residual_norm(wide, wide, quantize=True, kind=fq.RMS_NORM, **kw), 4),
                        (lambda **kw: fq.residual_norm_grad(x, x, x, x, (None, None, s, s), gate=s.new_zeros(8), **kw), 6),
-                       (lambda **kw: fq.grad_norm(p, 1.0, **kw), 3), (lambda **kw: fq.clip_grads(p, 1.0, **kw), 3)):
+                       (lambda **kw: fq.grad_norm(p, 1.0, **kw), 3), (lambda **kw: fq.clip_grads(p, 1.0, **kw), 2)):
         MADE.clear()
         call(stream=there["side"])
         assert len(MADE) == made
