@@ -21,7 +21,6 @@
 namespace fp4q {
 
 constexpr int64_t kAnyGrid = 1 << 16;
-constexpr int kForwardWaves = 16;
 
 // Codes of 8 values of a block of 32 that four neighbouring lanes hold, as
 // fp4q_quantize gives them, and its scale byte.
@@ -193,7 +192,11 @@ struct Moments {
 template <int XB, int BB, int OUT, int GATE, int MULTI, int NV>
 __global__ __launch_bounds__(MULTI ? 1024 : 256) void residual_norm_kernel(const ResidualNorm a,
                                                                            const FastDiv div) {
+    // two chunks leave 1024 threads no registers for the vectors of the norm
+    // behind the block, which then lie in LDS, 16 floats per lane each
+    constexpr bool kLds = MULTI && NV == 2;
     __shared__ float red[MULTI ? 2 * 32 : 1];
+    __shared__ u32x4 vectors[kLds ? 2 * 2 * NV * 1024 : 1];
     const int cols = (int)a.cols;
     Place<NV> pl = Place<NV>::template make<MULTI>(cols);
     // a lane past the row's end holds its place in the last block of 32 again,
@@ -214,12 +217,19 @@ __global__ __launch_bounds__(MULTI ? 1024 : 256) void residual_norm_kernel(const
         const int64_t g = GATE ? (int64_t)fastdiv((uint32_t)row, div) * a.ldg : 0;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            in.b[k].load(a.b, row * a.ldb + pl.start(k));
-            in.x[k].load(a.x, row * a.ldx + pl.start(k));
-            if (GATE) in.g[k].load(a.gate, g + pl.start(k));
+            in.b[k].load_row(a.b, row * a.ldb, pl.start(k));
+            in.x[k].load_row(a.x, row * a.ldx, pl.start(k));
+            if (GATE) in.g[k].load_row(a.gate, g, pl.start(k));
         }
     };
     fetch(r);
+    // half h of this lane's chunk k of the weight (o = 0) or the bias
+    auto slot = [&](int o, int k, int h) __attribute__((always_inline)) -> u32x4& {
+        return vectors[((o * NV + k) * 2 + h) * 1024 + threadIdx.x];
+    };
+    auto words = [](const float(&v)[8], int h) __attribute__((always_inline)) {
+        return (u32x4){as_u32(v[4 * h]), as_u32(v[4 * h + 1]), as_u32(v[4 * h + 2]), as_u32(v[4 * h + 3])};
+    };
     float pw[NV][8], pc[NV][8], w[NV][8], c[NV][8];
     const bool post = a.post != kPostNone, post_layer = a.post == 0;
 #pragma unroll
@@ -234,6 +244,13 @@ __global__ __launch_bounds__(MULTI ? 1024 : 256) void residual_norm_kernel(const
         for (int e = 0; e < 8; ++e) {
             pw[k][e] *= a.branch_scale * g[e];
             pc[k][e] *= a.branch_scale * g[e];
+        }
+        if (kLds) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                slot(0, k, h) = words(pw[k], h);
+                slot(1, k, h) = words(pc[k], h);
+            }
         }
     }
     float pm = 0.0f, pr = 1.0f, m = 0.0f, rs = 0.0f;
@@ -265,20 +282,32 @@ __global__ __launch_bounds__(MULTI ? 1024 : 256) void residual_norm_kernel(const
             pr = 1.0f / sqrtf(var + a.eps);
         }
 #pragma unroll
-        for (int k = 0; k < NV; ++k)
+        for (int k = 0; k < NV; ++k) {
+            if (kLds) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const u32x4 vw = slot(0, k, h), vc = slot(1, k, h);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        pw[k][4 * h + e] = as_f32(vw[e]);
+                        pc[k][4 * h + e] = as_f32(vc[e]);
+                    }
+                }
+            }
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 float t = (n[k][e] - pm) * pr * pw[k][e] + pc[k][e];
                 if (GATE) t *= g[k][e];
                 v[k][e] = a.x_scale * v[k][e] + t;
             }
+        }
         float var;
         moments.of(pl, v, !a.rms, m, var);
         rs = 1.0f / sqrtf(var + a.eps);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int64_t c0 = pl.start(k);
-            store_chunk<XB>(a.xo, r * a.ldxo + c0, v[k]);
+            store_row<XB>(a.xo, r * a.ldxo, pl.start(k), v[k]);
             float f[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) f[e] = ((v[k][e] - m) * rs) * w[k][e] + c[k][e];
@@ -288,17 +317,25 @@ __global__ __launch_bounds__(MULTI ? 1024 : 256) void residual_norm_kernel(const
                 *(uint32_t*)(a.codes + r * (cols / 2) + c0 / 2) = q;
                 a.scales[r * (cols / 32) + c0 / 32] = (uint8_t)byte;
             } else {
-                store_chunk<OUT>(a.y, r * a.ldy + c0, f);
+                store_row<OUT>(a.y, r * a.ldy, pl.start(k), f);
             }
         }
     }
     stats(last);
 }
 
+// Waves per compute unit by the bytes that a lane loads for an element: up to 4
+// leave registers for more of them.  16, 20, 24 and 32 waves: 8192 x 2048 bf16
+// 26.3, 25.6, 24.7, 25.7 us, 16384 x 5120 158, 139, 139, 140; with an fp32 stream
+// 34.4, 34.6, 35.6, 36.9 and 178, 190, 190, 192; 4000 x 1111 fp32 with a gate per
+// sequence 13.3, 13.6, 14.7, 14.3.
+constexpr int kWavesLight = 24, kWavesHeavy = 16;
+
 template <int XB, int BB, int OUT, int GATE>
 static void go_rows(const NormShape sh, const ResidualNorm& a, hipStream_t s) {
     const FastDiv div = make_fastdiv((uint32_t)a.gate_rows);
-    const unsigned groups = (unsigned)norm_groups(sh, a.rows, kForwardWaves, 1);
+    const int loaded = (XB ? 2 : 4) + (BB ? 2 : 4) + (GATE == 0 ? 0 : GATE == 2 ? 2 : 4);
+    const unsigned groups = (unsigned)norm_groups(sh, a.rows, loaded <= 4 ? kWavesLight : kWavesHeavy, 1);
 #define FP4Q_GO(MULTI, NV)                                                                      \
     if (sh.multi == (bool)MULTI && sh.nv == NV)                                                 \
     FP4Q_LAUNCH((residual_norm_kernel<XB, BB, OUT, GATE, MULTI, NV>), dim3(groups),             \
