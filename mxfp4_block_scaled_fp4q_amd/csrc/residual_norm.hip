@@ -195,6 +195,9 @@ __global__ __launch_bounds__(MULTI ? 1024 : 256) void residual_norm_kernel(const
     // two chunks leave 1024 threads no registers for the vectors of the norm
     // behind the block, which then lie in LDS, 16 floats per lane each
     constexpr bool kLds = MULTI && NV == 2;
+    // nor, where gates come with the rows, for the next row (2000 x 13824 fp32 150
+    // us with spills, 91 without the next row)
+    constexpr bool kAhead = !kLds || !GATE;
     __shared__ float red[MULTI ? 2 * 32 : 1];
     __shared__ u32x4 vectors[kLds ? 2 * 2 * NV * 1024 : 1];
     const int cols = (int)a.cols;
@@ -222,7 +225,7 @@ __global__ __launch_bounds__(MULTI ? 1024 : 256) void residual_norm_kernel(const
             if (GATE) in.g[k].load_row(a.gate, g, pl.start(k));
         }
     };
-    fetch(r);
+    if (kAhead) fetch(r);
     // half h of this lane's chunk k of the weight (o = 0) or the bias
     auto slot = [&](int o, int k, int h) __attribute__((always_inline)) -> u32x4& {
         return vectors[((o * NV + k) * 2 + h) * 1024 + threadIdx.x];
@@ -265,6 +268,7 @@ __global__ __launch_bounds__(MULTI ? 1024 : 256) void residual_norm_kernel(const
     int64_t last = -1;
     for (; r < a.rows; r += step) {
         float v[NV][8], n[NV][8], g[NV][8];
+        if (!kAhead) fetch(r);
 #pragma unroll
         for (int k = 0; k < NV; ++k)
 #pragma unroll
@@ -275,7 +279,7 @@ __global__ __launch_bounds__(MULTI ? 1024 : 256) void residual_norm_kernel(const
             }
         if (last >= 0) stats(last);
         last = r;
-        fetch(r + step);
+        if (kAhead) fetch(r + step);
         if (post) {
             float var;
             moments.of(pl, n, post_layer, pm, var);
