@@ -45,7 +45,7 @@ static Slabs make_slabs(int64_t rows, int64_t gate_rows, int64_t most, int64_t l
         s.count = all * s.k;
     } else {
         s.k = 0;
-        s.each = each / s.group * s.group;
+        s.each = (each < rows ? each / s.group : all) * s.group;
         s.count = (rows + s.each - 1) / s.each;
     }
     s.div = make_fastdiv((uint32_t)std::max<int64_t>(s.k, 1));
@@ -654,29 +654,51 @@ __global__ __launch_bounds__(T ? T : 256) void residual_grad_kernel(
         for (int o = 0; o < 4; ++o)
 #pragma unroll
             for (int k = 0; k < NV; ++k) store_row<0>(out, o * cols, pl.start(k), sums_of(o, k));
-        return;
-    }
-    // The teams' sums of the same columns are added up through LDS, four of a
-    // lane's columns at a time: part j of a lane's eight is added by team j % P.
-    const int threads = blockDim.x;
+    } else {
+        // The teams' sums of the same columns are added up through LDS, four of a
+        // lane's columns at a time: part j of a lane's eight is added by team j % P.
+        const int threads = blockDim.x;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const float* v = sums_of(j >> 1, 0) + 4 * (j & 1);
-        sums[(NV == 1 ? j : 0) * threads + threadIdx.x] =
-            (u32x4){as_u32(v[0]), as_u32(v[1]), as_u32(v[2]), as_u32(v[3])};
-    }
-    __syncthreads();
-    const int lane = threadIdx.x - wave0 * 64, waves = MULTI ? W * 64 : 64;
-    for (int j = team; j < 8; j += P) {
-        float v[4] = {};
-#pragma unroll 4
-        for (int q = 0; q < P; ++q) {
-            const u32x4 t = sums[j * threads + q * waves + lane];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] += as_f32(t[e]);
+        for (int j = 0; j < 8; ++j) {
+            const float* v = sums_of(j >> 1, 0) + 4 * (j & 1);
+            sums[(NV == 1 ? j : 0) * threads + threadIdx.x] =
+                (u32x4){as_u32(v[0]), as_u32(v[1]), as_u32(v[2]), as_u32(v[3])};
         }
-        *(u32x4_a4*)(out + (j >> 1) * cols + pl.start(0) + 4 * (j & 1)) =
-            (u32x4){as_u32(v[0]), as_u32(v[1]), as_u32(v[2]), as_u32(v[3])};
+        __syncthreads();
+        const int lane = threadIdx.x - wave0 * 64, waves = MULTI ? W * 64 : 64;
+        for (int j = team; j < 8; j += P) {
+            float v[4] = {};
+#pragma unroll 4
+            for (int q = 0; q < P; ++q) {
+                const u32x4 t = sums[j * threads + q * waves + lane];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] += as_f32(t[e]);
+            }
+            *(u32x4_a4*)(out + (j >> 1) * cols + pl.start(0) + 4 * (j & 1)) =
+                (u32x4){as_u32(v[0]), as_u32(v[1]), as_u32(v[2]), as_u32(v[3])};
+        }
+    }
+    if (sl.count > 1) return;
+    // the only slab: what the join kernel does
+    __syncthreads();
+    for (int c = threadIdx.x; c < cols; c += blockDim.x) {
+        float s1c = out[2 * cols + c], s2c = out[3 * cols + c];
+        if (a.dweight) a.dweight[c] = out[c];
+        if (a.dbias) a.dbias[c] = out[cols + c];
+        if (!GATE) {
+            s1c *= a.branch_scale;
+            s2c *= a.branch_scale;
+            if (a.dgate)
+                a.dgate[c] = vec1(a.post_weight, a.w_bf16, c, 1.0f) * s1c +
+                             vec1(a.post_bias, a.w_bf16, c, 0.0f) * s2c;
+            if (a.gate) {
+                const float g = load_as(a.gate, a.gate_bf16, c);
+                s1c *= g;
+                s2c *= g;
+            }
+        }
+        if (a.dpost_weight) a.dpost_weight[c] = s1c;
+        if (a.dpost_bias) a.dpost_bias[c] = s2c;
     }
 }
 
@@ -705,11 +727,13 @@ static GradShape grad_shape(int64_t cols, bool whole) {
 // As many slabs as 256 compute units hold workgroups of (12 waves to a unit, 8
 // where a row of gates comes with every row), of a few rows and more: 4 and 8
 // rows take 7.4 and 9.9 us at 256 x 1112 fp32 (32 and 64 workgroups), 20.4 and
-// 18.9 with the join at 1000 x 2048 bf16, where the partial sums count.
+// 18.9 with the join at 1000 x 2048 bf16, where the partial sums count.  Up to 4
+// rows to a team are one slab, which needs no join.
 static Slabs grad_slabs(int64_t rows, int64_t cols, int64_t gate_rows) {
     const auto slabs = [&](bool whole) {
         const GradShape sh = grad_shape(cols, whole);
         const int64_t most = sh.nv == 0 ? 256 : 256 * std::max(1, (whole ? 8 : 12) * 64 / sh.threads);
+        if (sh.nv && rows <= 4 * (sh.threads / 64 / sh.W)) return make_slabs(rows, gate_rows, 1, rows);
         return make_slabs(rows, gate_rows, most, sh.nv && sh.T ? (rows <= 512 ? 4 : 8) : 16);
     };
     const Slabs sl = slabs(false);
@@ -779,7 +803,7 @@ hipError_t launch_residual_norm_grad(const ResidualNormGrad& a, void* ws, hipStr
         a.b_bf16 ? go_dy<1, 1>(sh, a, sl, means, p, s) : go_dy<1, 0>(sh, a, sl, means, p, s);
     else
         a.b_bf16 ? go_dy<0, 1>(sh, a, sl, means, p, s) : go_dy<0, 0>(sh, a, sl, means, p, s);
-    if (sums) {
+    if (sums && (sh.nv == 0 || sl.count > 1)) {
         int64_t gates = a.dgate && sl.k ? sl.count / sl.k : 0;
         if (sl.k <= kFewParts) gates = (gates + 15) / 16;
         gates = std::min(gates, kGridY);
