@@ -685,8 +685,17 @@ fp4q_status_t fp4q_residual_norm_grad(
  *   fp32 gradient overflows; a NaN in a gradient makes both results NaN, an Inf
  *   (and no NaN) the norm Inf and the scale 0.
  *   workspace >= fp4q_grad_norm_workspace_bytes(tensors, n) device bytes,
- *   16-byte aligned.  The descriptors travel as kernel arguments (192 tensors to
- *   a launch), so a call can be captured into a graph.  Deterministic.
+ *   16-byte aligned.
+ *   table: NULL, and the descriptors travel as kernel arguments (192 tensors to
+ *   a launch); or a copy in device memory, 16-byte aligned, of what
+ *   fp4q_grad_table made of the same tensors: any number of them is one launch,
+ *   and a launch is cheaper.  Same bits either way.  Calls can be captured into
+ *   a graph.  Deterministic.
+ *
+ * fp4q_grad_table (host only, nothing launched) lays the descriptors out in HOST
+ * memory `table` (16-byte aligned, *table_bytes long; NULL to ask for the size)
+ * and sets *table_bytes to what is needed.  The table holds the tensors'
+ * addresses: it is made anew when one changes.
  */
 typedef enum { FP4Q_NORM_L2 = 0, FP4Q_NORM_MAX = 1 } fp4q_norm_order_t;
 typedef struct fp4q_tensor {
@@ -695,9 +704,11 @@ typedef struct fp4q_tensor {
     int64_t dtype; /* fp4q_dtype_t */
 } fp4q_tensor_t;
 size_t fp4q_grad_norm_workspace_bytes(const fp4q_tensor_t* tensors, int32_t n);
-fp4q_status_t fp4q_grad_norm(const fp4q_tensor_t* tensors, int32_t n, fp4q_norm_order_t order,
-                             double max_norm, double eps, float* norm, float* scale,
-                             void* workspace, size_t workspace_bytes, void* stream);
+fp4q_status_t fp4q_grad_table(const fp4q_tensor_t* tensors, int32_t n, void* table,
+                              size_t* table_bytes);
+fp4q_status_t fp4q_grad_norm(const fp4q_tensor_t* tensors, int32_t n, const void* table,
+                             fp4q_norm_order_t order, double max_norm, double eps, float* norm,
+                             float* scale, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * fp4q_grad_clip -- fp4q_grad_norm, and every element times its scale, in place,
@@ -706,8 +717,8 @@ fp4q_status_t fp4q_grad_norm(const fp4q_tensor_t* tensors, int32_t n, fp4q_norm_
  * skip.  The tensors must not overlap; the other arguments and the results, NaN
  * and Inf included, are fp4q_grad_norm's (of fp32 products: Inf times 0 is NaN).
  */
-fp4q_status_t fp4q_grad_clip(const fp4q_tensor_t* tensors, int32_t n, fp4q_norm_order_t order,
-                             double max_norm, double eps, float* norm, void* workspace,
+fp4q_status_t fp4q_grad_clip(const fp4q_tensor_t* tensors, int32_t n, const void* table,
+                             fp4q_norm_order_t order, double max_norm, double eps, float* norm, void* workspace,
                              size_t workspace_bytes, void* stream);
 
 /*
@@ -715,8 +726,8 @@ fp4q_status_t fp4q_grad_clip(const fp4q_tensor_t* tensors, int32_t n, fp4q_norm_
  * place, each rounded to its type.  Tensors as in fp4q_grad_norm; those of one
  * call must not overlap.  With *scale = 1 nothing is read or written.
  */
-fp4q_status_t fp4q_grad_scale(const fp4q_tensor_t* tensors, int32_t n, const float* scale,
-                              void* stream);
+fp4q_status_t fp4q_grad_scale(const fp4q_tensor_t* tensors, int32_t n, const void* table,
+                              const float* scale, void* stream);
 
 /*
  * fp4q_adamw_step -- one AdamW step over many tensors:

@@ -35,7 +35,7 @@ EXPORTS = ["fp4q_channel_mask", "fp4q_quantize_masked", "fp4q_gemm_hcp_split",
            "fp4q_layer_norm_grad_workspace_bytes", "fp4q_layer_norm_grad", "fp4q_adamw_step",
            "fp4q_adamw_table", "fp4q_adamw_step_table", "fp4q_residual_norm",
            "fp4q_residual_norm_grad_workspace_bytes", "fp4q_residual_norm_grad",
-           "fp4q_grad_norm_workspace_bytes", "fp4q_grad_norm", "fp4q_grad_clip",
+           "fp4q_grad_norm_workspace_bytes", "fp4q_grad_table", "fp4q_grad_norm", "fp4q_grad_clip",
            "fp4q_grad_scale",
            "fp4q_set_next_launch", "fp4q_status_string",
            "fp4q_last_error", "fp4q_abi_version"]
@@ -124,9 +124,10 @@ def lib():
                                               P, P, P, I32, I64, I64, D, D, I32, P, I32, P, P, P, P, P,
                                               I64, P, I64, P, P, P, P, P, P, SZ, P]),
             "fp4q_grad_norm_workspace_bytes": (SZ, [P, I32]),
-            "fp4q_grad_norm": (I32, [P, I32, I32, D, D, P, P, P, SZ, P]),
-            "fp4q_grad_clip": (I32, [P, I32, I32, D, D, P, P, SZ, P]),
-            "fp4q_grad_scale": (I32, [P, I32, P, P]),
+            "fp4q_grad_table": (I32, [P, I32, P, P]),
+            "fp4q_grad_norm": (I32, [P, I32, P, I32, D, D, P, P, P, SZ, P]),
+            "fp4q_grad_clip": (I32, [P, I32, P, I32, D, D, P, P, SZ, P]),
+            "fp4q_grad_scale": (I32, [P, I32, P, P, P]),
             "fp4q_set_next_launch": (I32, [P, P, _ct.c_uint32]),
             "fp4q_status_string": (_ct.c_char_p, [I32]),
             "fp4q_last_error": (_ct.c_char_p, []),
@@ -863,6 +864,11 @@ def _device_of(t, stream):
     return d
 
 
+def _stream_on(d, stream):
+    """_stream where device d is the current one."""
+    return _torch_module._C._cuda_getCurrentRawStream(d) if stream is None else stream.cuda_stream
+
+
 def _same_device(t, name, d):
     if t.get_device() != d:
         _need_cuda(t)
@@ -912,19 +918,19 @@ def _gate(gate, gate_rows, rows, cols, d):
     return _dt(gate), gate_rows, ld
 
 
-def _norm_vectors(cols, d, weight, bias, post_weight, post_bias):
-    """Dtype code of the vectors of both norms."""
+def _norm_vectors(cols, d, *vectors):
+    """Dtype code of the vectors of both norms (weight, bias, post_weight,
+    post_bias)."""
     dtype, size = None, (cols,)
-    for t, name in ((weight, "weight"), (bias, "bias"), (post_weight, "post_weight"),
-                    (post_bias, "post_bias")):
+    for t in vectors:
         if t is None:
             continue
         if dtype is None:
-            dtype = t.dtype
-            code = _dt(t)
+            dtype, code = t.dtype, _dt(t)
         elif t.dtype is not dtype:
             raise TypeError("the norms' weights and biases must have the same dtype")
         if t.shape != size or t.get_device() != d or not t.is_contiguous():
+            name = ("weight", "bias", "post_weight", "post_bias")[[v is t for v in vectors].index(True)]
             _vec_on(t, name, d, size, dtype)
     return F32 if dtype is None else code
 
@@ -946,7 +952,8 @@ def residual_norm(x, branch, weight=None, bias=None, eps=1e-5, kind=LAYER_NORM, 
     ldx = _rows(x, "x")
     R, C = size = x.shape
     d = _device_of(x, stream)
-    ldb = _rows_on(branch, "branch", d, size)
+    ldb = C if branch.shape == size and branch.get_device() == d and branch.is_contiguous() else \
+        _rows_on(branch, "branch", d, size)
     xdt = _dt(x)
     wdt = _norm_vectors(C, d, weight, bias, post_weight, post_bias)
     if gate is None:
@@ -996,7 +1003,7 @@ def residual_norm(x, branch, weight=None, bias=None, eps=1e-5, kind=LAYER_NORM, 
         R, C, x.data_ptr(), xdt, ldx, branch.data_ptr(), _dt(branch), ldb, post_kind, _ptr(post_weight),
         _ptr(post_bias), gate_at, gdt, gate_rows, ldg, x_scale, branch_scale, kind, _ptr(weight),
         _ptr(bias), wdt, eps, x_out.data_ptr(), ldxo, y_at, ydt, ldy, codes_at, scales_at, pm_at, pr_at,
-        m_at, r_at, _stream(stream))
+        m_at, r_at, _stream_on(d, stream))
     if status:
         _check(status)
     return x_out, (codes, scales) if quantize else y, (pm, pr, m, r)
@@ -1097,7 +1104,7 @@ def residual_norm_grad(dy, dx_out, x_out, branch, stats, weight=None, kind=LAYER
         _dt(dbranch), ldb, post_kind, _ptr(post_weight), _ptr(post_bias), gate_at, gdt, gate_rows, ldg,
         x_scale, branch_scale, kind, _ptr(weight), wdt, _ptr(pm), _ptr(pr), _ptr(m), _ptr(r), dx.data_ptr(),
         lddx, dbranch.data_ptr(), lddb, _ptr(dpost_weight), _ptr(dpost_bias), _ptr(dgate), _ptr(dweight),
-        _ptr(dbias), workspace.data_ptr(), nbytes, _stream(stream))
+        _ptr(dbias), workspace.data_ptr(), nbytes, _stream_on(d, stream))
     if status:
         _check(status)
     return dx, dbranch, dweight, dbias, dpost_weight, dpost_bias, dgate
@@ -1105,7 +1112,7 @@ def residual_norm_grad(dy, dx_out, x_out, branch, stats, weight=None, kind=LAYER
 
 class GradPlan:
     """The tensors of a gradient norm, checked once (see grad_plan).  Holds their
-    memory, through tensors of its own."""
+    memory, through tensors of its own, and their table in device memory."""
 
     def __init__(self, grads):
         torch = _torch()
@@ -1123,6 +1130,23 @@ class GradPlan:
                 raise ValueError("the gradients must lie on one device")
             self.array[i] = Tensor(t.data_ptr(), t.numel(), _dt(t))
         self.nbytes = lib().fp4q_grad_norm_workspace_bytes(self.array, self.n)
+        size = _ct.c_size_t(0)
+        fill = lib().fp4q_grad_table
+        _check(fill(self.array, self.n, None, _ct.byref(size)))
+        host = torch.empty(size.value + 16, dtype=torch.uint8)
+        host = host[-host.data_ptr() % 16:][:size.value]
+        _check(fill(self.array, self.n, host.data_ptr(), _ct.byref(size)))
+        self.table, self.streams = host.to(self.like.device), {_stream(None)}
+
+    def read_on(self, d, stream):
+        """The table's address, and the handle of the stream that is about to read
+        it: its memory is not to be reused before that work is done, should the
+        plan be dropped."""
+        handle = _stream_on(d, stream)
+        if handle not in self.streams:
+            self.table.record_stream(_torch().cuda.current_stream() if stream is None else stream)
+            self.streams.add(handle)
+        return self.table.data_ptr(), handle
 
 
 def grad_plan(grads):
@@ -1184,9 +1208,10 @@ def grad_norm(plan, max_norm=None, eps=1e-6, order=NORM_L2, norm=None, scale=Non
     elif scale is not None:
         raise ValueError("scale needs max_norm")
     workspace, nbytes = _norm_workspace(workspace, plan, d, empty)
-    status = (_lib or lib()).fp4q_grad_norm(plan.array, plan.n, order, 0.0 if max_norm is None else max_norm,
-                                            eps, norm.data_ptr(), _ptr(scale), workspace.data_ptr(), nbytes,
-                                            _stream(stream))
+    table, handle = plan.read_on(d, stream)
+    status = (_lib or lib()).fp4q_grad_norm(plan.array, plan.n, table, order,
+                                            0.0 if max_norm is None else max_norm, eps, norm.data_ptr(),
+                                            _ptr(scale), workspace.data_ptr(), nbytes, handle)
     if status:
         _check(status)
     return norm, scale
@@ -1200,8 +1225,10 @@ def scale_grads(plan, scale, stream=None):
     _need(scale, "scale", _torch().float32)
     if scale.numel() != 1:
         raise ValueError(f"scale must have one element, got {scale.numel()}")
-    _same_device(scale, "scale", _device_of(plan.like, stream))
-    status = (_lib or lib()).fp4q_grad_scale(plan.array, plan.n, scale.data_ptr(), _stream(stream))
+    d = _device_of(plan.like, stream)
+    _same_device(scale, "scale", d)
+    table, handle = plan.read_on(d, stream)
+    status = (_lib or lib()).fp4q_grad_scale(plan.array, plan.n, table, scale.data_ptr(), handle)
     if status:
         _check(status)
 
@@ -1215,8 +1242,9 @@ def clip_grads(plan, max_norm, eps=1e-6, order=NORM_L2, norm=None, workspace=Non
     empty = _allocator(plan.like, stream)
     norm = _scalar(norm, "norm", d, empty)
     workspace, nbytes = _norm_workspace(workspace, plan, d, empty)
-    status = (_lib or lib()).fp4q_grad_clip(plan.array, plan.n, order, max_norm, eps, norm.data_ptr(),
-                                            workspace.data_ptr(), nbytes, _stream(stream))
+    table, handle = plan.read_on(d, stream)
+    status = (_lib or lib()).fp4q_grad_clip(plan.array, plan.n, table, order, max_norm, eps,
+                                            norm.data_ptr(), workspace.data_ptr(), nbytes, handle)
     if status:
         _check(status)
     return norm

@@ -150,7 +150,7 @@ fp4q_status_t grad_tensors(const char* who, const fp4q_tensor_t* tensors, int32_
 
 // Arguments that the gradient norm and the clipping share.
 fp4q_status_t grad_norm_args(const char* who, const fp4q_tensor_t* tensors, int32_t n,
-                             fp4q_norm_order_t order, double max_norm, double eps, const float* norm,
+                             const void* table, fp4q_norm_order_t order, double max_norm, double eps, const float* norm,
                              const float* scale, const void* workspace, size_t workspace_bytes) {
     if (order != FP4Q_NORM_L2 && order != FP4Q_NORM_MAX)
         return fail(FP4Q_ERR_INVALID, "%s: bad order %d", who, (int)order);
@@ -160,6 +160,8 @@ fp4q_status_t grad_norm_args(const char* who, const fp4q_tensor_t* tensors, int3
     if (e != FP4Q_OK) return e;
     if (((uintptr_t)norm % 4) || ((uintptr_t)scale % 4))
         return fail(FP4Q_ERR_ALIGNMENT, "%s: pointers must be element-aligned", who);
+    if (!aligned16(table))
+        return fail(FP4Q_ERR_ALIGNMENT, "%s: table must be 16-byte aligned", who);
     const size_t need = fp4q::grad_norm_workspace_bytes(tensors, n);
     if (!workspace) return fail(FP4Q_ERR_INVALID, "%s: null workspace", who);
     if (!aligned16(workspace))
@@ -1015,37 +1017,55 @@ size_t fp4q_grad_norm_workspace_bytes(const fp4q_tensor_t* tensors, int32_t n) {
     return fp4q::grad_norm_workspace_bytes(tensors, n);
 }
 
-fp4q_status_t fp4q_grad_norm(const fp4q_tensor_t* tensors, int32_t n, fp4q_norm_order_t order,
+fp4q_status_t fp4q_grad_table(const fp4q_tensor_t* tensors, int32_t n, void* table,
+                              size_t* table_bytes) {
+    if (!table_bytes) return fail(FP4Q_ERR_INVALID, "grad_table: null pointer");
+    const fp4q_status_t e = grad_tensors("grad_table", tensors, n);
+    if (e != FP4Q_OK) return e;
+    const size_t need = fp4q::grad_table_bytes(tensors, n), have = *table_bytes;
+    *table_bytes = need;
+    if (!table) return FP4Q_OK;
+    if (!aligned16(table))
+        return fail(FP4Q_ERR_ALIGNMENT, "grad_table: table must be 16-byte aligned");
+    if (have < need) return fail(FP4Q_ERR_WORKSPACE, "grad_table: table %zu < %zu bytes", have, need);
+    fp4q::grad_table(tensors, n, table);
+    return FP4Q_OK;
+}
+
+fp4q_status_t fp4q_grad_norm(const fp4q_tensor_t* tensors, int32_t n, const void* table,
+                             fp4q_norm_order_t order,
                              double max_norm, double eps, float* norm, float* scale,
                              void* workspace, size_t workspace_bytes, void* stream) {
     if (!norm && !scale) return fail(FP4Q_ERR_INVALID, "grad_norm: null pointer");
-    const fp4q_status_t e = grad_norm_args("grad_norm", tensors, n, order, max_norm, eps, norm, scale,
+    const fp4q_status_t e = grad_norm_args("grad_norm", tensors, n, table, order, max_norm, eps, norm, scale,
                                            workspace, workspace_bytes);
     if (e != FP4Q_OK) return e;
-    return hip_status(fp4q::launch_grad_norm(tensors, n, order == FP4Q_NORM_MAX, max_norm, eps, norm,
+    return hip_status(fp4q::launch_grad_norm(tensors, n, table, order == FP4Q_NORM_MAX, max_norm, eps, norm,
                                              scale, workspace, (hipStream_t)stream),
                       "grad_norm launch");
 }
 
-fp4q_status_t fp4q_grad_clip(const fp4q_tensor_t* tensors, int32_t n, fp4q_norm_order_t order,
-                             double max_norm, double eps, float* norm, void* workspace,
+fp4q_status_t fp4q_grad_clip(const fp4q_tensor_t* tensors, int32_t n, const void* table,
+                             fp4q_norm_order_t order, double max_norm, double eps, float* norm, void* workspace,
                              size_t workspace_bytes, void* stream) {
-    const fp4q_status_t e = grad_norm_args("grad_clip", tensors, n, order, max_norm, eps, norm, nullptr,
+    const fp4q_status_t e = grad_norm_args("grad_clip", tensors, n, table, order, max_norm, eps, norm, nullptr,
                                            workspace, workspace_bytes);
     if (e != FP4Q_OK) return e;
-    return hip_status(fp4q::launch_grad_clip(tensors, n, order == FP4Q_NORM_MAX, max_norm, eps, norm,
+    return hip_status(fp4q::launch_grad_clip(tensors, n, table, order == FP4Q_NORM_MAX, max_norm, eps, norm,
                                              workspace, (hipStream_t)stream),
                       "grad_clip launch");
 }
 
-fp4q_status_t fp4q_grad_scale(const fp4q_tensor_t* tensors, int32_t n, const float* scale,
-                              void* stream) {
+fp4q_status_t fp4q_grad_scale(const fp4q_tensor_t* tensors, int32_t n, const void* table,
+                              const float* scale, void* stream) {
     const fp4q_status_t e = grad_tensors("grad_scale", tensors, n);
     if (e != FP4Q_OK) return e;
     if (!scale) return fail(FP4Q_ERR_INVALID, "grad_scale: null pointer");
     if ((uintptr_t)scale % 4)
         return fail(FP4Q_ERR_ALIGNMENT, "grad_scale: pointers must be element-aligned");
-    return hip_status(fp4q::launch_grad_scale(tensors, n, scale, (hipStream_t)stream),
+    if (!aligned16(table))
+        return fail(FP4Q_ERR_ALIGNMENT, "grad_scale: table must be 16-byte aligned");
+    return hip_status(fp4q::launch_grad_scale(tensors, n, table, scale, (hipStream_t)stream),
                       "grad_scale launch");
 }
 

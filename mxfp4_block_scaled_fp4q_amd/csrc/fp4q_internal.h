@@ -176,13 +176,18 @@ hipError_t launch_norm_grad(const void* dy, int dydtype, int64_t lddy, const voi
                             const float* mean, const float* rstd, bool rms, void* dx, int64_t lddx,
                             float* dw, float* db, void* ws, hipStream_t s);
 // Norm of many tensors taken as one vector, with the factor that clips it to
-// max_norm, and the product of the tensors with such a factor.
+// max_norm, and the product of the tensors with such a factor.  table: the
+// tensors in device memory as grad_table lays them out, or null.
+size_t grad_table_bytes(const fp4q_tensor* t, int n);
+void grad_table(const fp4q_tensor* t, int n, void* table);
 size_t grad_norm_workspace_bytes(const fp4q_tensor* t, int n);
-hipError_t launch_grad_norm(const fp4q_tensor* t, int n, bool largest, double max_norm, double eps,
-                            float* norm, float* scale, void* ws, hipStream_t s);
-hipError_t launch_grad_clip(const fp4q_tensor* t, int n, bool largest, double max_norm, double eps,
-                            float* norm, void* ws, hipStream_t s);
-hipError_t launch_grad_scale(const fp4q_tensor* t, int n, const float* scale, hipStream_t s);
+hipError_t launch_grad_norm(const fp4q_tensor* t, int n, const void* table, bool largest,
+                            double max_norm, double eps, float* norm, float* scale, void* ws,
+                            hipStream_t s);
+hipError_t launch_grad_clip(const fp4q_tensor* t, int n, const void* table, bool largest,
+                            double max_norm, double eps, float* norm, void* ws, hipStream_t s);
+hipError_t launch_grad_scale(const fp4q_tensor* t, int n, const void* table, const float* scale,
+                             hipStream_t s);
 hipError_t launch_adamw(const fp4q_adamw_tensor* t, int n, int bits, int gdtype, double lr,
                         double beta1, double beta2, double eps, int64_t step, uint64_t seed,
                         const float* grad_scale, hipStream_t s);

@@ -9,6 +9,7 @@
 // rounded to fp32 (off by at most one step), whatever the order of the sum.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "../../include/libfp4q.h"
 #include "fp4q_device.h"
@@ -25,44 +26,62 @@ __device__ __forceinline__ Global<T> global(const void* p) {
     return (Global<T>)p;
 }
 
-constexpr int kTensors = 192;            // descriptors per launch: 4 KB of kernel arguments
 constexpr int64_t kChunk = 16384;        // elements per workgroup
 constexpr int64_t kMaxGroups = 1 << 22;  // workgroups per launch: 2^30 threads
 
+// Where a launch's tensors stand: in the kernel arguments, up to N of them, or in
+// device memory, with the tensor of every chunk (40, 150, 300 and 1000 tensors of
+// up to 9000 elements: 8.6, 8.9, 13.5 and 32 us a norm against 7.4, 7.5, 7.6 and
+// 8.5).
+constexpr int64_t kBf16Bit = (int64_t)1 << 62;  // in a number of elements: they are bf16
+template <int N>
 struct Tensors {
-    void* p[kTensors];
-    int64_t n[kTensors];        // elements; the top bit: bf16
-    uint32_t first[kTensors];   // first workgroup
+    void* p[N];
+    int64_t n[N];
+    uint32_t first[N];  // first workgroup
     int count;
 };
-static_assert(sizeof(Tensors) <= 4096 - 64, "kernel arguments");
-constexpr int64_t kBf16Bit = (int64_t)1 << 62;
+constexpr int kFew = 64, kMany = 192;
+static_assert(sizeof(Tensors<kMany>) <= 4096 - 64, "kernel arguments");
+struct Desc {
+    void* p;
+    int64_t n;
+    uint64_t first;
+};
+struct Table {
+    const Desc* d;
+    const uint32_t* owner;
+    uint32_t group0;  // of the launch's first workgroup
+};
 
-// The workgroup's tensor (the last that starts at or before it, found by all
-// lanes at once) and its elements [i0, i1).
+// A workgroup's (or wave's) part of a tensor: elements [i0, i1).
 struct Piece {
     void* p;
     int64_t i0, i1;
     bool bf16;
 };
-template <int64_t CHUNK>
-__device__ __forceinline__ Piece piece_of(const Tensors& t, uint32_t group) {
+__device__ __forceinline__ Piece make_piece(void* p, int64_t n, int64_t i0, int64_t chunk) {
+    return {p, i0, min(i0 + chunk, n & ~kBf16Bit), (n & kBf16Bit) != 0};
+}
+// The tensor of `group`: the last that starts at or before it, found by all lanes
+// at once.
+template <int64_t CHUNK, int N>
+__device__ __forceinline__ Piece piece_of(const Tensors<N>& t, uint32_t group) {
     const int l = threadIdx.x & 63;
-    int k = 0;
+    int k = -1;
 #pragma unroll
-    for (int j = 0; j < kTensors; j += 64) {
+    for (int j = 0; j < N; j += 64) {
         const int i = j + l;
         const bool below = i < t.count && (i == 0 || t.first[i] <= group);
         k += __popcll(__ballot(below));
     }
-    k -= 1;
-    Piece q;
-    const int64_t n = t.n[k];
-    q.p = t.p[k];
-    q.bf16 = (n & kBf16Bit) != 0;
-    q.i0 = (int64_t)(group - t.first[k]) * CHUNK;
-    q.i1 = min(q.i0 + CHUNK, n & ~kBf16Bit);
-    return q;
+    return make_piece(t.p[k], t.n[k], (int64_t)(group - t.first[k]) * CHUNK, CHUNK);
+}
+template <int64_t CHUNK>
+__device__ __forceinline__ Piece piece_of(const Table& t, uint32_t group) {
+    group += t.group0;
+    const Desc d = t.d[t.owner[group]];
+    return make_piece(d.p, d.n, (int64_t)(group - (uint32_t)d.first) * CHUNK, CHUNK);
 }
 // 16 bytes of a gradient at any element, and its values.
 template <int B16>
@@ -165,8 +184,8 @@ __device__ __forceinline__ double value_of(const Total<MAX>& t) {
     return MAX ? (double)t.top : (t.s[0] + t.s[1]) + (t.s[2] + t.s[3]);
 }
 
-template <int MAX>
-__global__ __launch_bounds__(kThreads) void grad_norm_kernel(const Tensors t, double* __restrict__ part) {
+template <int MAX, class SOURCE>
+__global__ __launch_bounds__(kThreads) void grad_norm_kernel(const SOURCE t, double* __restrict__ part) {
     __shared__ double red[kThreads / 64];
     const Piece q = piece_of<kChunk>(t, blockIdx.x);
     Total<MAX> t0;
@@ -235,7 +254,8 @@ __device__ __forceinline__ void scale_piece(const Piece& q, float f) {
                 global<float>(q.p)[i] = g;
         });
 }
-__global__ __launch_bounds__(kThreads) void grad_scale_kernel(const Tensors t,
+template <class SOURCE>
+__global__ __launch_bounds__(kThreads) void grad_scale_kernel(const SOURCE t,
                                                               const float* __restrict__ scale) {
     const float f = *scale;
     if (f == 1.0f) return;
@@ -247,8 +267,8 @@ __global__ __launch_bounds__(kThreads) void grad_scale_kernel(const Tensors t,
 // every workgroup adds them up, in the join kernel's order, which costs a launch
 // less (40 tensors of up to 5000 elements 16.5 -> 12.8 us a call).
 constexpr int kFewParts = 1024;
-template <int MAX>
-__global__ __launch_bounds__(kThreads) void grad_clip_kernel(const Tensors t,
+template <int MAX, class SOURCE>
+__global__ __launch_bounds__(kThreads) void grad_clip_kernel(const SOURCE t,
                                                              const double* __restrict__ part, int n,
                                                              const Clip c) {
     __shared__ double red[16];
@@ -286,7 +306,8 @@ __global__ __launch_bounds__(kThreads) void grad_clip_kernel(const Tensors t,
 // that both make the same norm).
 constexpr int64_t kSmallChunk = 1024, kSmallPieces = 64;
 template <int MAX, int CLIP>
-__global__ __launch_bounds__(1024) void grad_small_kernel(const Tensors t, int pieces, const Clip c) {
+__global__ __launch_bounds__(1024) void grad_small_kernel(const Tensors<kFew> t, int pieces,
+                                                          const Clip c) {
     __shared__ double red[16];
     __shared__ float factor;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -317,14 +338,14 @@ static bool is_small(const fp4q_tensor_t* t, int n) {
 }
 
 // Calls launch(tensors, groups, groups of earlier launches) until all are done.
-template <class F>
-static hipError_t for_tensors(const fp4q_tensor_t* t, int n, F launch, int64_t chunk = kChunk) {
-    Tensors a;
+template <int N, class F>
+static hipError_t for_args(const fp4q_tensor_t* t, int n, F launch, int64_t chunk = kChunk) {
+    Tensors<N> a;
     int64_t done = 0, before = 0;  // chunks of tensor i that earlier launches took; of all
     for (int i = 0; i < n;) {
         int64_t groups = 0;
         a.count = 0;
-        while (i < n && a.count < kTensors && groups < kMaxGroups) {
+        while (i < n && a.count < N && groups < kMaxGroups) {
             const int64_t left = groups_of(t[i], chunk) - done;
             if (left > 0) {
                 const int64_t take = std::min(left, kMaxGroups - groups);
@@ -348,22 +369,52 @@ static hipError_t for_tensors(const fp4q_tensor_t* t, int n, F launch, int64_t c
     }
     return hipSuccess;
 }
-
-size_t grad_norm_workspace_bytes(const fp4q_tensor_t* t, int n) {
+static int64_t all_groups(const fp4q_tensor_t* t, int n) {
     int64_t groups = 0;
     for (int i = 0; i < n; ++i) groups += groups_of(t[i]);
-    return (size_t)(groups + 2) * sizeof(double);  // a factor, and partial sums
+    return groups;
+}
+template <class F>
+static hipError_t for_tensors(const fp4q_tensor_t* t, int n, const void* table, F launch) {
+    if (!table) return n <= kFew ? for_args<kFew>(t, n, launch) : for_args<kMany>(t, n, launch);
+    const int64_t groups = all_groups(t, n);
+    for (int64_t g = 0; g < groups; g += kMaxGroups) {
+        const Table a = {(const Desc*)table, (const uint32_t*)((const Desc*)table + n), (uint32_t)g};
+        launch(a, std::min(groups - g, kMaxGroups), g);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+size_t grad_table_bytes(const fp4q_tensor_t* t, int n) {
+    return (size_t)n * sizeof(Desc) + (size_t)all_groups(t, n) * 4;
+}
+void grad_table(const fp4q_tensor_t* t, int n, void* table) {
+    Desc* d = (Desc*)table;
+    uint32_t* owner = (uint32_t*)(d + n);
+    uint64_t groups = 0;
+    for (int i = 0; i < n; ++i) {
+        d[i] = {t[i].data, t[i].numel | (t[i].dtype == FP4Q_BF16 ? kBf16Bit : 0), groups};
+        for (int64_t k = groups_of(t[i]); k > 0; --k) owner[groups++] = (uint32_t)i;
+    }
+}
+
+size_t grad_norm_workspace_bytes(const fp4q_tensor_t* t, int n) {
+    return (size_t)(all_groups(t, n) + 2) * sizeof(double);  // a factor, and partial sums
 }
 
 // Partial sums of all tensors; their number in *groups.
-static hipError_t launch_parts(const fp4q_tensor_t* t, int n, bool largest, double* part,
-                               int64_t* groups, hipStream_t s) {
+static hipError_t launch_parts(const fp4q_tensor_t* t, int n, const void* table, bool largest,
+                               double* part, int64_t* groups, hipStream_t s) {
     *groups = 0;
-    return for_tensors(t, n, [&](const Tensors& a, int64_t now, int64_t before) {
+    return for_tensors(t, n, table, [&](const auto& a, int64_t now, int64_t before) {
+        using S = std::decay_t<decltype(a)>;
+        const dim3 grid((unsigned)now), block(kThreads);
         if (largest)
-            FP4Q_LAUNCH(grad_norm_kernel<1>, dim3((unsigned)now), dim3(kThreads), 0, s, a, part + before);
+            FP4Q_LAUNCH((grad_norm_kernel<1, S>), grid, block, 0, s, a, part + before);
         else
-            FP4Q_LAUNCH(grad_norm_kernel<0>, dim3((unsigned)now), dim3(kThreads), 0, s, a, part + before);
+            FP4Q_LAUNCH((grad_norm_kernel<0, S>), grid, block, 0, s, a, part + before);
         *groups = before + now;
     });
 }
@@ -379,7 +430,7 @@ static hipError_t launch_join(const double* part, int64_t groups, bool largest, 
 static hipError_t launch_small(const fp4q_tensor_t* t, int n, bool largest, bool clip, const Clip& c,
                                hipStream_t s) {
     bool done = false;
-    const auto go = [&](const Tensors& a, int64_t now, int64_t) {
+    const auto go = [&](const Tensors<kFew>& a, int64_t now, int64_t) {
         done = true;
         if (largest && clip)
             FP4Q_LAUNCH((grad_small_kernel<1, 1>), dim3(1), dim3(1024), 0, s, a, (int)now, c);
@@ -390,47 +441,51 @@ static hipError_t launch_small(const fp4q_tensor_t* t, int n, bool largest, bool
         else
             FP4Q_LAUNCH((grad_small_kernel<0, 0>), dim3(1), dim3(1024), 0, s, a, (int)now, c);
     };
-    const hipError_t e = for_tensors(t, n, go, kSmallChunk);
+    static_assert(kSmallPieces <= kFew, "each piece may be a tensor");
+    const hipError_t e = for_args<kFew>(t, n, go, kSmallChunk);
     return e != hipSuccess || done ? e : launch_join(nullptr, 0, largest, c, s);  // nothing: norm 0
 }
 
-hipError_t launch_grad_norm(const fp4q_tensor_t* t, int n, bool largest, double max_norm, double eps,
-                            float* norm, float* scale, void* ws, hipStream_t s) {
+hipError_t launch_grad_norm(const fp4q_tensor_t* t, int n, const void* table, bool largest,
+                            double max_norm, double eps, float* norm, float* scale, void* ws,
+                            hipStream_t s) {
     const Clip c = {max_norm, eps, norm, scale};
     if (is_small(t, n)) return launch_small(t, n, largest, false, c, s);
     int64_t groups;
-    const hipError_t e = launch_parts(t, n, largest, (double*)ws, &groups, s);
+    const hipError_t e = launch_parts(t, n, table, largest, (double*)ws, &groups, s);
     return e != hipSuccess ? e : launch_join((double*)ws, groups, largest, c, s);
 }
 
-hipError_t launch_grad_clip(const fp4q_tensor_t* t, int n, bool largest, double max_norm, double eps,
-                            float* norm, void* ws, hipStream_t s) {
+hipError_t launch_grad_scale(const fp4q_tensor_t* t, int n, const void* table, const float* scale,
+                             hipStream_t s) {
+    return for_tensors(t, n, table, [&](const auto& a, int64_t now, int64_t) {
+        using S = std::decay_t<decltype(a)>;
+        FP4Q_LAUNCH(grad_scale_kernel<S>, dim3((unsigned)now), dim3(kThreads), 0, s, a, scale);
+    });
+}
+
+hipError_t launch_grad_clip(const fp4q_tensor_t* t, int n, const void* table, bool largest,
+                            double max_norm, double eps, float* norm, void* ws, hipStream_t s) {
     if (is_small(t, n))
         return launch_small(t, n, largest, true, {max_norm, eps, norm, nullptr}, s);
     double* part = (double*)ws + 2;  // behind the factor
     float* scale = (float*)ws;
     int64_t groups;
-    hipError_t e = launch_parts(t, n, largest, part, &groups, s);
+    hipError_t e = launch_parts(t, n, table, largest, part, &groups, s);
     if (e != hipSuccess) return e;
     if (groups > kFewParts) {
         e = launch_join(part, groups, largest, {max_norm, eps, norm, scale}, s);
-        return e != hipSuccess ? e : launch_grad_scale(t, n, scale, s);
+        return e != hipSuccess ? e : launch_grad_scale(t, n, table, scale, s);
     }
     // (only the first launch writes the norm)
-    return for_tensors(t, n, [&](const Tensors& a, int64_t now, int64_t before) {
+    return for_tensors(t, n, table, [&](const auto& a, int64_t now, int64_t before) {
+        using S = std::decay_t<decltype(a)>;
+        const dim3 grid((unsigned)now), block(kThreads);
         const Clip c = {max_norm, eps, before ? nullptr : norm, nullptr};
         if (largest)
-            FP4Q_LAUNCH(grad_clip_kernel<1>, dim3((unsigned)now), dim3(kThreads), 0, s, a, part,
-                        (int)groups, c);
+            FP4Q_LAUNCH((grad_clip_kernel<1, S>), grid, block, 0, s, a, part, (int)groups, c);
         else
-            FP4Q_LAUNCH(grad_clip_kernel<0>, dim3((unsigned)now), dim3(kThreads), 0, s, a, part,
-                        (int)groups, c);
-    });
-}
-
-hipError_t launch_grad_scale(const fp4q_tensor_t* t, int n, const float* scale, hipStream_t s) {
-    return for_tensors(t, n, [&](const Tensors& a, int64_t now, int64_t) {
-        FP4Q_LAUNCH(grad_scale_kernel, dim3((unsigned)now), dim3(kThreads), 0, s, a, scale);
+            FP4Q_LAUNCH((grad_clip_kernel<0, S>), grid, block, 0, s, a, part, (int)groups, c);
     });
 }
 

@@ -87,12 +87,12 @@ def grads(*t):
     ((FAKE, 10, 0), dict(order=2), 1), ((FAKE, 10, 0), dict(max_norm=-1.0), 1), ((FAKE, 10, 0), dict(max_norm=NAN), 1),
     ((FAKE, 10, 0), dict(max_norm=INF), 1), ((FAKE, 10, 0), dict(eps=-1.0), 1), ((FAKE, 10, 0), dict(eps=NAN), 1),
     ((FAKE, 10, 0), dict(n=-1), 1), ((FAKE, 10, 0), dict(norm=NUL, scale=NUL), 1), ((FAKE, 10, 0), dict(ws=NUL), 1),
-    ((FAKE, 10, 0), dict(ws=FAKE + 8), 3), ((FAKE, 10, 0), dict(nb=8), 4), ((FAKE, 10, 0), dict(norm=FAKE + 2), 3),
+    ((FAKE, 10, 0), dict(ws=FAKE + 8), 3), ((FAKE, 10, 0), dict(nb=8), 4), ((FAKE, 10, 0), dict(table=FAKE + 8), 3), ((FAKE, 10, 0), dict(norm=FAKE + 2), 3),
     ((FAKE, 10, 0), dict(scale=FAKE + 1), 3), ((NUL, 10, 0), {}, 1), ((FAKE, -1, 0), {}, 1),
     ((FAKE, 1 << 40, 0), {}, 1), ((FAKE, 10, 2), {}, 1), ((FAKE + 2, 10, 0), {}, 3), ((FAKE + 1, 10, 1), {}, 3),
 ])
 def test_grad_norm_refusals(L, t, kw, status):
-    a = dict(n=2, order=0, max_norm=1.0, eps=1e-6, norm=FAKE, scale=FAKE, ws=FAKE, nb=1 << 30)
+    a = dict(n=2, table=NUL, order=0, max_norm=1.0, eps=1e-6, norm=FAKE, scale=FAKE, ws=FAKE, nb=1 << 30)
     a.update(kw)
     two = grads((NUL, 0, 0), t)
     assert L.fp4q_grad_norm(two, *a.values(), NUL) == status
@@ -104,19 +104,47 @@ def test_grad_norm_refusals(L, t, kw, status):
 
 
 def test_grad_scale_refusals_and_empty_calls(L):
-    assert L.fp4q_grad_scale(grads((FAKE, 10, 0)), 1, NUL, NUL) == 1
-    assert L.fp4q_grad_scale(grads((FAKE, 10, 0)), 1, FAKE + 2, NUL) == 3
-    assert L.fp4q_grad_scale(grads((NUL, 10, 0)), 1, FAKE, NUL) == 1
-    assert L.fp4q_grad_scale(NUL, 1, FAKE, NUL) == 1 and L.fp4q_grad_scale(NUL, -1, FAKE, NUL) == 1
+    one = grads((FAKE, 10, 0))
+    assert L.fp4q_grad_scale(one, 1, NUL, NUL, NUL) == 1
+    assert L.fp4q_grad_scale(one, 1, NUL, FAKE + 2, NUL) == 3
+    assert L.fp4q_grad_scale(one, 1, FAKE + 4, FAKE, NUL) == 3
+    assert L.fp4q_grad_scale(grads((NUL, 10, 0)), 1, NUL, FAKE, NUL) == 1
+    assert L.fp4q_grad_scale(NUL, 1, NUL, FAKE, NUL) == 1 and L.fp4q_grad_scale(NUL, -1, NUL, FAKE, NUL) == 1
     assert "grad_scale" in L.fp4q_last_error().decode()
     # nothing to do launches nothing
-    assert L.fp4q_grad_scale(NUL, 0, FAKE, NUL) == 0
-    assert L.fp4q_grad_scale(grads(*[(NUL, 0, 1)] * 300), 300, FAKE, NUL) == 0
+    assert L.fp4q_grad_scale(NUL, 0, NUL, FAKE, NUL) == 0
+    assert L.fp4q_grad_scale(grads(*[(NUL, 0, 1)] * 300), 300, NUL, FAKE, NUL) == 0
+    assert L.fp4q_grad_scale(grads(*[(NUL, 0, 1)] * 300), 300, FAKE, FAKE, NUL) == 0
     too_many = grads(*[(FAKE, (1 << 40) - 1, 0)] * 17)
-    assert L.fp4q_grad_norm(too_many, 17, 0, 1.0, 0.0, FAKE, FAKE, FAKE, 1 << 60, NUL) == 2
+    assert L.fp4q_grad_norm(too_many, 17, NUL, 0, 1.0, 0.0, FAKE, FAKE, FAKE, 1 << 60, NUL) == 2
     assert L.fp4q_grad_norm_workspace_bytes(too_many, 17) == 0
     assert L.fp4q_grad_norm_workspace_bytes(NUL, 0) > 0
     assert ct.sizeof(fq.Tensor) == 24
+
+
+def table(L, t, buf=NUL, nbytes=0, n=None):
+    size = ct.c_size_t(nbytes)
+    return L.fp4q_grad_table(grads(*t), len(t) if n is None else n, buf, ct.byref(size)), size.value
+
+
+def test_grad_table(L):
+    assert table(L, [(FAKE, 1, 0), (NUL, 5, 0)])[0] == 1 and table(L, [(FAKE, 1, 0)], n=-1)[0] == 1
+    assert table(L, [(FAKE + 2, 1, 0)])[0] == 3 and table(L, [(FAKE, 1, 3)])[0] == 1
+    assert L.fp4q_grad_table(grads((FAKE, 1, 0)), 1, NUL, NUL) == 1
+    assert table(L, [(FAKE, (1 << 40) - 1, 0)] * 16)[0] == 0
+    assert table(L, [(FAKE, (1 << 40) - 1, 0)] * 17)[0] == 2
+    same = [(FAKE, 16384, 0), (NUL, 0, 0), (FAKE + 2, 16385, 1), (FAKE, 1, 1)]
+    status, size = table(L, same)
+    assert status == 0 and size == 4 * 24 + 4 * 4
+    buf = (ct.c_uint8 * (size + 32))()
+    at = (ct.addressof(buf) + 15) // 16 * 16
+    assert table(L, same, at, size - 1)[0] == 4 and table(L, same, at + 8, size)[0] == 3
+    assert table(L, same, at, size) == (0, size)
+    words = ct.cast(at, ct.POINTER(ct.c_uint64))
+    assert [words[i] for i in range(12)] == [FAKE, 16384, 0, 0, 0, 1, FAKE + 2, 16385 | 1 << 62, 1, FAKE,
+                                             1 | 1 << 62, 3]
+    owners = ct.cast(at + 96, ct.POINTER(ct.c_uint32))
+    assert [owners[i] for i in range(4)] == [0, 2, 2, 3]  # the tensor of every 16384 elements
 
 
 def test_bindings_refuse_host_tensors():
@@ -181,7 +209,7 @@ def test_bindings_check_shapes_types_and_devices(there):
     there_plan.like.at = 1
     with pytest.raises(ValueError, match="current device"):
         fq.grad_norm(there_plan, 1.0)
-    assert all(name.endswith("_bytes") for name, _ in fq._lib.calls)
+    assert all(name.endswith(("_bytes", "_table")) for name, _ in fq._lib.calls)
 
 
 def test_grad_plan_checks(there):
@@ -212,6 +240,8 @@ def test_grad_plan_checks(there):
 def test_what_a_call_allocates_belongs_to_its_stream(there):
     x, s, wide = rows(), dev(torch.zeros(4)), rows(4, 32)
     p = fq.grad_plan([x])
+    p.table = u8(64)
+    p.table.recorded = set()
     for call, made in ((lambda **kw: fq.residual_norm(x, x, post_kind=fq.LAYER_NORM, **kw), 6),
                        (lambda **kw: fq.residual_norm(wide, wide, quantize=True, kind=fq.RMS_NORM, **kw), 4),
                        (lambda **kw: fq.residual_norm_grad(x, x, x, x, (None, None, s, s), gate=s.new_zeros(8), **kw), 6),
@@ -224,3 +254,5 @@ def test_what_a_call_allocates_belongs_to_its_stream(there):
         MADE.clear()
         call()
         assert len(MADE) == made and all(t.owner == "main" and not t.recorded for t in MADE)
+    # the plan's table is read on both, and made on the first
+    assert p.table.recorded == {"side"}

@@ -141,6 +141,30 @@ def test_clipping_non_finite():
     assert fq.clip_grads(fq.grad_plan([g]), 1.0).isnan() and g.isnan().all()
 
 
+@pytest.mark.parametrize("sizes", [[16385, 3, 40000] * 20, [700] * 300, [70000]], ids=len)
+def test_arguments_and_table_give_the_same_bits(sizes):
+    """The C calls without a table, whose descriptors are kernel arguments."""
+    g = make(sizes, 8)
+    plan = fq.grad_plan(g)
+    norm, scale = fq.grad_norm(plan, 0.01)
+    a, b = torch.zeros(2, device="cuda").split(1)
+    ws = torch.empty(plan.nbytes, dtype=torch.uint8, device="cuda")
+    for order in ORDERS:
+        want = fq.grad_norm(plan, 0.01, order=order)
+        assert fq.lib().fp4q_grad_norm(plan.array, plan.n, None, order, 0.01, 1e-6, a.data_ptr(), b.data_ptr(),
+                                       ws.data_ptr(), plan.nbytes, None) == 0
+        assert torch.equal(a[0], want[0]) and torch.equal(b[0], want[1])
+    old = [t.clone() for t in g]
+    assert fq.lib().fp4q_grad_clip(plan.array, plan.n, None, 0, 0.01, 1e-6, a.data_ptr(), ws.data_ptr(), plan.nbytes,
+                                   None) == 0
+    assert torch.equal(a[0], norm)
+    assert all(torch.equal(t, (o.float() * scale).to(t.dtype)) for t, o in zip(g, old))
+    for t, o in zip(g, old):
+        t.copy_(o)
+    assert fq.lib().fp4q_grad_scale(plan.array, plan.n, None, scale.data_ptr(), None) == 0
+    assert all(torch.equal(t, (o.float() * scale).to(t.dtype)) for t, o in zip(g, old))
+
+
 def test_with_the_adamw_step():
     """grad_norm of an AdamW plan, its scale in the step: what a step over
     gradients clipped by hand gives."""
