@@ -1130,19 +1130,24 @@ class GradPlan:
                 raise ValueError("the gradients must lie on one device")
             self.array[i] = Tensor(t.data_ptr(), t.numel(), _dt(t))
         self.nbytes = lib().fp4q_grad_norm_workspace_bytes(self.array, self.n)
+        self.table, self.streams = None, {_stream(None)}
+        if torch.cuda.is_current_stream_capturing():
+            return  # no copies here: the descriptors travel as kernel arguments
         size = _ct.c_size_t(0)
         fill = lib().fp4q_grad_table
         _check(fill(self.array, self.n, None, _ct.byref(size)))
         host = torch.empty(size.value + 16, dtype=torch.uint8)
         host = host[-host.data_ptr() % 16:][:size.value]
         _check(fill(self.array, self.n, host.data_ptr(), _ct.byref(size)))
-        self.table, self.streams = host.to(self.like.device), {_stream(None)}
+        self.table = host.to(self.like.device)
 
     def read_on(self, d, stream):
         """The table's address, and the handle of the stream that is about to read
         it: its memory is not to be reused before that work is done, should the
         plan be dropped."""
         handle = _stream_on(d, stream)
+        if self.table is None:
+            return None, handle
         if handle not in self.streams:
             self.table.record_stream(_torch().cuda.current_stream() if stream is None else stream)
             self.streams.add(handle)

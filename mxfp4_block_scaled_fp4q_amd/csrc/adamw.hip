@@ -46,15 +46,6 @@
 
 namespace fp4q {
 
-// Pointers that come from memory are generic to the compiler, and generic
-// accesses wait on the LDS counter too: global<T>(p) is p in global memory.
-template <class T>
-using Global = T __attribute__((address_space(1))) *;
-template <class T>
-__device__ __forceinline__ Global<T> global(const void* p) {
-    return (Global<T>)p;
-}
-
 constexpr int kTensors = 44;     // descriptors per launch: 4 KB of kernel arguments
 constexpr int kChunk = 4096;     // elements per workgroup
 // Threads of a workgroup.  With 8-bit moments a lane has one set of 8 elements

@@ -22,6 +22,15 @@ typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
 typedef u32x4 u32x4_a4 __attribute__((aligned(4)));
 
+// Pointers that come from memory are generic to the compiler, and generic
+// accesses wait on the LDS counter too: global<T>(p) is p in global memory.
+template <class T>
+using Global = T __attribute__((address_space(1))) *;
+template <class T>
+__device__ __forceinline__ Global<T> global(const void* p) {
+    return (Global<T>)p;
+}
+
 __device__ __forceinline__ float as_f32(uint32_t u) { return __uint_as_float(u); }
 __device__ __forceinline__ uint32_t as_u32(float f) { return __float_as_uint(f); }
 

@@ -17,15 +17,6 @@
 
 namespace fp4q {
 
-// Pointers that come from memory are generic to the compiler, and generic
-// accesses wait on the LDS counter too: global<T>(p) is p in global memory.
-template <class T>
-using Global = T __attribute__((address_space(1))) *;
-template <class T>
-__device__ __forceinline__ Global<T> global(const void* p) {
-    return (Global<T>)p;
-}
-
 constexpr int64_t kChunk = 16384;        // elements per workgroup
 constexpr int64_t kMaxGroups = 1 << 22;  // workgroups per launch: 2^30 threads
 

@@ -162,6 +162,7 @@ def test_bindings_refuse_host_tensors():
 @pytest.fixture
 def there(world, monkeypatch):  # noqa: F811
     monkeypatch.setattr(Dev, "get_device", lambda self: getattr(self, "at", 0), raising=False)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
     for s in world.values():
         s.device_index = 0
     return world

@@ -229,6 +229,22 @@ def test_streams_graphs_and_repeats():
         fq.grad_norm(plan, 0.2)
 
 
+def test_a_plan_made_inside_a_capture():
+    g = make([20000, 50, 30000] * 30, 4)
+    norm, scale = fq.grad_norm(fq.grad_plan(g), 0.1)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        plan = fq.grad_plan(g)
+        out = fq.grad_norm(plan, 0.1)
+    for _ in range(3):
+        for t in out:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out[0], norm) and torch.equal(out[1], scale)
+        fq.grad_norm(plan, 0.2)
+
+
 def test_refusals_on_the_device():
     plan = fq.grad_plan(make([100]))
     with pytest.raises(fq.Fp4qError, match="workspace"):
