@@ -45,69 +45,94 @@ __device__ __forceinline__ uint32_t quantise8(const float (&f)[8], uint32_t& byt
 __global__ __launch_bounds__(256) void residual_norm_any_kernel(const ResidualNorm a) {
     __shared__ float red[4];
     const float n = (float)a.cols;
+    const bool post = a.post != kPostNone;
     for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
         const int64_t g0 = r / a.gate_rows * a.ldg;
-        float pm = 0.0f, pr = 1.0f, m = 0.0f;
-        if (a.post != kPostNone) {
-            if (a.post == 0) {
-                float s = 0.0f;
-                for (int64_t c = threadIdx.x; c < a.cols; c += 256)
-                    s += load_as(a.b, a.b_bf16, r * a.ldb + c);
-                pm = block_sum(s, red) / n;
-            }
-            float q = 0.0f;
-            for (int64_t c = threadIdx.x; c < a.cols; c += 256) {
-                const float d = load_as(a.b, a.b_bf16, r * a.ldb + c) - pm;
-                q += d * d;
-            }
-            pr = 1.0f / sqrtf(block_sum(q, red) / n + a.eps);
-        }
-        auto sum_at = [&](int64_t c) __attribute__((always_inline)) {
-            float v = load_as(a.b, a.b_bf16, r * a.ldb + c);
-            if (a.post != kPostNone)
-                v = (v - pm) * pr * vec1(a.post_weight, a.w_bf16, c, 1.0f) +
-                    vec1(a.post_bias, a.w_bf16, c, 0.0f);
-            if (a.gate) v *= load_as(a.gate, a.gate_bf16, g0 + c);
-            return a.x_scale * load_as(a.x, a.x_bf16, r * a.ldx + c) + a.branch_scale * v;
-        };
-        if (!a.rms) {
-            float s = 0.0f;
-            for (int64_t c = threadIdx.x; c < a.cols; c += 256) s += sum_at(c);
-            m = block_sum(s, red) / n;
-        }
-        float q = 0.0f;
-        for (int64_t c = threadIdx.x; c < a.cols; c += 256) {
-            const float d = sum_at(c) - m;
-            q += d * d;
-        }
-        const float rs = 1.0f / sqrtf(block_sum(q, red) / n + a.eps);
-        if (a.codes) {  // cols is a multiple of 32: whole groups of four lanes
-            for (int64_t c = threadIdx.x * 8; c < a.cols; c += 2048) {
-                float f[8];
+        float pm = 0.0f, pr = 1.0f, m = 0.0f, sum = 0.0f, mid = 0.0f;
+        // sums of the branch's elements and of their squares around `mid`
+        auto of_branch = [&](int64_t c, auto full, int left) __attribute__((always_inline)) {
+            constexpr int FULL = decltype(full)::value;
+            float b[8];
+            load8_as<FULL>(a.b, a.b_bf16, r * a.ldb + c, left, 0.0f, b);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float v = sum_at(c + e);
-                    store_as(a.xo, a.x_bf16, r * a.ldxo + c + e, v);
-                    f[e] = (v - m) * rs * vec1(a.weight, a.w_bf16, c + e, 1.0f) +
-                           vec1(a.bias, a.w_bf16, c + e, 0.0f);
-                }
-                uint32_t byte;
-                const uint32_t q8 = quantise8(f, byte);
-                *(uint32_t*)(a.codes + r * (a.cols / 2) + c / 2) = q8;
-                a.scales[r * (a.cols / 32) + c / 32] = (uint8_t)byte;
+            for (int e = 0; e < 8; ++e) sum += FULL || e < left ? b[e] : 0.0f;
+        };
+        auto of_branch2 = [&](int64_t c, auto full, int left) __attribute__((always_inline)) {
+            constexpr int FULL = decltype(full)::value;
+            float b[8];
+            load8_as<FULL>(a.b, a.b_bf16, r * a.ldb + c, left, 0.0f, b);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum += FULL || e < left ? (b[e] - mid) * (b[e] - mid) : 0.0f;
+        };
+        if (post) {
+            if (a.post == 0) {
+                over8(a.cols, of_branch);
+                pm = block_sum(sum, red) / n;
             }
-        } else {
-            for (int64_t c = threadIdx.x; c < a.cols; c += 256) {
-                const float v = sum_at(c);
-                store_as(a.xo, a.x_bf16, r * a.ldxo + c, v);
-                store_as(a.y, a.y_bf16, r * a.ldy + c,
-                         (v - m) * rs * vec1(a.weight, a.w_bf16, c, 1.0f) +
-                             vec1(a.bias, a.w_bf16, c, 0.0f));
-            }
+            sum = 0.0f;
+            mid = pm;
+            over8(a.cols, of_branch2);
+            pr = 1.0f / sqrtf(block_sum(sum, red) / n + a.eps);
         }
+        // x' of 8 elements
+        auto stream = [&](int64_t c, auto full, int left, float(&x)[8]) __attribute__((always_inline)) {
+            constexpr int FULL = decltype(full)::value;
+            float b[8], w[8], v[8];
+            load8_as<FULL>(a.b, a.b_bf16, r * a.ldb + c, left, 0.0f, b);
+            load8_as<FULL>(a.x, a.x_bf16, r * a.ldx + c, left, 0.0f, x);
+            load8_as<FULL>(a.post_weight, a.w_bf16, c, left, 1.0f, w);
+            load8_as<FULL>(a.post_bias, a.w_bf16, c, left, 0.0f, v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) b[e] = (b[e] - pm) * pr * w[e] + v[e];
+            load8_as<FULL>(a.gate, a.gate_bf16, g0 + c, left, 1.0f, w);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = a.x_scale * x[e] + a.branch_scale * (b[e] * w[e]);
+        };
+        auto of_stream = [&](int64_t c, auto full, int left) __attribute__((always_inline)) {
+            float x[8];
+            stream(c, full, left, x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum += decltype(full)::value || e < left ? x[e] : 0.0f;
+        };
+        auto of_stream2 = [&](int64_t c, auto full, int left) __attribute__((always_inline)) {
+            float x[8];
+            stream(c, full, left, x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                sum += decltype(full)::value || e < left ? (x[e] - mid) * (x[e] - mid) : 0.0f;
+        };
+        sum = 0.0f;
+        if (!a.rms) {
+            over8(a.cols, of_stream);
+            m = block_sum(sum, red) / n;
+        }
+        sum = 0.0f;
+        mid = m;
+        over8(a.cols, of_stream2);
+        const float rs = 1.0f / sqrtf(block_sum(sum, red) / n + a.eps);
+        // (each lane reads what it then writes: x_out may be x)
+        auto write = [&](int64_t c, auto full, int left) __attribute__((always_inline)) {
+            constexpr int FULL = decltype(full)::value;
+            float x[8], f[8], v[8];
+            stream(c, full, left, x);
+            load8_as<FULL>(a.weight, a.w_bf16, c, left, 1.0f, f);
+            load8_as<FULL>(a.bias, a.w_bf16, c, left, 0.0f, v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = (x[e] - m) * rs * f[e] + v[e];
+            store8_as<FULL>(a.xo, a.x_bf16, r * a.ldxo + c, left, x);
+            if (a.codes) {  // cols is a multiple of 32: whole groups of four lanes
+                uint32_t byte;
+                const uint32_t q = quantise8(f, byte);
+                *(uint32_t*)(a.codes + r * (a.cols / 2) + c / 2) = q;
+                a.scales[r * (a.cols / 32) + c / 32] = (uint8_t)byte;
+            } else {
+                store8_as<FULL>(a.y, a.y_bf16, r * a.ldy + c, left, f);
+            }
+        };
+        over8(a.cols, write);
         if (threadIdx.x == 0) {
             if (a.post_mean && a.post == 0) a.post_mean[r] = pm;
-            if (a.post_rstd && a.post != kPostNone) a.post_rstd[r] = pr;
+            if (a.post_rstd && post) a.post_rstd[r] = pr;
             if (a.mean && !a.rms) a.mean[r] = m;
             if (a.rstd) a.rstd[r] = rs;
         }

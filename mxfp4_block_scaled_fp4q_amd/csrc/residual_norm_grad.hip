@@ -68,54 +68,52 @@ struct RowStats {
         return {a.rms ? 0.0f : s.m, s.r, a.post == 0 ? s.pm : 0.0f, a.post != kPostNone ? s.pr : 1.0f};
     }
 };
-struct RowPoint {
-    const ResidualNormGrad& a;
-    int64_t r, g0;
-    RowStats s;
-    __device__ __forceinline__ RowPoint(const ResidualNormGrad& a, int64_t r)
-        : a(a), r(r), g0(r / a.gate_rows * a.ldg), s(RowStats::of(a, r)) {}
-    __device__ __forceinline__ float dy(int64_t c) const {
-        return load_as(a.dy, a.dy_bf16, r * a.lddy + c);
-    }
-    __device__ __forceinline__ float xh(int64_t c) const {
-        return (load_as(a.xo, a.x_bf16, r * a.ldxo + c) - s.m) * s.r;
-    }
-    __device__ __forceinline__ float nh(int64_t c) const {
-        return a.b ? (load_as(a.b, a.b_bf16, r * a.ldb + c) - s.pm) * s.pr : 0.0f;
-    }
-    __device__ __forceinline__ float D(int64_t c, const RowMeans& k) const {
-        const float t = dy(c) * vec1(a.weight, a.w_bf16, c, 1.0f);
-        const float d = s.r * (t - k.t - xh(c) * k.txh);
-        return a.dxo ? load_as(a.dxo, a.x_bf16, r * a.lddxo + c) + d : d;
-    }
-    __device__ __forceinline__ float u(int64_t c, float d) const {
-        d *= a.branch_scale * vec1(a.post_weight, a.w_bf16, c, 1.0f);
-        return a.gate ? d * load_as(a.gate, a.gate_bf16, g0 + c) : d;
-    }
-};
-
 __global__ __launch_bounds__(256) void residual_grad_rows_kernel(const ResidualNormGrad a,
                                                                  RowMeans* __restrict__ means) {
     __shared__ float red[4];
     const float n = (float)a.cols;
     for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
-        const RowPoint p(a, r);
+        const RowStats st = RowStats::of(a, r);
+        const int64_t g0 = r / a.gate_rows * a.ldg;
         RowMeans k = {0.0f, 0.0f, 0.0f, 0.0f};
         float s0 = 0.0f, s1 = 0.0f;
-        for (int64_t c = threadIdx.x; c < a.cols; c += 256) {
-            const float t = p.dy(c) * vec1(a.weight, a.w_bf16, c, 1.0f);
-            s0 += t * p.xh(c);
-            s1 += t;
-        }
+        auto first = [&](int64_t c, auto full, int left) __attribute__((always_inline)) {
+            constexpr int FULL = decltype(full)::value;
+            float x[8], t[8], w[8];
+            load8_as<FULL>(a.xo, a.x_bf16, r * a.ldxo + c, left, 0.0f, x);
+            load8_as<FULL>(a.dy, a.dy_bf16, r * a.lddy + c, left, 0.0f, t);
+            load8_as<FULL>(a.weight, a.w_bf16, c, left, 1.0f, w);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                t[e] *= w[e];  // 0 past the row's end
+                s0 += t[e] * ((x[e] - st.m) * st.r);
+                s1 += t[e];
+            }
+        };
+        over8(a.cols, first);
         k.txh = block_sum(s0, red) / n;
         if (!a.rms) k.t = block_sum(s1, red) / n;
         if (a.post != kPostNone) {
             s0 = s1 = 0.0f;
-            for (int64_t c = threadIdx.x; c < a.cols; c += 256) {
-                const float u = p.u(c, p.D(c, k));
-                s0 += u * p.nh(c);
-                s1 += u;
-            }
+            auto second = [&](int64_t c, auto full, int left) __attribute__((always_inline)) {
+                constexpr int FULL = decltype(full)::value;
+                float x[8], t[8], w[8], s[8], b[8], p[8], g[8];
+                load8_as<FULL>(a.xo, a.x_bf16, r * a.ldxo + c, left, 0.0f, x);
+                load8_as<FULL>(a.dy, a.dy_bf16, r * a.lddy + c, left, 0.0f, t);
+                load8_as<FULL>(a.dxo, a.x_bf16, r * a.lddxo + c, left, 0.0f, s);
+                load8_as<FULL>(a.b, a.b_bf16, r * a.ldb + c, left, 0.0f, b);
+                load8_as<FULL>(a.weight, a.w_bf16, c, left, 1.0f, w);
+                load8_as<FULL>(a.post_weight, a.w_bf16, c, left, 1.0f, p);
+                load8_as<FULL>(a.gate, a.gate_bf16, g0 + c, left, 1.0f, g);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float d = s[e] + st.r * (t[e] * w[e] - k.t - (x[e] - st.m) * st.r * k.txh);
+                    const float u = FULL || e < left ? d * (a.branch_scale * p[e] * g[e]) : 0.0f;
+                    s0 += u * ((b[e] - st.pm) * st.pr);
+                    s1 += u;
+                }
+            };
+            over8(a.cols, second);
             k.unh = block_sum(s0, red) / n;
             if (a.post == 0) k.u = block_sum(s1, red) / n;
         }
@@ -202,42 +200,6 @@ __global__ __launch_bounds__(1024) void residual_grad_means_kernel(const Residua
 // `cols` floats: dw, dc, and S1, S2 of the slab's group, or with whole groups
 // dwp, dbp (the groups' dg is then written at once).  Each element is read and
 // written by one lane, so that dx and db may lie on dxo and b.
-// FULL: all 8 elements are there, otherwise the first `left`.
-template <int B16, int FULL>
-__device__ __forceinline__ void load8(const void* p, int64_t i, int left, float (&f)[8]) {
-    if (FULL) {
-        Chunk<B16> c;
-        c.load(p, i);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = c.at(e);
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = e < left ? load1<B16>(p, i + e) : 0.0f;
-    }
-}
-template <int B16, int FULL>
-__device__ __forceinline__ void store8(void* p, int64_t i, int left, const float (&f)[8]) {
-    if (FULL) {
-        store_chunk<B16>(p, i, f);
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (e < left) store1<B16>(p, i + e, f[e]);
-    }
-}
-template <int FULL>
-__device__ __forceinline__ void load8_as(const void* p, int bf16, int64_t i, int left, float none,
-                                         float (&f)[8]) {
-    if (!p) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = none;
-    } else if (bf16) {
-        load8<1, FULL>(p, i, left, f);
-    } else {
-        load8<0, FULL>(p, i, left, f);
-    }
-}
-
 template <int XB, int BB, int DB, int FULL>
 __device__ __forceinline__ void tile(const ResidualNormGrad& a, const RowMeans* __restrict__ means,
                                      const Slabs& sl, float* part, int64_t c, int left) {

@@ -2,6 +2,8 @@
 // of a row's elements, sums over its lanes and waves, and where a row's elements
 // lie in the registers of the lanes that hold it.
 #pragma once
+#include <type_traits>
+
 #include "fp4q_device.h"
 #include "fp4q_internal.h"
 
@@ -28,12 +30,6 @@ __device__ __forceinline__ float vec1(const void* p, int bf16, int64_t i, float 
 // The same where the type is known at run time only.
 __device__ __forceinline__ float load_as(const void* p, int bf16, int64_t i) {
     return bf16 ? load1<1>(p, i) : load1<0>(p, i);
-}
-__device__ __forceinline__ void store_as(void* p, int bf16, int64_t i, float v) {
-    if (bf16)
-        store1<1>(p, i, v);
-    else
-        store1<0>(p, i, v);
 }
 
 // 8 consecutive elements as they lie in memory.
@@ -114,6 +110,61 @@ __device__ __forceinline__ void load_vec8(const void* p, int bf16, int64_t i, fl
         c.load(p, i);
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[e] = c.at(e);
+    }
+}
+
+// Any width: a lane takes 8 elements at a time.  FULL: all 8 are there, otherwise
+// the first `left`.
+template <int B16, int FULL>
+__device__ __forceinline__ void load8(const void* p, int64_t i, int left, float (&f)[8]) {
+    if (FULL) {
+        Chunk<B16> c;
+        c.load(p, i);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = c.at(e);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = e < left ? load1<B16>(p, i + e) : 0.0f;
+    }
+}
+template <int B16, int FULL>
+__device__ __forceinline__ void store8(void* p, int64_t i, int left, const float (&f)[8]) {
+    if (FULL) {
+        store_chunk<B16>(p, i, f);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (e < left) store1<B16>(p, i + e, f[e]);
+    }
+}
+template <int FULL>
+__device__ __forceinline__ void load8_as(const void* p, int bf16, int64_t i, int left, float none,
+                                         float (&f)[8]) {
+    if (!p) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = none;
+    } else if (bf16) {
+        load8<1, FULL>(p, i, left, f);
+    } else {
+        load8<0, FULL>(p, i, left, f);
+    }
+}
+template <int FULL>
+__device__ __forceinline__ void store8_as(void* p, int bf16, int64_t i, int left, const float (&f)[8]) {
+    if (bf16)
+        store8<1, FULL>(p, i, left, f);
+    else
+        store8<0, FULL>(p, i, left, f);
+}
+// f(first element, whether 8 are left (std::true_type or false_type), how many)
+// over a row that 256 threads share.
+template <class F>
+__device__ __forceinline__ void over8(int64_t cols, F f) {
+    for (int64_t c = threadIdx.x * 8; c < cols; c += 2048) {
+        if (c + 8 <= cols)
+            f(c, std::true_type{}, 8);
+        else
+            f(c, std::false_type{}, (int)(cols - c));
     }
 }
 
