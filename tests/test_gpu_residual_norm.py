@@ -402,3 +402,95 @@ def test_other_stream_and_graph_replays(C):
         torch.cuda.synchronize()
         assert all(np.array_equal(host_bits(t), w) for t, w in zip(out, want))
         step()
+
+
+@pytest.mark.parametrize("C", [5, 300, 1000, 2048, 9000, 20000])
+def test_overflowing_squares(C):
+    """Finite elements whose squares overflow fp32 make the norm's rstd 0 and its
+    output the bias, in front of the sum as behind it, and leave other rows alone."""
+    for post, kind in ((LAYER, LAYER), (RMS, RMS)):
+        c = Case(5, C, F32, F32, post, kind)
+        ref = c.forward()
+        c.b[1, C // 2], c.x[3, 0] = 1e25, -1e25
+        xo, y, (_, pr, _, r) = c.forward()
+        assert pr[1] == 0 and r[3] == 0 and xo.isfinite().all() and y.isfinite().all()
+        assert torch.equal(xo[1], c.x[1] + c.pc) and torch.equal(y[3], c.c)
+        keep = [0, 2, 4]
+        assert torch.equal(xo[keep], ref[0][keep]) and torch.equal(y[keep], ref[1][keep])
+
+
+def test_offsets_beyond_32_bits():
+    """The last rows of operands of more than 2^31 elements: the same bits as
+    from a call on them alone."""
+    R, C, last = 270001, 8192, 5
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+
+    def big():
+        t = torch.zeros(R, C, dtype=BF, device="cuda")
+        t[-last:] = torch.randn(last, C, generator=g, device="cuda").to(BF)
+        return t
+    x, b, dy, dxo = (big() for _ in range(4))
+    w = torch.rand(C, generator=g, device="cuda") + 0.5
+    kw = dict(kind=RMS, post_kind=RMS, post_weight=w)
+    xo, y, stats = fq.residual_norm(x, b, w, **kw)
+    few = [t[-last:].contiguous() for t in (x, b, dy, dxo)]
+    xo2, y2, stats2 = fq.residual_norm(few[0], few[1], w, **kw)
+    assert torch.equal(xo[-last:], xo2) and torch.equal(y[-last:], y2) and torch.equal(stats[3][-last:], stats2[3])
+    assert not xo[:-last].any() and not y[:-last].any()
+    full = fq.residual_norm_grad(dy, dxo, xo, b, stats, w, **kw)
+    part = fq.residual_norm_grad(few[2], few[3], xo2, few[1], stats2, w, **kw)
+    assert torch.equal(full[0][-last:], part[0]) and torch.equal(full[1][-last:], part[1])
+    assert not full[0][:-last].any() and not full[1][:-last].any()
+    # the sums of the few rows that are not zero, in another order: 2 roundings a row
+    for a, e in zip(full[2:5], part[2:5]):
+        assert torch.allclose(a, e, rtol=0, atol=10 * E * float(e.abs().max()) * last)
+    _, (codes, scales), _ = fq.residual_norm(x, b, w, quantize=True, **kw)
+    wc, ws = fq.residual_norm(few[0], few[1], w, quantize=True, **kw)[1]
+    assert torch.equal(codes[-last:], wc) and torch.equal(scales[-last:], ws)
+
+
+def test_two_calls_at_once():
+    """Calls on two streams have workspaces of their own."""
+    cases = [Case(900, C, BF, BF, RMS, LAYER, gates=g) for C, g in ((520, 300), (2048, 7))]
+    work = []
+    for c in cases:
+        xo, _, stats = c.forward()
+        dy, dxo = (make(c.rng, c.R, c.C, BF, 0, 0.0, 1e-3)[0] for _ in range(2))
+        work.append((c, dy, dxo, xo, stats))
+
+    def grad(c, dy, dxo, xo, stats):
+        return fq.residual_norm_grad(dy, dxo, xo, c.b, stats, c.w, **c.kw)
+    want = [[host_bits(t) for t in grad(*w)] for w in work]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in work]
+    for _ in range(3):
+        got = []
+        for s, w in zip(streams, work):
+            s.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(s):
+                got.append(grad(*w))
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert all(np.array_equal(host_bits(t), e) for t, e in zip(a, b))
+
+
+@pytest.mark.parametrize("C", [513, 1025, 1540, 2055, 3001, 3600, 4100, 4608, 5125, 6144, 6145, 7170, 8185])
+def test_every_number_of_waves(C):
+    """Rows of every number of waves, teams that share a workgroup among them,
+    rows that do not divide among the teams, with and without a gate per row."""
+    for i, R in enumerate((3, 13, 45)):
+        Case(R, C, BF, F32, LAYER, RMS, gates=(0, 1, 4)[i]).check_backward(BF)
+        Case(R, C, F32, BF, RMS, LAYER, gates=(1, R, 0)[i]).check_backward(F32, inplace=i == 1)
+        Case(R, C, BF, BF, LAYER, LAYER, gates=(1, 0, 4)[i]).check_forward(F32)
+
+
+def test_many_short_rows():
+    """Rows of one or two chunks per lane that a wave holds alone."""
+    for C in (96, 520, 600, 1000, 1024):
+        c = Case(1100, C, BF, BF, RMS, LAYER, gates=300)
+        c.check_forward(BF)
+        if C % 32 == 0:
+            y, (codes, scales) = c.forward(out_dtype=F32)[1], c.forward(quantize=True)[1]
+            wc, ws = fq.quantize(y, 32)
+            assert torch.equal(codes, wc) and torch.equal(scales, ws)
