@@ -52,6 +52,12 @@ static Slabs make_slabs(int64_t rows, int64_t gate_rows, int64_t most, int64_t l
     return s;
 }
 
+// Which of the four column sums anybody asks for, a bit each.
+__host__ __device__ inline int wanted_sums(const ResidualNormGrad& a) {
+    return (a.dweight ? 1 : 0) | (a.dbias ? 2 : 0) | (a.dpost_weight || a.dgate ? 4 : 0) |
+           (a.dpost_bias || (a.dgate && a.post_bias) ? 8 : 0);
+}
+
 // Sums of row r: mean_c(t xh), mean_c(t), mean_c(u nh), mean_c(u).
 struct RowMeans {
     float txh, t, unh, u;
@@ -350,7 +356,7 @@ __global__ __launch_bounds__(1024) void residual_grad_join_kernel(const Residual
     for (int64_t g = (blockIdx.y - 4) * (few ? 16 : 1) + (few ? wave : 0); g < groups; g += step) {
         const float* q = p + (g * sl.k * 4 + 2) * a.cols;
         float s1 = slab_sum(q, stride, few ? 0 : wave, few ? 1 : 16, sl.k);
-        float s2 = slab_sum(q + a.cols, stride, few ? 0 : wave, few ? 1 : 16, sl.k);
+        float s2 = a.post_bias ? slab_sum(q + a.cols, stride, few ? 0 : wave, few ? 1 : 16, sl.k) : 0.0f;
         if (!few) {
             __syncthreads();
             s1 = all16(s1, 0);
@@ -610,12 +616,15 @@ __global__ __launch_bounds__(T ? T : 256) void residual_grad_kernel(
     auto sums_of = [&](int o, int k) __attribute__((always_inline)) -> float(&)[8] {
         return o == 0 ? dw[k] : o == 1 ? dc[k] : o == 2 ? (GATE ? dpw[k] : s1[k]) : (GATE ? dpc[k] : s2[k]);
     };
+    const int wanted = wanted_sums(a);
     // (where two lanes hold an element, their sums of it are the same bits)
     if (NV != 1 || P == 1) {
 #pragma unroll
-        for (int o = 0; o < 4; ++o)
+        for (int o = 0; o < 4; ++o) {
+            if (!(wanted >> o & 1)) continue;
 #pragma unroll
             for (int k = 0; k < NV; ++k) store_row<0>(out, o * cols, pl.start(k), sums_of(o, k));
+        }
     } else {
         // The teams' sums of the same columns are added up through LDS, four of a
         // lane's columns at a time: part j of a lane's eight is added by team j % P.
@@ -629,6 +638,7 @@ __global__ __launch_bounds__(T ? T : 256) void residual_grad_kernel(
         __syncthreads();
         const int lane = threadIdx.x - wave0 * 64, waves = MULTI ? W * 64 : 64;
         for (int j = team; j < 8; j += P) {
+            if (!(wanted >> (j >> 1) & 1)) continue;
             float v[4] = {};
 #pragma unroll 4
             for (int q = 0; q < P; ++q) {
@@ -644,7 +654,7 @@ __global__ __launch_bounds__(T ? T : 256) void residual_grad_kernel(
     // the only slab: what the join kernel does
     __syncthreads();
     for (int c = threadIdx.x; c < cols; c += blockDim.x) {
-        float s1c = out[2 * cols + c], s2c = out[3 * cols + c];
+        float s1c = out[2 * cols + c], s2c = wanted & 8 ? out[3 * cols + c] : 0.0f;
         if (a.dweight) a.dweight[c] = out[c];
         if (a.dbias) a.dbias[c] = out[cols + c];
         if (!GATE) {
@@ -667,10 +677,6 @@ __global__ __launch_bounds__(T ? T : 256) void residual_grad_kernel(
 constexpr int64_t kAnyGrid = 1 << 16;
 
 constexpr int64_t kGridY = 1 << 15;
-
-static bool any_sums(const ResidualNormGrad& a) {
-    return a.dweight || a.dbias || a.dpost_weight || a.dpost_bias || a.dgate;
-}
 
 // How rows are held: by waves of their own (T = 0) or by teams of W waves in a
 // workgroup of at most T threads, nv chunks per lane; nv = 0: the rows' means
@@ -757,7 +763,7 @@ static void go_dy(const GradShape sh, const ResidualNormGrad& a, const Slabs& sl
 hipError_t launch_residual_norm_grad(const ResidualNormGrad& a, void* ws, hipStream_t s) {
     const Slabs sl = grad_slabs(a.rows, a.cols, a.gate_rows);
     const GradShape sh = grad_shape(a.cols, a.gate_rows < a.rows && !sl.k);
-    const bool sums = any_sums(a);
+    const bool sums = wanted_sums(a) != 0;
     RowMeans* means = (RowMeans*)ws;
     float* part = sh.nv == 0 ? (float*)(means + a.rows) : (float*)ws;
     float* p = sums ? part : nullptr;
