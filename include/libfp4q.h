@@ -718,8 +718,8 @@ fp4q_status_t fp4q_grad_norm(const fp4q_tensor_t* tensors, int32_t n, const void
  * and Inf included, are fp4q_grad_norm's (of fp32 products: Inf times 0 is NaN).
  */
 fp4q_status_t fp4q_grad_clip(const fp4q_tensor_t* tensors, int32_t n, const void* table,
-                             fp4q_norm_order_t order, double max_norm, double eps, float* norm, void* workspace,
-                             size_t workspace_bytes, void* stream);
+                             fp4q_norm_order_t order, double max_norm, double eps, float* norm,
+                             void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * fp4q_grad_scale -- every element of the tensors times *scale (device fp32), in
