@@ -1131,6 +1131,8 @@ class GradPlan:
             if t.get_device() != d:
                 raise ValueError("the gradients must lie on one device")
             words.extend((t.data_ptr(), t.numel(), codes[t.dtype]))
+        ends = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in grads if t.numel())
+        self.overlap = any(b[0] < a[1] for a, b in zip(ends, ends[1:]))
         self.array = (Tensor * self.n).from_buffer(words)
         self.nbytes = lib().fp4q_grad_norm_workspace_bytes(self.array, self.n)
         self.table, self.streams = None, {_stream(None)}
@@ -1173,6 +1175,15 @@ def _grads_of(plan):
         if plan.grads is None:
             plan.grads = grad_plan([row[1] for row in plan.tensors])
         return plan.grads
+    return plan
+
+
+def _grads_to_write(plan):
+    """_grads_of a plan that is going to be written: memory that two of its
+    gradients share would be scaled twice, by workgroups that race."""
+    plan = _grads_of(plan)
+    if plan.overlap:
+        raise ValueError("gradients that are scaled must not overlap")
     return plan
 
 
@@ -1227,8 +1238,8 @@ def grad_norm(plan, max_norm=None, eps=1e-6, order=NORM_L2, norm=None, scale=Non
 
 def scale_grads(plan, scale, stream=None):
     """Multiplies a plan's gradients by a device fp32 scalar in place
-    (fp4q_grad_scale)."""
-    plan = _grads_of(plan)
+    (fp4q_grad_scale).  Gradients that share memory are refused."""
+    plan = _grads_to_write(plan)
     _need_cuda(scale)
     _need(scale, "scale", _torch().float32)
     if scale.numel() != 1:
@@ -1244,8 +1255,8 @@ def scale_grads(plan, scale, stream=None):
 def clip_grads(plan, max_norm, eps=1e-6, order=NORM_L2, norm=None, workspace=None, stream=None):
     """Clips a plan's gradients in place to the norm max_norm (fp4q_grad_clip):
     what scale_grads does with grad_norm's scale.  Returns the norm they had, a
-    device fp32 scalar."""
-    plan = _grads_of(plan)
+    device fp32 scalar.  Gradients that share memory are refused."""
+    plan = _grads_to_write(plan)
     d = _device_of(plan.like, stream)
     empty = _allocator(plan.like, stream)
     norm = _scalar(norm, "norm", d, empty)

@@ -150,8 +150,9 @@ fp4q_status_t grad_tensors(const char* who, const fp4q_tensor_t* tensors, int32_
 
 // Arguments that the gradient norm and the clipping share.
 fp4q_status_t grad_norm_args(const char* who, const fp4q_tensor_t* tensors, int32_t n,
-                             const void* table, fp4q_norm_order_t order, double max_norm, double eps, const float* norm,
-                             const float* scale, const void* workspace, size_t workspace_bytes) {
+                             const void* table, fp4q_norm_order_t order, double max_norm,
+                             double eps, const float* norm, const float* scale,
+                             const void* workspace, size_t workspace_bytes) {
     if (order != FP4Q_NORM_L2 && order != FP4Q_NORM_MAX)
         return fail(FP4Q_ERR_INVALID, "%s: bad order %d", who, (int)order);
     if (!(max_norm >= 0.0) || !(max_norm < 1e300) || !(eps >= 0.0) || !(eps < 1e300))

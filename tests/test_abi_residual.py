@@ -238,6 +238,22 @@ def test_grad_plan_checks(there):
     assert fq._lib.calls[-1][1][0] is a.grads.array and a.grads.array[1].data == ones[1].data_ptr()
 
 
+def test_gradients_that_share_memory_are_not_scaled(there):
+    whole = torch.zeros(32)
+    part = lambda a, b: dev(whole[a:b])  # noqa: E731
+    for grads, shared in (([part(0, 16), part(16, 32), part(16, 16)], False), ([part(16, 32), part(0, 16)], False),
+                          ([part(0, 17), part(16, 32)], True), ([part(0, 32), part(4, 5), part(30, 30)], True),
+                          ([part(8, 9), part(0, 8), part(8, 9)], True)):
+        p = fq.grad_plan(grads)
+        fq.grad_norm(p, 1.0)
+        for call in (lambda: fq.clip_grads(p, 1.0), lambda: fq.scale_grads(p, rows(1))):
+            if shared:
+                with pytest.raises(ValueError, match="overlap"):
+                    call()
+            else:
+                call()
+
+
 def test_what_a_call_allocates_belongs_to_its_stream(there):
     x, s, wide = rows(), dev(torch.zeros(4)), rows(4, 32)
     p = fq.grad_plan([x])
