@@ -303,8 +303,10 @@ __global__ __launch_bounds__(256) void residual_grad_tile_kernel(const ResidualN
 // Adds up the rows of partial sums: 64 columns per workgroup, one to a lane, 16
 // waves over the slabs.  blockIdx.y: dw, dc, dwp, dbp, then the gate's groups:
 // one at a time, gridDim.y - 4 apart, or 16 at a time where a wave adds up the
-// few parts of one (kFewParts).
-constexpr int64_t kJoinGroups = 1 << 22;
+// few parts of one (kFewParts).  group0: the first workgroup's number, since a
+// launch holds below 2^32 threads a side.
+constexpr int64_t kJoinThreads = 1024, kJoinGroups = 1 << 21;
+static_assert(kJoinGroups * kJoinThreads < (int64_t)1 << 32, "threads of a launch");
 constexpr int kFewParts = 16;
 // factor(i): of slab i's row
 template <class F>
@@ -322,7 +324,7 @@ __device__ __forceinline__ float slab_sum(const float* p, int64_t stride, int fi
     for (int64_t i = first; i < count; i += step) s += p[i * stride];
     return s;
 }
-__global__ __launch_bounds__(1024) void residual_grad_join_kernel(const ResidualNormGrad a,
+__global__ __launch_bounds__(kJoinThreads) void residual_grad_join_kernel(const ResidualNormGrad a,
                                                                   const float* __restrict__ part,
                                                                   const Slabs sl, int64_t group0) {
     __shared__ float red[2][16][64];
@@ -784,17 +786,20 @@ hipError_t launch_residual_norm_grad(const ResidualNormGrad& a, void* ws, hipStr
         a.b_bf16 ? go_dy<1, 1>(sh, a, sl, means, p, s) : go_dy<1, 0>(sh, a, sl, means, p, s);
     else
         a.b_bf16 ? go_dy<0, 1>(sh, a, sl, means, p, s) : go_dy<0, 0>(sh, a, sl, means, p, s);
+    hipError_t e = hipGetLastError();
     if (sums && (sh.nv == 0 || sl.count > 1)) {
         int64_t gates = a.dgate && sl.k ? sl.count / sl.k : 0;
         if (sl.k <= kFewParts) gates = (gates + 15) / 16;
         gates = std::min(gates, kGridY);
         const int64_t groups = (a.cols + 63) / 64;
-        for (int64_t g = 0; g < groups; g += kJoinGroups)
+        for (int64_t g = 0; g < groups && e == hipSuccess; g += kJoinGroups) {
             FP4Q_LAUNCH(residual_grad_join_kernel,
                         dim3((unsigned)std::min(groups - g, kJoinGroups), (unsigned)(4 + gates)),
-                        dim3(1024), 0, s, a, part, sl, g);
+                        dim3((unsigned)kJoinThreads), 0, s, a, part, sl, g);
+            e = hipGetLastError();
+        }
     }
-    return hipGetLastError();
+    return e;
 }
 
 }  // namespace fp4q
