@@ -42,24 +42,27 @@ struct Slabs {
     }
     __device__ __forceinline__ int64_t group_of(uint32_t i) const { return fastdiv(i, div); }  // of parts
 };
-// At most `most` slabs of at least `least` rows, or as many as there are groups.
-static Slabs make_slabs(int64_t rows, int64_t gate_rows, int64_t most, int64_t least) {
-    Slabs s;
+// `groups` whole groups to a slab.
+static Slabs whole_slabs(int64_t rows, int64_t group, int64_t groups) {
+    Slabs s = {};
     s.rows = rows;
-    s.group = std::min(gate_rows, rows);
-    const int64_t all = (rows + s.group - 1) / s.group;
-    const int64_t each = std::max(least, (rows + most - 1) / most);
-    if (s.group > each || all == 1) {
-        const int64_t k = std::max<int64_t>(1, std::min((s.group + each - 1) / each, most / all));
-        s.each = (s.group + k - 1) / k;
-        s.k = (s.group + s.each - 1) / s.each;
-        s.count = all * s.k;
-    } else {
-        s.k = 0;
-        s.each = (each < rows ? each / s.group : all) * s.group;
-        s.count = (rows + s.each - 1) / s.each;
-    }
-    s.div = make_fastdiv((uint32_t)std::max<int64_t>(s.k, 1));
+    s.group = group;
+    s.each = groups * group;
+    s.count = (rows + s.each - 1) / s.each;
+    s.div = make_fastdiv(1);
+    return s;
+}
+// Parts of groups, of about `each` rows: at most `most` slabs, or one to a group.
+static Slabs part_slabs(int64_t rows, int64_t group, int64_t most, int64_t each) {
+    Slabs s = {};
+    s.rows = rows;
+    s.group = group;
+    const int64_t all = (rows + group - 1) / group;
+    const int64_t k = std::max<int64_t>(1, std::min((group + each - 1) / each, most / all));
+    s.each = (group + k - 1) / k;
+    s.k = (group + s.each - 1) / s.each;
+    s.count = all * s.k;
+    s.div = make_fastdiv((uint32_t)s.k);
     return s;
 }
 
@@ -711,15 +714,44 @@ static GradShape grad_shape(int64_t cols, bool whole) {
 // rows take 7.4 and 9.9 us at 256 x 1112 fp32 (32 and 64 workgroups), 20.4 and
 // 18.9 with the join at 1000 x 2048 bf16, where the partial sums count.  Up to 4
 // rows to a team are one slab, which needs no join.
+//
+// Groups that are shorter than such a slab lie in slabs of whole groups, a group
+// to a team.  Where that leaves a quarter of the teams and more without a group,
+// the groups may be slabs of their own, whose rows all teams share: whichever has
+// the fewer rows one after another, a slab's beginning and end counted as 3 of
+// them (4 with waves on their own).  16384 x 1024 bf16 with 8, 12, 24, 32, 40 and
+// 64 rows to a group: whole 53, 62, 59, 65, 79 and 117 us, on their own 87, 68, 52,
+// 49, 50 and 44; 49152 x 512 with 16, 24, 32, 40 and 64: 72, 65, 66, 77, 106 and
+// 88, 78, 71, 74, 65.
 static Slabs grad_slabs(int64_t rows, int64_t cols, int64_t gate_rows) {
-    const auto slabs = [&](bool whole) {
-        const GradShape sh = grad_shape(cols, whole);
-        const int64_t most = sh.nv == 0 ? 256 : 256 * std::max(1, (whole ? 8 : 12) * 64 / sh.threads);
-        if (sh.nv && rows <= 4 * (sh.threads / 64 / sh.W)) return make_slabs(rows, gate_rows, 1, rows);
-        return make_slabs(rows, gate_rows, most, sh.nv && sh.T ? (rows <= 512 ? 4 : 8) : 16);
+    struct Limits {
+        int64_t teams, most, each;  // teams of a workgroup, slabs, rows of a slab
+        bool one;                   // one slab for all rows
     };
-    const Slabs sl = slabs(false);
-    return gate_rows < rows && !sl.k ? slabs(true) : sl;
+    const auto limits = [&](const GradShape& sh, int waves) {
+        Limits l;
+        l.teams = sh.nv ? sh.threads / 64 / sh.W : 1;
+        l.most = sh.nv ? 256 * std::max(1, waves * 64 / sh.threads) : 256;
+        l.each = std::max<int64_t>(sh.nv && sh.T ? (rows <= 512 ? 4 : 8) : 16, (rows + l.most - 1) / l.most);
+        l.one = sh.nv && rows <= 4 * l.teams;
+        return l;
+    };
+    const Limits p = limits(grad_shape(cols, false), 12);
+    if (gate_rows >= rows) return part_slabs(rows, rows, p.one ? 1 : p.most, p.one ? rows : p.each);
+    const GradShape sh = grad_shape(cols, true);
+    const Limits w = limits(sh, 8);
+    const int64_t all = (rows + gate_rows - 1) / gate_rows;
+    if (w.one) return whole_slabs(rows, gate_rows, all);
+    const Slabs parts = part_slabs(rows, gate_rows, p.most, p.each);
+    if (gate_rows > p.each) return parts;
+    const int64_t fit = w.each < rows ? w.each / gate_rows : all;
+    if (sh.nv == 0) return whole_slabs(rows, gate_rows, fit);
+    const int64_t groups = std::max(fit, (all + w.most - 1) / w.most);
+    const int64_t turns = (groups + w.teams - 1) / w.teams;
+    const int64_t shared = (parts.count + p.most - 1) / p.most *
+                           ((gate_rows + p.teams - 1) / p.teams + (sh.T ? 3 : 4));
+    const bool idle = 4 * groups <= 3 * turns * w.teams;
+    return idle && shared < turns * gate_rows ? parts : whole_slabs(rows, gate_rows, groups);
 }
 
 size_t residual_norm_grad_workspace_bytes(int64_t rows, int64_t cols, int64_t gate_rows) {

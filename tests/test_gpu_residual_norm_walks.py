@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import mxfp4_block_scaled_fp4q_amd as fq
+from test_gpu_residual_norm import BF, F32, LAYER, RMS, Case
 
 pytestmark = pytest.mark.gpu
 
@@ -23,3 +24,12 @@ def test_column_sums_of_rows_beyond_one_launch():
     assert torch.equal(dc, dy[0].float()) and torch.equal(dw, dy[0].float() * x[0].float())
     assert torch.equal(dx[0], dpc.bfloat16()) and torch.equal(dpw, dpc * b[0].float())
     assert torch.isfinite(dpc).all() and dpc[-40:].any()
+
+
+@pytest.mark.parametrize("C", [300, 520, 1030, 2050])
+@pytest.mark.parametrize("R,gates", [(5000, 7), (5000, 12), (5000, 13), (20000, 24), (20000, 33), (20000, 40), (20000, 77)])
+def test_gates_that_do_not_go_round(R, gates, C):
+    """Groups that are fewer than the teams of a workgroup, or do not divide
+    among them: as slabs of their own and as whole ones."""
+    R = R if C < 1000 else R // 4
+    Case(R, C, BF, BF, LAYER, RMS, gates=gates, gdt=F32).check_backward(BF)
