@@ -338,7 +338,8 @@ __global__ __launch_bounds__(MULTI ? 1024 : 256) void residual_norm_kernel(const
             for (int e = 0; e < 8; ++e) {
                 float t = (n[k][e] - pm) * pr * pw[k][e] + pc[k][e];
                 if (GATE) t *= g[k][e];
-                v[k][e] = a.x_scale * v[k][e] + t;
+                // not a contraction of either product: two waves may hold the element
+                v[k][e] = __builtin_fmaf(a.x_scale, v[k][e], t);
             }
         }
         float var;

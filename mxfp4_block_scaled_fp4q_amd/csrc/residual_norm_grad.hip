@@ -19,6 +19,12 @@
 #include "residual_norm.h"
 #include "row_norm.h"
 
+// A product and a sum become one operation where they stand in one expression,
+// and nowhere else.  Elements that two waves hold have different places in their
+// lanes, and left to itself the compiler contracts a b + c d one way for one place
+// and the other way for another: their bits differed, and the last store won.
+#pragma clang fp contract(on)
+
 namespace fp4q {
 
 // Slabs of rows that each leave one row of partial column sums.  A slab holds

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import mxfp4_block_scaled_fp4q_amd as fq
-from test_gpu_residual_norm import BF, F32, LAYER, RMS, Case
+from test_gpu_residual_norm import BF, F32, LAYER, NONE, RMS, Case
 
 pytestmark = pytest.mark.gpu
 
@@ -33,3 +33,30 @@ def test_gates_that_do_not_go_round(R, gates, C):
     among them: as slabs of their own and as whole ones."""
     R = R if C < 1000 else R // 4
     Case(R, C, BF, BF, LAYER, RMS, gates=gates, gdt=F32).check_backward(BF)
+
+
+def same(a, b):
+    return [i for i, (x, y) in enumerate(zip(a, b)) if y is not None and not torch.equal(x, y)] == []
+
+
+SHARED = [513, 519, 1025, 1543, 5121, 6139, 8185, 8200, 9217, 13825]  # two waves hold the last elements
+
+
+@pytest.mark.parametrize("C", SHARED)
+def test_repeated_calls_give_the_same_bits(C):
+    """Elements that two waves hold, at other places of their lanes, are stored by
+    both: the same bits whichever is the last, in every form of the gates."""
+    R = 2600 if C < 1000 else 700
+    for post, kind, gates, dt, gdt in ((RMS, LAYER, 5, BF, BF), (LAYER, RMS, 5, F32, BF), (LAYER, LAYER, 1, BF, F32),
+                                       (NONE, RMS, 3, F32, F32), (LAYER, LAYER, 0, BF, BF), (RMS, RMS, R, F32, BF)):
+        c = Case(R, C, dt, dt, post, kind, gates=gates, gdt=gdt, xs=0.75, bs=0.3)
+        xo, y, stats = c.forward()
+        dy, dxo = (torch.randn(R, C, device="cuda").to(dt) for _ in range(2))
+
+        def back():
+            return fq.residual_norm_grad(dy, dxo, xo, c.b, stats, c.w, **c.kw)
+        want = back()
+        for _ in range(4):
+            assert same(back(), want), (C, post, kind, gates, dt)
+            again = c.forward()
+            assert same((*again[:2], *again[2]), (xo, y, *stats)), (C, post, kind, gates, dt)
