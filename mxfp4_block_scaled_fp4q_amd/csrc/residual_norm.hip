@@ -313,6 +313,10 @@ __global__ __launch_bounds__(MULTI ? 1024 : 256) void residual_norm_kernel(const
                 v[k][e] = in.x[k].at(e);
                 if (GATE) g[k][e] = in.g[k].at(e);
             }
+        // x' may lie on x, whose last elements two waves hold: all of a row has
+        // arrived before the barrier that its stores come after
+#pragma unroll
+        for (int k = 0; MULTI && k < NV; ++k) in.x[k].arrived();
         if (last >= 0) stats(last);
         last = r;
         if (kAhead) fetch(r + step);

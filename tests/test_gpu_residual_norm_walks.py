@@ -60,3 +60,16 @@ def test_repeated_calls_give_the_same_bits(C):
             assert same(back(), want), (C, post, kind, gates, dt)
             again = c.forward()
             assert same((*again[:2], *again[2]), (xo, y, *stats)), (C, post, kind, gates, dt)
+
+
+@pytest.mark.parametrize("C", SHARED)
+def test_forward_on_its_own_operand(C):
+    """x_out on x's memory: the same bits as in memory of its own, with rows
+    enough that every workgroup walks."""
+    for post, gates, xdt, bdt in ((LAYER, 0, BF, BF), (NONE, 0, F32, F32), (NONE, 0, BF, F32), (RMS, 3, F32, BF)):
+        c = Case(2600 if C < 1000 else 700, C, xdt, bdt, post, RMS if gates else LAYER, gates=gates)
+        xo, y, stats = c.forward()
+        for _ in range(2):
+            into, c.x = c.x, c.x.clone()
+            x2, y2, stats2 = fq.residual_norm(into, c.b, c.w, c.c, eps=c.eps, x_out=into, **c.kw)
+            assert x2 is into and same((x2, y2, *stats2), (xo, y, *stats))
