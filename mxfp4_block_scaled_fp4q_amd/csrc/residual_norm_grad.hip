@@ -529,10 +529,11 @@ __global__ __launch_bounds__(T ? T : 256) void residual_grad_kernel(
                 h[k][e] = (in.b[k].at(e) - st.pm) * st.pr;
                 if (GATE) g[k][e] = in.g[k].at(e);
             }
-        // dx and db may lie on dxo and b, whose last elements two waves hold: all
-        // of a row has arrived before the barrier that its stores come after
+        // dx and db may lie on dxo, b and dy, whose last elements two waves hold:
+        // all of a row has arrived before the barrier that its stores come after
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
+            in.d[k].arrived();
             in.s[k].arrived();
             in.b[k].arrived();
         }

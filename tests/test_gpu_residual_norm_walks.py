@@ -73,3 +73,25 @@ def test_forward_on_its_own_operand(C):
             into, c.x = c.x, c.x.clone()
             x2, y2, stats2 = fq.residual_norm(into, c.b, c.w, c.c, eps=c.eps, x_out=into, **c.kw)
             assert x2 is into and same((x2, y2, *stats2), (xo, y, *stats))
+
+
+@pytest.mark.parametrize("C", SHARED)
+def test_backward_on_its_own_operands(C):
+    """dx on dx_out's or dy's memory and dbranch on branch's or dy's: the same
+    bits as in memory of their own."""
+    R = 2600 if C < 1000 else 700
+    for post, gates, dt in ((LAYER, 0, BF), (NONE, 0, F32), (RMS, 5, BF)):
+        c = Case(R, C, dt, dt, post, RMS if gates else LAYER, gates=gates)
+        xo, _, stats = c.forward()
+        dy, dxo = (torch.randn(R, C, device="cuda").to(dt) for _ in range(2))
+
+        def run(dx, dbranch):
+            """Operands by name; results on the named ones."""
+            t = dict(dy=dy.clone(), dx_out=dxo.clone(), branch=c.b.clone())
+            at = {k: t.get(v) for k, v in (("dx", dx), ("dbranch", dbranch))}
+            out = fq.residual_norm_grad(t["dy"], t["dx_out"], xo, t["branch"], stats, c.w, **at, **c.kw)
+            assert all(v is None or out[i] is v for i, v in enumerate(at.values()))
+            return out
+        want = run(None, None)
+        for dx, dbranch in (("dx_out", "branch"), ("dy", "branch"), ("dx_out", "dy"), ("dy", None), (None, "dy")):
+            assert same(run(dx, dbranch), want), (dx, dbranch)
