@@ -566,7 +566,8 @@ fp4q_status_t fp4q_gemm_gated_grad(int64_t M, int64_t F, int64_t K, const uint8_
  *   too (either kind), and y the bias throughout; where their sum overflows,
  *   FP4Q_LAYER_NORM gives a NaN row.
  */
-typedef enum { FP4Q_LAYER_NORM = 0, FP4Q_RMS_NORM = 1 } fp4q_norm_t;
+/* (FP4Q_NO_NORM is for the post_kind of fp4q_residual_norm; fp4q_layer_norm refuses it) */
+typedef enum { FP4Q_LAYER_NORM = 0, FP4Q_RMS_NORM = 1, FP4Q_NO_NORM = 2 } fp4q_norm_t;
 fp4q_status_t fp4q_layer_norm(fp4q_norm_t kind, const void* x, fp4q_dtype_t x_dtype, int64_t rows,
                               int64_t cols, int64_t ld_x, const void* weight, const void* bias,
                               fp4q_dtype_t w_dtype, double eps, void* y, fp4q_dtype_t y_dtype,
@@ -622,7 +623,6 @@ fp4q_status_t fp4q_layer_norm_grad(fp4q_norm_t kind, const void* dy, fp4q_dtype_
  *   Any rows and cols below 2^31.  Inf and NaN stay in their row, in which they
  *   act as in fp4q_layer_norm.
  */
-#define FP4Q_NO_NORM ((fp4q_norm_t)2)
 fp4q_status_t fp4q_residual_norm(int64_t rows, int64_t cols, const void* x, fp4q_dtype_t x_dtype,
                                  int64_t ld_x, const void* branch, fp4q_dtype_t b_dtype,
                                  int64_t ld_b, fp4q_norm_t post_kind, const void* post_weight,
