@@ -1113,7 +1113,8 @@ def residual_norm_grad(dy, dx_out, x_out, branch, stats, weight=None, kind=LAYER
 
 class GradPlan:
     """The tensors of a gradient norm, checked once (see grad_plan).  Holds their
-    memory, through tensors of its own, and their table in device memory."""
+    memory, through tensors of its own, and their table in device memory (of a
+    plan made inside a capture, from the first call outside one)."""
 
     def __init__(self, grads):
         torch = _torch()
@@ -1135,9 +1136,14 @@ class GradPlan:
         self.overlap = any(b[0] < a[1] for a, b in zip(ends, ends[1:]))
         self.array = (Tensor * self.n).from_buffer(words)
         self.nbytes = lib().fp4q_grad_norm_workspace_bytes(self.array, self.n)
-        self.table, self.streams = None, {_stream(None)}
+        self.table = None
+        self._make_table()
+
+    def _make_table(self):
+        torch = _torch()
         if torch.cuda.is_current_stream_capturing():
             return  # no copies here: the descriptors travel as kernel arguments
+        self.streams = {_stream(None)}
         size = _ct.c_size_t(0)
         fill = lib().fp4q_grad_table
         _check(fill(self.array, self.n, None, _ct.byref(size)))
@@ -1152,7 +1158,9 @@ class GradPlan:
         plan be dropped."""
         handle = _stream_on(d, stream)
         if self.table is None:
-            return None, handle
+            self._make_table()  # of a plan that was made inside a capture
+            if self.table is None:
+                return None, handle
         if handle not in self.streams:
             self.table.record_stream(_torch().cuda.current_stream() if stream is None else stream)
             self.streams.add(handle)
