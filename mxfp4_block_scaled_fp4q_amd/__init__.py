@@ -1143,7 +1143,7 @@ class GradPlan:
         torch = _torch()
         if torch.cuda.is_current_stream_capturing():
             return  # no copies here: the descriptors travel as kernel arguments
-        self.streams = {_stream(None)}
+        self.streams = {_stream_on(self.like.get_device(), None)}
         size = _ct.c_size_t(0)
         fill = lib().fp4q_grad_table
         _check(fill(self.array, self.n, None, _ct.byref(size)))

@@ -4,7 +4,7 @@ import torch
 
 import mxfp4_block_scaled_fp4q_amd as fq
 from test_abi_residual import rows, there  # noqa: F401  (there is a fixture)
-from test_binding_memory import dev, u8, world  # noqa: F401  (world is a fixture)
+from test_binding_memory import Dev, dev, u8, world  # noqa: F401  (world is a fixture)
 
 
 @pytest.fixture
@@ -61,3 +61,19 @@ def test_a_plan_that_a_capture_left_without_a_table_gets_one(tables, there, adam
     assert read() == other.table.data_ptr() and other.table.recorded == {"main"}
     fq.scale_grads(other, rows(1))
     assert read() == other.table.data_ptr()
+
+
+def test_a_table_belongs_to_its_devices_stream(tables, there, monkeypatch):  # noqa: F811
+    """A plan of another device's gradients than the current one's: its memory is
+    that device's current stream's, whatever the current device's is called."""
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: (0x10, 0x77)[d])
+    monkeypatch.setattr(Dev, "get_device", lambda self: 1)
+    plan = fq.grad_plan([dev(torch.zeros(8))])
+    (table,) = tables["made"]
+    there["side"].device_index, there["side"].cuda_stream = 1, 0x10  # on device 1, not the one it was made on
+    plan.read_on(1, there["side"])
+    assert table.recorded == {"side"}
+    table.recorded.clear()
+    there["side"].cuda_stream = 0x77
+    plan.read_on(1, there["side"])
+    assert not table.recorded
