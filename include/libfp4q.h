@@ -621,7 +621,8 @@ fp4q_status_t fp4q_layer_norm_grad(fp4q_norm_t kind, const void* dy, fp4q_dtype_
  *   to skip (means are not written with FP4Q_RMS_NORM, the first two not with
  *   FP4Q_NO_NORM).
  *   Any rows and cols below 2^31.  Inf and NaN stay in their row, in which they
- *   act as in fp4q_layer_norm.
+ *   act as in fp4q_layer_norm; an Inf in a gate or a vector makes its column of
+ *   x_out, or y, Inf or NaN.
  */
 fp4q_status_t fp4q_residual_norm(int64_t rows, int64_t cols, const void* x, fp4q_dtype_t x_dtype,
                                  int64_t ld_x, const void* branch, fp4q_dtype_t b_dtype,
@@ -649,7 +650,7 @@ fp4q_status_t fp4q_residual_norm(int64_t rows, int64_t cols, const void* x, fp4q
  *   branch_scale D n, n = nh post_weight + post_bias
  *   dy: bf16 or fp32; dx_out and dx: of x_dtype; branch and dbranch: of b_dtype;
  *   each with its row stride.  dx may be dx_out's memory, dbranch branch's, and
- *   either dy's where the types agree, element for element.  x_out and the
+ *   one of them dy's where the types agree, element for element.  x_out and the
  *   statistics as the forward call wrote them, the other operands as it was
  *   given them.  branch may be NULL with FP4Q_NO_NORM where dgate is NULL.
  *   dpost_weight, dpost_bias, dweight, dbias: fp32 [cols]; dgate: fp32 [gate

@@ -8,9 +8,9 @@
 // atomics, the order of every sum is fixed by the sizes.  Four streams, their next
 // row and the sums take 140 to 165 registers, so a compute unit holds 12 waves.
 // These are one workgroup of teams of waves, a row to a team, so that they leave
-// one row of partial sums together: 8192 x 2048 bf16 44 us (39 + the join's 4.7,
-// 5.2 TB/s) against 55 with a workgroup to each team, whose partial sums were a
-// quarter of the data.  16384 x 5120 with an fp32 stream 305 + 7.7 us (5.0 TB/s),
+// one row of partial sums together: 8192 x 2048 bf16 44 to 49 us a call (36 to 39
+// and the join's 4.0 to 4.7; 5.2 TB/s) against 55 with a workgroup to each team,
+// whose partial sums were a quarter of the data.  16384 x 5120 with an fp32 stream 305 + 7.7 us (5.0 TB/s),
 // 1999 x 1111 fp32 with gates per sequence 16.3 + 4.8 (three rows to a team one
 // after another, and two launches).
 #include <algorithm>
