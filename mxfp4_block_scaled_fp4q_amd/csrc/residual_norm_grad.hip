@@ -10,9 +10,9 @@
 // These are one workgroup of teams of waves, a row to a team, so that they leave
 // one row of partial sums together: 8192 x 2048 bf16 44 to 49 us a call (36 to 39
 // and the join's 4.0 to 4.7; 5.2 TB/s) against 55 with a workgroup to each team,
-// whose partial sums were a quarter of the data.  16384 x 5120 with an fp32 stream 305 + 7.7 us (5.0 TB/s),
-// 1999 x 1111 fp32 with gates per sequence 16.3 + 4.8 (three rows to a team one
-// after another, and two launches).
+// whose partial sums were a quarter of the data.  16384 x 5120 with an fp32 stream
+// 305 + 7.7 us (5.0 TB/s), 1999 x 1111 fp32 with gates per sequence 16.3 + 4.8
+// (three rows to a team one after another, and two launches).
 #include <algorithm>
 #include <type_traits>
 
@@ -333,9 +333,8 @@ __device__ __forceinline__ float slab_sum(const float* p, int64_t stride, int fi
     for (int64_t i = first; i < count; i += step) s += p[i * stride];
     return s;
 }
-__global__ __launch_bounds__(kJoinThreads) void residual_grad_join_kernel(const ResidualNormGrad a,
-                                                                  const float* __restrict__ part,
-                                                                  const Slabs sl, int64_t group0) {
+__global__ __launch_bounds__(kJoinThreads) void residual_grad_join_kernel(
+    const ResidualNormGrad a, const float* __restrict__ part, const Slabs sl, int64_t group0) {
     __shared__ float red[2][16][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t at = (group0 + blockIdx.x) * 64 + lane, c = min(at, a.cols - 1);
